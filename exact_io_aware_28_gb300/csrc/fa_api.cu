@@ -413,6 +413,240 @@ fa_status fa_fwd_fp8(const void* q8, const void* k8, const void* vt8, const floa
                                   static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+bool bad4(const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// log2 of a supported page size, or -1.
+int page_shift(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+// The pool: its sizes, and pages at least `page_elems` elements apart.
+fa_status check_pool(int num_pages, int page_size, long long page_stride, long long page_elems) {
+  if (num_pages < 1) return FA_ERR_INVALID_ARG;
+  if (page_shift(page_size) < 0) return FA_ERR_UNSUPPORTED;
+  if ((long long)num_pages * page_size >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (page_stride < page_elems || page_stride % 8 != 0) return FA_ERR_INVALID_ARG;
+  if (page_stride > (1ll << 38)) return FA_ERR_UNSUPPORTED;   // the tensor map's limit
+  return FA_OK;
+}
+
+fa_status check_table(const int32_t* table, long long table_stride, int max_pages, int page_size) {
+  if (bad4(table) || max_pages < 1 || table_stride < max_pages) return FA_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+bool bad_row_stride(long long stride, long long row) { return stride < row || stride % 8 != 0; }
+
+// Do two int32 arrays share memory?
+bool overlap(const int32_t* a, long long na, const int32_t* b, long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4u * static_cast<uintptr_t>(nb) && y < x + 4u * static_cast<uintptr_t>(na);
+}
+
+bool bad_softmax_scale(float scale) { return !(isfinite(scale) && scale > 0.f); }
+
+}  // namespace
+
+fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
+                          const int32_t* free_pages, int n_free, int32_t* block_table,
+                          long long table_stride, int max_pages, int32_t* total_len,
+                          int32_t* token_start, int32_t* slots, int n_slots,
+                          int32_t* pages_taken, int B, int page_size, int num_pages,
+                          void* stream) {
+  if (B < 1 || n_free < 0 || n_slots < 0) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pool(num_pages, page_size, 8, 8);
+  if (st == FA_OK) st = check_table(block_table, table_stride, max_pages, page_size);
+  if (st != FA_OK) return st;
+  if (B > 8192 || (long long)B * max_pages * page_size >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (bad4(cache_len) || bad4(new_len) || bad4(total_len) || bad4(token_start) ||
+      bad4(pages_taken))
+    return FA_ERR_INVALID_ARG;
+  if ((n_free > 0 && bad4(free_pages)) || (n_slots > 0 && bad4(slots))) return FA_ERR_INVALID_ARG;
+  // Every block reads the inputs while others write the outputs.
+  const int32_t* ins[3] = {cache_len, new_len, free_pages};
+  const long long n_in[3] = {B, B, n_free};
+  const int32_t* outs[5] = {total_len, token_start, slots, pages_taken, block_table};
+  const long long n_out[5] = {B, B + 1ll, n_slots, 1, (B - 1) * table_stride + max_pages};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 5; ++j)
+      if (overlap(ins[i], n_in[i], outs[j], n_out[j])) return FA_ERR_INVALID_ARG;
+  return to_status(launch_paged_tables(cache_len, new_len, free_pages, n_free, block_table,
+                                       table_stride, max_pages, total_len, token_start, slots,
+                                       n_slots, pages_taken, B, page_shift(page_size), num_pages,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                          void* k_cache, void* v_cache, long long page_stride,
+                          const int32_t* slots, int T, int num_pages, int Hkv, int page_size,
+                          int d, void* stream) {
+  if (T < 0 || Hkv < 1) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  fa_status st = check_pool(num_pages, page_size, page_stride, (long long)Hkv * page_size * d);
+  if (st != FA_OK) return st;
+  if (T == 0) return FA_OK;
+  if (bad_ptr(k) || bad_ptr(v) || bad_ptr(k_cache) || bad_ptr(v_cache) || bad4(slots))
+    return FA_ERR_INVALID_ARG;
+  if (bad_row_stride(k_stride, (long long)Hkv * d) || bad_row_stride(v_stride, (long long)Hkv * d))
+    return FA_ERR_INVALID_ARG;
+  return to_status(launch_paged_append(k, v, k_stride, v_stride, k_cache, v_cache, page_stride,
+                                       slots, T, num_pages, Hkv, page_shift(page_size), d,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_latent_append(const void* c, const void* k_rope, long long c_stride,
+                           long long rope_stride, void* cache, long long page_stride,
+                           const int32_t* slots, int T, int num_pages, int page_size,
+                           void* stream) {
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pool(num_pages, page_size, page_stride,
+                            (long long)page_size * (FA_LATENT_RANK + FA_LATENT_ROPE));
+  if (st != FA_OK) return st;
+  if (T == 0) return FA_OK;
+  if (bad_ptr(c) || bad_ptr(k_rope) || bad_ptr(cache) || bad4(slots)) return FA_ERR_INVALID_ARG;
+  if (bad_row_stride(c_stride, FA_LATENT_RANK) || bad_row_stride(rope_stride, FA_LATENT_ROPE))
+    return FA_ERR_INVALID_ARG;
+  return to_status(launch_latent_append(c, k_rope, c_stride, rope_stride, cache, page_stride,
+                                        slots, T, num_pages, page_shift(page_size),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+fa_status check_decode_paged(int B, int Hq, int Hkv, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || Hq / Hkv > 16) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa_status check_latent_decode(int B, int H) {
+  if (B < 1 || H < 1) return FA_ERR_INVALID_ARG;
+  return H <= 128 && B <= 65535 ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
+  if (check_decode_paged(B, Hq, Hkv, d) != FA_OK) return 0;
+  return decode_paged_part_bytes(Hq / Hkv, d) + (static_cast<size_t>(B) + 1) * sizeof(long long);
+}
+
+fa_status fa_decode_paged(const void* q, const void* k, const void* v, long long page_stride,
+                          const int32_t* block_table, long long table_stride, int max_pages,
+                          const int32_t* cache_len, void* o, float* lse, int B, int Hq, int Hkv,
+                          int num_pages, int page_size, int d, float scale, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  fa_status st = check_decode_paged(B, Hq, Hkv, d);
+  if (st == FA_OK)
+    st = check_pool(num_pages, page_size, page_stride, (long long)Hkv * page_size * d);
+  if (st == FA_OK) st = check_table(block_table, table_stride, max_pages, page_size);
+  if (st != FA_OK) return st;
+  if (bad_ptr(q) || bad_ptr(k) || bad_ptr(v) || bad_ptr(o) || bad_ptr(workspace) || bad4(lse) ||
+      bad4(cache_len) || bad_softmax_scale(scale))
+    return FA_ERR_INVALID_ARG;
+  if (workspace_bytes < fa_decode_paged_workspace_bytes(B, Hq, Hkv, d)) return FA_ERR_INVALID_ARG;
+  int* err = error_word();
+  if (!err) return FA_ERR_CUDA;
+  return to_status(launch_decode_paged(q, k, v, page_stride, block_table, table_stride, max_pages,
+                                       page_shift(page_size), num_pages, cache_len, o, lse, B, Hq,
+                                       Hkv, d, scale, workspace, err, wait_limit_ns(),
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_latent_decode_workspace_bytes(int B, int H) {
+  return check_latent_decode(B, H) == FA_OK ? latent_decode_bytes(B, H) : 0;
+}
+
+fa_status fa_latent_decode(const void* q, const void* cache, long long page_stride,
+                           const int32_t* block_table, long long table_stride, int max_pages,
+                           const int32_t* cache_len, void* o, float* lse, int B, int H,
+                           int num_pages, int page_size, float scale, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  fa_status st = check_latent_decode(B, H);
+  if (st == FA_OK)
+    st = check_pool(num_pages, page_size, page_stride,
+                    (long long)page_size * (FA_LATENT_RANK + FA_LATENT_ROPE));
+  if (st == FA_OK) st = check_table(block_table, table_stride, max_pages, page_size);
+  if (st != FA_OK) return st;
+  if (bad_ptr(q) || bad_ptr(cache) || bad_ptr(o) || bad_ptr(workspace) || bad4(lse) ||
+      bad4(cache_len) || bad_softmax_scale(scale))
+    return FA_ERR_INVALID_ARG;
+  if (workspace_bytes < fa_latent_decode_workspace_bytes(B, H)) return FA_ERR_INVALID_ARG;
+  int* err = error_word();
+  if (!err) return FA_ERR_CUDA;
+  return to_status(launch_latent_decode(q, cache, page_stride, block_table, table_stride,
+                                        max_pages, page_shift(page_size), num_pages, cache_len, o,
+                                        lse, B, H, scale, workspace, err, wait_limit_ns(),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_latent_fwd(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                        void* o, float* o_acc, float* lse, int B, int H, int N, int causal,
+                        const int32_t* kv_len, float scale, fa_dtype dtype, void* stream) {
+  fa_status st = fa::check_shape(B, H, N, FA_LATENT_V);
+  if (st != FA_OK) return st;
+  if (bad_ptr(q) || bad_ptr(k_nope) || bad_ptr(k_rope) || bad_ptr(v) || bad_ptr(o) ||
+      !aligned16(o_acc))
+    return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
+  st = check_masks_scale(kv_len, lse, scale);
+  if (st != FA_OK) return st;
+  int* err = error_word();
+  if (!err) return FA_ERR_CUDA;
+  LatentProblem p{B, H, N, FA_LATENT_V, causal ? 1 : 0, nullptr, kv_len, scale, err,
+                  wait_limit_ns()};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return to_status(dtype == FA_BF16
+                       ? launch_latent_fwd_sm103(p, q, k_nope, k_rope, v, o, o_acc, lse, s)
+                       : launch_latent_fwd_simt(p, q, k_nope, k_rope, v, o, o_acc, lse, s));
+}
+
+size_t fa_latent_bwd_workspace_bytes(int B, int H, int N) {
+  if (check_shape(B, H, N, FA_LATENT_V) != FA_OK) return 0;
+  const size_t rows = (size_t)B * H * N;
+  return round_up(rows * sizeof(float), 256) + rows * FA_LATENT_ROPE * sizeof(float);
+}
+
+fa_status fa_latent_bwd(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                        const float* o_acc, const float* lse, const void* dO, void* dq,
+                        void* dk_nope, void* dk_rope, void* dv, int B, int H, int N, int causal,
+                        const int32_t* kv_len, float scale, fa_dtype dtype, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  fa_status st = fa::check_shape(B, H, N, FA_LATENT_V);
+  if (st != FA_OK) return st;
+  if (bad_ptr(q) || bad_ptr(k_nope) || bad_ptr(k_rope) || bad_ptr(v) || bad_ptr(o_acc) ||
+      bad_ptr(dO) || bad_ptr(dq) || bad_ptr(dk_nope) || bad_ptr(dk_rope) || bad_ptr(dv))
+    return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
+  st = check_masks_scale(kv_len, lse, scale);
+  if (st != FA_OK) return st;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < fa_latent_bwd_workspace_bytes(B, H, N))
+    return FA_ERR_INVALID_ARG;
+  int* err = error_word();
+  if (!err) return FA_ERR_CUDA;
+  LatentProblem p{B, H, N, FA_LATENT_V, causal ? 1 : 0, nullptr, kv_len, scale, err,
+                  wait_limit_ns()};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* Dsum = static_cast<float*>(workspace);
+  float* dkr_part = reinterpret_cast<float*>(
+      static_cast<char*>(workspace) + round_up((size_t)B * H * N * sizeof(float), 256));
+  cudaError_t e = launch_latent_rowdot(p, dtype, o_acc, dO, Dsum, s);
+  if (e == cudaSuccess)
+    e = dtype == FA_BF16 ? launch_latent_bwd_sm103(p, q, k_nope, k_rope, v, lse, dO, Dsum, dq,
+                                                   dk_nope, dkr_part, dv, s)
+                         : launch_latent_bwd_simt(p, q, k_nope, k_rope, v, lse, dO, Dsum, dq,
+                                                  dk_nope, dkr_part, dv, s);
+  if (e == cudaSuccess) e = launch_latent_rope_sum(p, dtype, dkr_part, dk_rope, s);
+  return to_status(e);
+}
+
 fa_status fa_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
   int* err = error_word();

@@ -540,6 +540,23 @@ bool make_head_map(CUtensorMap* map, const void* ptr, int BH, int N, int d) {
   return make_head_map_rows(map, ptr, BH, N, d, 128);
 }
 
+// A pool of pages [P, heads, page, d] bf16 whose pages lie `page_stride` elements apart, as a
+// 4-D tensor; 64-column boxes of `box_rows` rows of one head of one page, 128B swizzle.
+bool make_page_map(CUtensorMap* map, const void* ptr, int P, int heads, int page, int d,
+                   long long page_stride, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page),
+                        static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(P)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(page) * d * 2,
+                           static_cast<cuuint64_t>(page_stride) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [B*H, N, d] fp32 accumulator as a 3-D tensor with 32 x 32 boxes (128-byte rows, 128-byte
 // swizzle); rows beyond N are outside the map, so a box that overhangs the sequence end is
 // clipped.

@@ -117,6 +117,68 @@ cudaError_t launch_accumulate(float* acc, const void* x, long long n, fa_dtype d
                               cudaStream_t s);
 cudaError_t launch_finish(void* out, const float* acc, long long n, fa_dtype dt, cudaStream_t s);
 
+// Paged cache (fa_paged.cu): block tables and slot maps, rows into their slots.  page_shift is
+// log2 of the page size; strides count elements.
+cudaError_t launch_paged_tables(const int32_t* cache_len, const int32_t* new_len,
+                                const int32_t* free_pages, int n_free, int32_t* table,
+                                long long table_stride, int max_pages, int32_t* total_len,
+                                int32_t* token_start, int32_t* slots, int n_slots,
+                                int32_t* pages_taken, int B, int page_shift, int num_pages,
+                                cudaStream_t s);
+cudaError_t launch_paged_append(const void* k, const void* v, long long k_stride,
+                                long long v_stride, void* k_cache, void* v_cache,
+                                long long page_stride, const int32_t* slots, int T, int num_pages,
+                                int Hkv, int page_shift, int d, cudaStream_t s);
+cudaError_t launch_latent_append(const void* c, const void* k_rope, long long c_stride,
+                                 long long rope_stride, void* cache, long long page_stride,
+                                 const int32_t* slots, int T, int num_pages, int page_shift,
+                                 cudaStream_t s);
+
+// Decode over a paged cache (fa_decode_paged.cu) and absorbed latent decode
+// (fa_latent_decode.cu); the workspace holds partial results, then the sequences' tile sums.
+size_t decode_paged_part_bytes(int G, int d);
+cudaError_t launch_decode_paged(const void* q, const void* k, const void* v,
+                                long long page_stride, const int32_t* table,
+                                long long table_stride, int max_pages, int page_shift,
+                                int num_pages, const int32_t* cache_len, void* o, float* lse,
+                                int B, int Hq, int Hkv, int d, float scale, void* workspace,
+                                int* err, unsigned long long wait_ns, cudaStream_t s);
+size_t latent_decode_bytes(int B, int H);
+cudaError_t launch_latent_decode(const void* q, const void* cache, long long page_stride,
+                                 const int32_t* table, long long table_stride, int max_pages,
+                                 int page_shift, int num_pages, const int32_t* cache_len, void* o,
+                                 float* lse, int B, int H, float scale, void* workspace, int* err,
+                                 unsigned long long wait_ns, cudaStream_t s);
+
+// Expanded latent attention: fp32 tensors on the CUDA cores (fa_latent_simt.cu), bf16 on the
+// tensor cores (fa_latent_fwd.cu, fa_latent_bwd.cu).  Problem::d and the block mask are unused.
+using LatentProblem = Problem;
+cudaError_t launch_latent_fwd_simt(const LatentProblem& p, const void* q, const void* kn,
+                                   const void* kr, const void* v, void* o, float* o_acc,
+                                   float* lse, cudaStream_t s);
+cudaError_t launch_latent_fwd_sm103(const LatentProblem& p, const void* q, const void* kn,
+                                    const void* kr, const void* v, void* o, float* o_acc,
+                                    float* lse, cudaStream_t s);
+cudaError_t launch_latent_rowdot(const LatentProblem& p, fa_dtype dt, const float* o_acc,
+                                 const void* dO, float* Dsum, cudaStream_t s);
+cudaError_t launch_latent_bwd_simt(const LatentProblem& p, const void* q, const void* kn,
+                                   const void* kr, const void* v, const float* lse,
+                                   const void* dO, const float* Dsum, void* dq, void* dkn,
+                                   float* dkr_part, void* dv, cudaStream_t s);
+cudaError_t launch_latent_bwd_sm103(const LatentProblem& p, const void* q, const void* kn,
+                                    const void* kr, const void* v, const float* lse,
+                                    const void* dO, const float* Dsum, void* dq, void* dkn,
+                                    float* dkr_part, void* dv, cudaStream_t s);
+cudaError_t launch_latent_rope_sum(const LatentProblem& p, fa_dtype dt, const float* part,
+                                   void* dkr, cudaStream_t s);
+
+// Tensor map of a pool of pages [P, heads, page, d] bf16 with 64 x box_rows boxes.
+bool make_page_map(CUtensorMap* map, const void* ptr, int P, int heads, int page, int d,
+                   long long page_stride, int box_rows);
+
+// x rounded up to a multiple of a.
+size_t round_up(size_t x, size_t a);
+
 // Tensor map of a [B*H, N, d] fp32 accumulator with 32 x 32 boxes (128-byte swizzle), for bulk
 // reduce-add; rows beyond N are outside the map.
 bool make_acc_map(CUtensorMap* map, const void* ptr, int BH, int N, int d);

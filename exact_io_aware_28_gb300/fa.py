@@ -24,7 +24,15 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bwd_preprocess", "f
            "fa_selftest_wait_timeout", "fa_decode_workspace_bytes", "fa_decode",
            "fa_fp8_vt_bytes", "fa_fp8_quantize_qk", "fa_fp8_quantize_v", "fa_fwd_fp8",
            "fa_fwd_dropout", "fa_bwd_dropout", "fa_bwd_main_dropout", "fa_dropout_random_bytes",
-           "fa_attn_merge", "fa_grad_accumulate", "fa_grad_finish")
+           "fa_attn_merge", "fa_grad_accumulate", "fa_grad_finish",
+           "fa_paged_tables", "fa_paged_append", "fa_decode_paged_workspace_bytes",
+           "fa_decode_paged", "fa_latent_fwd", "fa_latent_bwd_workspace_bytes", "fa_latent_bwd",
+           "fa_latent_append", "fa_latent_decode_workspace_bytes", "fa_latent_decode")
+
+# Columns of latent attention: the latent vector, the keys' rotated part, a head's own key part
+# and its values.
+LATENT_RANK, LATENT_ROPE, LATENT_NOPE, LATENT_V = 512, 64, 128, 128
+LATENT_ROW, LATENT_QK = LATENT_RANK + LATENT_ROPE, LATENT_NOPE + LATENT_ROPE
 
 # Largest number of partial results fa_attn_merge accepts.
 FA_MERGE_MAX_PARTS = 1024
@@ -102,6 +110,26 @@ def load() -> ctypes.CDLL:
     lib.fa_grad_accumulate.restype = I
     lib.fa_grad_finish.argtypes = [P, P, L, I, P]
     lib.fa_grad_finish.restype = I
+    lib.fa_paged_tables.argtypes = [P, P, P, I, P, L, I, P, P, P, I, P, I, I, I, P]
+    lib.fa_paged_tables.restype = I
+    lib.fa_paged_append.argtypes = [P, P, L, L, P, P, L, P, I, I, I, I, I, P]
+    lib.fa_paged_append.restype = I
+    lib.fa_decode_paged_workspace_bytes.argtypes = [I, I, I, I]
+    lib.fa_decode_paged_workspace_bytes.restype = S
+    lib.fa_decode_paged.argtypes = [P, P, P, L, P, L, I, P, P, P, I, I, I, I, I, I, F, P, S, P]
+    lib.fa_decode_paged.restype = I
+    lib.fa_latent_fwd.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, F, I, P]
+    lib.fa_latent_fwd.restype = I
+    lib.fa_latent_bwd_workspace_bytes.argtypes = [I, I, I]
+    lib.fa_latent_bwd_workspace_bytes.restype = S
+    lib.fa_latent_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, P, F, I, P, S, P]
+    lib.fa_latent_bwd.restype = I
+    lib.fa_latent_append.argtypes = [P, P, L, L, P, L, P, I, I, I, P]
+    lib.fa_latent_append.restype = I
+    lib.fa_latent_decode_workspace_bytes.argtypes = [I, I]
+    lib.fa_latent_decode_workspace_bytes.restype = S
+    lib.fa_latent_decode.argtypes = [P, P, L, P, L, I, P, P, P, I, I, I, I, F, P, S, P]
+    lib.fa_latent_decode.restype = I
     _lib = lib
     return lib
 
@@ -516,3 +544,354 @@ def fa_grad_finish(out, acc, stream=None) -> None:
                                _stream(stream))
     if st != FA_OK:
         raise FaError(st, "fa_grad_finish")
+
+
+# ----------------------------------------------------------- paged cache
+
+def _same_gpu(*ts):
+    """Every tensor lies on the current CUDA device, where the library launches."""
+    here = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("the library takes CUDA tensors (device memory); got a "
+                             f"{t.device.type} tensor")
+        if here is None:
+            here = torch.cuda.current_device()
+        if t.device.index != here:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}: "
+                             "enter torch.cuda.device(...) for it")
+
+
+def _shaped(name, t, shape, dtype):
+    """``t`` is dense and has the shape (None: any size) and type named."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be {list(shape)} (None: any size), not {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(name, t, shape, dtype=torch.bfloat16):
+    """Elements between the first index's entries of ``t``, whose other dimensions are dense (a
+    slice of a larger tensor along them is taken as it is)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be {list(shape)} (None: any size), not {list(t.shape)}")
+    dense = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != dense:
+            raise ValueError(f"{name} must be dense behind its first dimension")
+        dense *= n
+    return t.stride(0) if t.shape[0] > 1 else dense   # a single entry's stride says nothing
+
+
+def _table(block_table, B):
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be torch.int32")
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1:
+        raise ValueError(f"block_table must be [{B}, max_pages], not {list(block_table.shape)}")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table rows must be dense")
+    return block_table.stride(0) if B > 1 else block_table.shape[1]
+
+
+class _Helper:
+    """Where an allocating helper runs: its outputs and scratch memory belong to the stream the
+    kernels run on, and inputs made on another stream are kept until that work is done."""
+
+    def __init__(self, stream, *inputs):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        self.ctx = torch.cuda.stream(stream)
+        if stream is not None and stream != torch.cuda.current_stream():
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+def fa_paged_tables(cache_len, new_len, free_pages, block_table, total_len, token_start, slots,
+                    pages_taken, page_size: int, num_pages: int, stream=None) -> None:
+    """Block tables and slot maps from the requests' lengths (int32 tensors throughout).
+
+    cache_len, new_len [B], free_pages [F] in; block_table [B, max_pages] in and out; out:
+    total_len [B], token_start [B + 1], slots [T], pages_taken [1].
+    """
+    B = cache_len.shape[0] if cache_len.dim() else 0
+    i32 = torch.int32
+    for name, t, n in (("cache_len", cache_len, B), ("new_len", new_len, B),
+                       ("free_pages", free_pages, None), ("total_len", total_len, B),
+                       ("token_start", token_start, B + 1), ("slots", slots, None),
+                       ("pages_taken", pages_taken, 1)):
+        _shaped(name, t, (n,), i32)
+    stride = _table(block_table, B)
+    _same_gpu(cache_len, new_len, free_pages, block_table, total_len, token_start, slots,
+              pages_taken)
+    st = load().fa_paged_tables(cache_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
+                                free_pages.numel(), block_table.data_ptr(), stride,
+                                block_table.shape[1], total_len.data_ptr(),
+                                token_start.data_ptr(), slots.data_ptr(), slots.numel(),
+                                pages_taken.data_ptr(), B, int(page_size), int(num_pages),
+                                _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_tables")
+
+
+def paged_tables(cache_len, new_len, free_pages, block_table, page_size: int, num_pages: int,
+                 num_slots: int, stream=None):
+    """Allocate the outputs and run fa_paged_tables; block_table is updated in place.
+
+    Returns (total_len, token_start, slots, pages_taken); ``num_slots`` rows of slots, those
+    behind the last new token -1.
+    """
+    B = cache_len.shape[0]
+    with _Helper(stream, cache_len, new_len, free_pages, block_table):
+        n = int(num_slots)
+        buf = torch.empty(2 * B + 2 + n, dtype=torch.int32, device=cache_len.device)
+        total, start = buf[:B], buf[B:2 * B + 1]
+        taken, slots = buf[2 * B + 1:2 * B + 2], buf[2 * B + 2:]
+        fa_paged_tables(cache_len, new_len, free_pages, block_table, total, start, slots, taken,
+                        page_size, num_pages)
+    return total, start, slots, taken
+
+
+def fa_paged_append(k, v, k_cache, v_cache, slots, stream=None) -> None:
+    """Rows k, v [T, Hkv, d] (bf16, any stride between tokens) into slots [T] (int32) of the pools
+    k_cache, v_cache [num_pages, Hkv, page_size, d] (equal strides)."""
+    T, Hkv, d = k.shape
+    P, page = k_cache.shape[0], k_cache.shape[2] if k_cache.dim() == 4 else 0
+    ks, vs = _rows("k", k, (T, Hkv, d)), _rows("v", v, (T, Hkv, d))
+    kp, vp = (_rows(n, c, (P, Hkv, page, d)) for n, c in (("k_cache", k_cache),
+                                                          ("v_cache", v_cache)))
+    if kp != vp:
+        raise ValueError("k_cache and v_cache must have the same stride between pages")
+    _shaped("slots", slots, (T,), torch.int32)
+    _same_gpu(k, v, k_cache, v_cache, slots)
+    st = load().fa_paged_append(k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(),
+                                v_cache.data_ptr(), kp, slots.data_ptr(), T, P, Hkv, page, d,
+                                _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_append")
+
+
+paged_append = fa_paged_append   # it allocates nothing
+
+
+def fa_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load().fa_decode_paged_workspace_bytes(B, Hq, Hkv, d))
+
+
+def alloc_decode_paged_workspace(B: int, Hq: int, Hkv: int, d: int, device="cuda"):
+    n = fa_decode_paged_workspace_bytes(B, Hq, Hkv, d)
+    if n == 0:
+        raise FaError(FA_ERR_INVALID_ARG, "fa_decode_paged_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fa_decode_paged(q, k, v, block_table, cache_len, o, lse, workspace, scale=None,
+                    stream=None) -> None:
+    """q [B, Hq, d] over the pools k, v [num_pages, Hkv, page_size, d] (bf16) through block_table
+    [B, max_pages] and cache_len [B] (int32); o [B, Hq, d] bf16 and lse [B, Hq] fp32 out."""
+    bf16 = torch.bfloat16
+    _shaped("q", q, (None, None, None), bf16)
+    B, Hq, d = q.shape
+    kp, vp = (_rows(n, c, (None, None, None, d)) for n, c in (("k", k), ("v", v)))
+    if kp != vp or k.shape != v.shape:
+        raise ValueError("k and v must have the same shape and stride between pages")
+    P, Hkv, page, _ = k.shape
+    stride = _table(block_table, B)
+    _shaped("cache_len", cache_len, (B,), torch.int32)
+    _shaped("o", o, (B, Hq, d), bf16)
+    _shaped("lse", lse, (B, Hq), torch.float32)
+    _same_gpu(q, k, v, block_table, cache_len, o, lse, workspace)
+    scale = 1.0 / d ** 0.5 if scale is None else float(scale)
+    st = load().fa_decode_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), kp,
+                                block_table.data_ptr(), stride, block_table.shape[1],
+                                cache_len.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, P,
+                                page, d, scale, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_decode_paged")
+
+
+def decode_paged(q, k, v, block_table, cache_len, scale=None, workspace=None, stream=None):
+    """Allocate o, lse (and the workspace unless given) and run fa_decode_paged."""
+    B, Hq, d = q.shape
+    with _Helper(stream, q, k, v, block_table, cache_len, workspace):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = alloc_decode_paged_workspace(B, Hq, k.shape[1], d, q.device)
+        fa_decode_paged(q, k, v, block_table, cache_len, o, lse, workspace, scale)
+    return o, lse
+
+
+# ----------------------------------------------------------- latent attention
+
+def _latent_shapes(q, k_nope, k_rope, v, kv_len):
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, H, N, {LATENT_QK}], not {list(q.shape)}")
+    B, H, N, _ = q.shape
+    dt = q.dtype
+    _shaped("q", q, (B, H, N, LATENT_QK), dt)
+    _shaped("k_nope", k_nope, (B, H, N, LATENT_NOPE), dt)
+    _shaped("k_rope", k_rope, (B, N, LATENT_ROPE), dt)
+    _shaped("v", v, (B, H, N, LATENT_V), dt)
+    if kv_len is not None:
+        _shaped("kv_len", kv_len, (B,), torch.int32)
+    return B, H, N, _dtype_code(q)
+
+
+def fa_latent_fwd(q, k_nope, k_rope, v, o, o_acc, lse, causal: bool = False, kv_len=None,
+                  scale: Optional[float] = None, stream=None) -> None:
+    """Expanded latent attention: q [B, H, N, 192], k_nope [B, H, N, 128], k_rope [B, N, 64] shared
+    by the heads, v [B, H, N, 128]; out o (as v), o_acc (fp32 O for the backward, or None) and
+    lse fp32 [B, H, N]."""
+    B, H, N, code = _latent_shapes(q, k_nope, k_rope, v, kv_len)
+    _shaped("o", o, (B, H, N, LATENT_V), q.dtype)
+    if o_acc is not None:
+        _shaped("o_acc", o_acc, (B, H, N, LATENT_V), torch.float32)
+    _shaped("lse", lse, (B, H, N), torch.float32)
+    _same_gpu(q, k_nope, k_rope, v, o, o_acc, lse, kv_len)
+    scale = 1.0 / LATENT_QK ** 0.5 if scale is None else float(scale)
+    st = load().fa_latent_fwd(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(o_acc),
+                              _ptr(lse), B, H, N, int(causal), _ptr(kv_len), scale, code,
+                              _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_latent_fwd")
+
+
+def latent_forward(q, k_nope, k_rope, v, causal: bool = False, kv_len=None, scale=None,
+                   need_grad: bool = False, stream=None):
+    """Allocate and run fa_latent_fwd.  Returns (o, lse), with ``need_grad`` (o, lse, o_acc)."""
+    B, H, N, _ = q.shape
+    with _Helper(stream, q, k_nope, k_rope, v, kv_len):
+        o = torch.empty_like(v)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        o_acc = None
+        if need_grad and q.dtype != torch.float32:
+            o_acc = torch.empty(v.shape, dtype=torch.float32, device=q.device)
+        fa_latent_fwd(q, k_nope, k_rope, v, o, o_acc, lse, causal, kv_len, scale)
+    if not need_grad:
+        return o, lse
+    return o, lse, o if o_acc is None else o_acc   # fp32: o is its own unrounded form
+
+
+def fa_latent_bwd_workspace_bytes(B: int, H: int, N: int) -> int:
+    return int(load().fa_latent_bwd_workspace_bytes(B, H, N))
+
+
+def alloc_latent_workspace(B: int, H: int, N: int, device="cuda") -> torch.Tensor:
+    n = fa_latent_bwd_workspace_bytes(B, H, N)
+    if n == 0:
+        raise FaError(FA_ERR_INVALID_ARG, "fa_latent_bwd_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fa_latent_bwd(q, k_nope, k_rope, v, o_acc, lse, do, dq, dk_nope, dk_rope, dv, workspace,
+                  causal: bool = False, kv_len=None, scale: Optional[float] = None,
+                  stream=None) -> None:
+    """Gradients of fa_latent_fwd (preallocated) for the upstream gradient ``do``; o_acc and lse
+    as the forward wrote them."""
+    B, H, N, code = _latent_shapes(q, k_nope, k_rope, v, kv_len)
+    _shaped("o_acc", o_acc, (B, H, N, LATENT_V), torch.float32)
+    _shaped("lse", lse, (B, H, N), torch.float32)
+    for name, t, like in (("do", do, v), ("dq", dq, q), ("dk_nope", dk_nope, k_nope),
+                          ("dk_rope", dk_rope, k_rope), ("dv", dv, v)):
+        _shaped(name, t, tuple(like.shape), q.dtype)
+    _same_gpu(q, k_nope, k_rope, v, o_acc, lse, do, dq, dk_nope, dk_rope, dv, workspace, kv_len)
+    scale = 1.0 / LATENT_QK ** 0.5 if scale is None else float(scale)
+    st = load().fa_latent_bwd(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o_acc), _ptr(lse),
+                              _ptr(do), _ptr(dq), _ptr(dk_nope), _ptr(dk_rope), _ptr(dv), B, H, N,
+                              int(causal), _ptr(kv_len), scale, code, _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_latent_bwd")
+
+
+def latent_backward(q, k_nope, k_rope, v, o_acc, lse, do, causal: bool = False, kv_len=None,
+                    scale=None, workspace=None, stream=None):
+    """Allocate the gradients (and the workspace unless given) and run fa_latent_bwd.
+    Returns (dq, dk_nope, dk_rope, dv)."""
+    B, H, N, _ = q.shape
+    with _Helper(stream, q, k_nope, k_rope, v, o_acc, lse, do, kv_len, workspace):
+        dq, dkn, dkr, dv = (torch.empty_like(t) for t in (q, k_nope, k_rope, v))
+        if workspace is None:
+            workspace = alloc_latent_workspace(B, H, N, q.device)
+        fa_latent_bwd(q, k_nope, k_rope, v, o_acc, lse, do, dq, dkn, dkr, dv, workspace, causal,
+                      kv_len, scale)
+    return dq, dkn, dkr, dv
+
+
+def fa_latent_append(c, k_rope, cache, slots, stream=None) -> None:
+    """Latent rows c [T, 512] and k_rope [T, 64] (bf16, any stride between tokens) into slots [T]
+    (int32) of the pool cache [num_pages, page_size, 576]."""
+    T = c.shape[0]
+    cs, rs = _rows("c", c, (T, LATENT_RANK)), _rows("k_rope", k_rope, (T, LATENT_ROPE))
+    ps = _rows("cache", cache, (None, None, LATENT_ROW))
+    _shaped("slots", slots, (T,), torch.int32)
+    _same_gpu(c, k_rope, cache, slots)
+    st = load().fa_latent_append(c.data_ptr(), k_rope.data_ptr(), cs, rs, cache.data_ptr(), ps,
+                                 slots.data_ptr(), T, cache.shape[0], cache.shape[1],
+                                 _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_latent_append")
+
+
+latent_append = fa_latent_append   # it allocates nothing
+
+
+def fa_latent_decode_workspace_bytes(B: int, H: int) -> int:
+    return int(load().fa_latent_decode_workspace_bytes(B, H))
+
+
+def alloc_latent_decode_workspace(B: int, H: int, device="cuda") -> torch.Tensor:
+    n = fa_latent_decode_workspace_bytes(B, H)
+    if n == 0:
+        raise FaError(FA_ERR_INVALID_ARG, "fa_latent_decode_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fa_latent_decode(q, cache, block_table, cache_len, o, lse, workspace, scale=None,
+                     stream=None) -> None:
+    """Absorbed latent decode: q [B, H, 576] over the pool cache [num_pages, page_size, 576]
+    (bf16) through block_table [B, max_pages] and cache_len [B] (int32); o [B, H, 512] bf16 and
+    lse [B, H] fp32 out."""
+    bf16 = torch.bfloat16
+    _shaped("q", q, (None, None, LATENT_ROW), bf16)
+    B, H, _ = q.shape
+    ps = _rows("cache", cache, (None, None, LATENT_ROW))
+    stride = _table(block_table, B)
+    _shaped("cache_len", cache_len, (B,), torch.int32)
+    _shaped("o", o, (B, H, LATENT_RANK), bf16)
+    _shaped("lse", lse, (B, H), torch.float32)
+    _same_gpu(q, cache, block_table, cache_len, o, lse, workspace)
+    scale = 1.0 / LATENT_QK ** 0.5 if scale is None else float(scale)
+    st = load().fa_latent_decode(q.data_ptr(), cache.data_ptr(), ps, block_table.data_ptr(), stride,
+                                 block_table.shape[1], cache_len.data_ptr(), o.data_ptr(),
+                                 lse.data_ptr(), B, H, cache.shape[0], cache.shape[1], scale,
+                                 workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != FA_OK:
+        raise FaError(st, "fa_latent_decode")
+
+
+def latent_decode(q, cache, block_table, cache_len, scale=None, workspace=None, stream=None):
+    """Allocate o, lse (and the workspace unless given) and run fa_latent_decode."""
+    B, H, _ = q.shape
+    with _Helper(stream, q, cache, block_table, cache_len, workspace):
+        o = torch.empty((B, H, LATENT_RANK), dtype=q.dtype, device=q.device)
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = alloc_latent_decode_workspace(B, H, q.device)
+        fa_latent_decode(q, cache, block_table, cache_len, o, lse, workspace, scale)
+    return o, lse

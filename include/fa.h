@@ -319,6 +319,150 @@ fa_status fa_grad_accumulate(float* acc, const void* x, long long n, fa_dtype dt
  */
 fa_status fa_grad_finish(void* out, const float* acc, long long n, fa_dtype dtype, void* stream);
 
+/*
+ * A paged key/value cache: the pool holds num_pages pages of page_size tokens, and a block table
+ * says which pages a sequence's tokens are in.
+ *   page_size     16, 32, 64, 128 or 256 (FA_ERR_UNSUPPORTED otherwise).
+ *   block_table   device int32 [B, max_pages], rows table_stride elements apart (>= max_pages):
+ *                 token x of sequence b is row x % page_size of page block_table[b][x / page_size].
+ *                 An entry outside [0, num_pages) is a hole: nothing is read or written there, and
+ *                 the keys it stands for are hidden from the queries.
+ *   slot          page * page_size + row of one token; num_pages * page_size must be below 2^31.
+ *   page_stride   elements between pages, a multiple of 8 and at least a page's own size, so that
+ *                 pages may be parts of larger blocks (keys and values side by side, say).
+ * Lengths are clamped to [0, max_pages * page_size] on the device.  The pages of different
+ * sequences may be the same (a shared prefix) for reading.
+ */
+
+/*
+ * Block tables and slot maps from the requests' lengths (the pages a step needs, on the GPU).
+ *   cache_len   in : int32 [B], tokens each request has in the cache.
+ *   new_len     in : int32 [B], tokens the step adds; clamped to what the table row can hold.
+ *   free_pages  in : int32 [n_free], page numbers to take, from the front (NULL if n_free = 0).
+ *   block_table in/out: entries of pages a request has (ceil(cache_len / page_size) of them) are
+ *                 kept, the ones its new tokens need are written, -1 when the list has run out;
+ *                 the entries behind them stay as they are.
+ *   total_len   out: int32 [B], cache_len + new_len after the clamps.
+ *   token_start out: int32 [B + 1], exclusive sums of the new tokens: request b's are the packed
+ *                 rows token_start[b] .. token_start[b + 1] - 1.
+ *   slots       out: int32 [n_slots], the slot of every packed new token; -1 for a token in a hole
+ *                 and for the rows behind the last token.  May be shorter than the tokens are.
+ *   pages_taken out: int32 [1], pages the step needs; more than n_free: the list was too short.
+ * Requests take pages in order.  FA_ERR_INVALID_ARG if cache_len, new_len or free_pages shares
+ * memory with an output.
+ * FA_ERR_UNSUPPORTED for B > 8192 or B * max_pages * page_size >= 2^31.
+ */
+fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
+                          const int32_t* free_pages, int n_free, int32_t* block_table,
+                          long long table_stride, int max_pages, int32_t* total_len,
+                          int32_t* token_start, int32_t* slots, int n_slots,
+                          int32_t* pages_taken, int B, int page_size, int num_pages,
+                          void* stream);
+
+/*
+ * Rows of new tokens into their slots.
+ *   k, v     in : bf16, token t's rows [Hkv, d] at k + t * k_stride, v + t * v_stride (elements,
+ *                 multiples of 8, >= Hkv * d: a slice of a fused projection is taken as it is).
+ *   k_cache, v_cache out: bf16 pools [num_pages, Hkv, page_size, d], pages page_stride apart.
+ *   slots    in : int32 [T]; a slot outside the pool: the token is skipped.  Slots should differ:
+ *                 rows that share one are written in no particular order, piece by piece.
+ * d = 64 or 128; T = 0 does nothing.
+ */
+fa_status fa_paged_append(const void* k, const void* v, long long k_stride, long long v_stride,
+                          void* k_cache, void* v_cache, long long page_stride,
+                          const int32_t* slots, int T, int num_pages, int Hkv, int page_size,
+                          int d, void* stream);
+
+/*
+ * Decode attention over a paged cache: fa_decode with the keys and values found through the block
+ * table.
+ *   q       in : bf16 [B, Hq, d];  k, v in: bf16 pools [num_pages, Hkv, page_size, d].
+ *   cache_len in: int32 [B].
+ *   o       out: bf16 [B, Hq, d], 0 for a sequence with no visible key; lse out: fp32 [B, Hq]
+ *                 (-inf there).
+ *   workspace   : at least fa_decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes, 16-byte aligned,
+ *                 contents on entry do not matter; calls that may run at the same time (two
+ *                 streams, two captured graphs) need one each.
+ * d = 64 or 128, Hq / Hkv = 1 .. 16 (FA_ERR_UNSUPPORTED otherwise).  Keys past the length and in
+ * holes are never computed with, whatever those rows hold.  Two kernels run on `stream`.
+ */
+size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
+fa_status fa_decode_paged(const void* q, const void* k, const void* v, long long page_stride,
+                          const int32_t* block_table, long long table_stride, int max_pages,
+                          const int32_t* cache_len, void* o, float* lse, int B, int Hq, int Hkv,
+                          int num_pages, int page_size, int d, float scale, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Latent attention: keys and values of all heads come from one latent vector a token (512 columns,
+ * c), and the keys' rotated part (64 columns, r) is one vector a token for all heads.
+ *   expanded form -- head h has keys (k_nope_h, k_rope) of 128 + 64 columns, k_nope_h = c W_uk,h and
+ *     k_rope = r shared by the heads, and values v_h = c W_uv,h of 128: training and prompts.
+ *   absorbed form -- with q_h = (q_nope_h W_uk,h^T, q_rope_h) of 512 + 64 columns the scores are
+ *     q_h . (c, r) and o_h = P_h c, whose product with W_uv,h is the head's output: single tokens,
+ *     the cache holding 576 values a token.
+ * The projections are the caller's matrix products.  `scale` is that of the expanded keys in both
+ * forms, normally 1/sqrt(192).
+ */
+#define FA_LATENT_RANK 512
+#define FA_LATENT_ROPE 64
+#define FA_LATENT_NOPE 128
+#define FA_LATENT_V 128
+
+/*
+ * Expanded form, forward.
+ *   q in: [B, H, N, 192];  k_nope in: [B, H, N, 128];  k_rope in: [B, N, 64];  v in: [B, H, N, 128];
+ *   o out: [B, H, N, 128];  all of `dtype`, dense, 16-byte aligned.
+ *   o_acc   out: NULL, or fp32 [B, H, N, 128]: O before its rounding to `dtype`, which
+ *                fa_latent_bwd takes.  With fp32 tensors it may be o itself.
+ *   lse     out: fp32 [B, H, N].
+ *   causal, kv_len, scale: as fa_fwd.  Rows of k_nope, k_rope and v past kv_len[b] may hold
+ *                anything.
+ */
+fa_status fa_latent_fwd(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                        void* o, float* o_acc, float* lse, int B, int H, int N, int causal,
+                        const int32_t* kv_len, float scale, fa_dtype dtype, void* stream);
+
+/*
+ * Expanded form, backward, for dO = dL/dO: dq, dk_nope, dv of the heads and dk_rope, the sum of
+ * the heads' gradients of the shared part.  o_acc and lse as fa_latent_fwd wrote them (same masks,
+ * same scale).  workspace: at least fa_latent_bwd_workspace_bytes(B, H, N) bytes, 256-byte
+ * aligned: the fp32 row sums of dO o O, then the heads' fp32 shares of dk_rope.  Gradients of keys
+ * past kv_len[b] are 0.  No atomics: the same call gives the same bits.
+ */
+size_t fa_latent_bwd_workspace_bytes(int B, int H, int N);
+fa_status fa_latent_bwd(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                        const float* o_acc, const float* lse, const void* dO, void* dq,
+                        void* dk_nope, void* dk_rope, void* dv, int B, int H, int N, int causal,
+                        const int32_t* kv_len, float scale, fa_dtype dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Rows of new tokens into a paged latent cache, bf16 [num_pages, page_size, 576]: c [T, 512] into
+ * columns 0 .. 511 and k_rope [T, 64] into 512 .. 575, rows c_stride and rope_stride elements
+ * apart.  slots, T, page_stride: as fa_paged_append.
+ */
+fa_status fa_latent_append(const void* c, const void* k_rope, long long c_stride,
+                           long long rope_stride, void* cache, long long page_stride,
+                           const int32_t* slots, int T, int num_pages, int page_size,
+                           void* stream);
+
+/*
+ * Absorbed form over a paged latent cache: one new token per sequence.
+ *   q     in : bf16 [B, H, 576], the absorbed queries (512) and their rotated part (64).
+ *   cache in : bf16 [num_pages, page_size, 576], pages page_stride elements apart.
+ *   o     out: bf16 [B, H, 512] = softmax(scale q (c, r)^T) c over the visible tokens, 0 where none
+ *              is; lse out: fp32 [B, H] (-inf there).
+ *   workspace: as fa_decode_paged, of fa_latent_decode_workspace_bytes(B, H) bytes.
+ * H = 1 .. 128 (FA_ERR_UNSUPPORTED otherwise).
+ */
+size_t fa_latent_decode_workspace_bytes(int B, int H);
+fa_status fa_latent_decode(const void* q, const void* cache, long long page_stride,
+                           const int32_t* block_table, long long table_stride, int max_pages,
+                           const int32_t* cache_len, void* o, float* lse, int B, int H,
+                           int num_pages, int page_size, float scale, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* fa_status_string(fa_status s);
 
