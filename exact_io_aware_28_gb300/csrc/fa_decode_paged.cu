@@ -18,11 +18,19 @@
 // outside the pool is not loaded, and its rows, like those past the length, are hidden: their
 // scores are replaced, never computed with, and their V rows are zeroed in shared memory.
 //
+// A tile's way (scores, maximum, P, P V) is a chain of about 2.5k cycles, at d = 64 twice what HBM
+// takes for its 32 KB, and an issuing thread spends some 1.8k cycles on a tile's twelve MMAs,
+// commits and waits (traced).  So two groups of four softmax warps take the tiles in turn, each
+// with its own maximum, sum and O^T, joined at the end like parts of different CTAs; and one
+// thread issues the scores of every tile that has landed, another the P V products.  Score and P
+// buffers go with the stages: a tile's stage is filled only after the P V of the tile before in
+// it, so they are free by then.
+//
 // Work: fa_paged_sched.cuh cuts the line of all tiles into one range per CTA, one CTA per SM.
 // A pair inside one range is finished there; only pairs that a range's end cuts go through the
 // workspace and the combine kernel, at most two partial results a CTA.
-//   warp 0     producer (a lane per page);      warp 1  MMA issuer (one thread);
-//   warp 2     tensor memory (S^T x 2, O^T x 2); warps 4-7 softmax, thread = key row.
+//   warp 0     producer (a lane per page);      warps 1, 3  MMA issuers (one thread each);
+//   warp 2     tensor memory;                   warps 4-11  softmax, thread = key row.
 // Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and leaves.
 #include <atomic>
 
@@ -42,25 +50,25 @@ using sched::Segment;
 
 constexpr int kKeys = 128;                    // keys per tile
 constexpr int kN = 16;                        // query heads padded to the MMA's N
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 6;
 constexpr int kSub = kKeys * 128;             // [128 rows][64 bf16] swizzled subtile, 16 KB
 constexpr int kPBytes = 2 * kN * 128;         // [16][128 keys] bf16
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr uint32_t kO = kMaxStages * kN;      // first column of O^T: 2 segments x 2 groups
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units; exact, see fa_fwd_sm103.cu
 
 struct Bars {
   uint64_t full[kMaxStages];
-  uint64_t empty[kMaxStages];
+  uint64_t empty[kMaxStages];  // P V of the stage's tile has completed
   uint64_t q_full[2];
   uint64_t q_empty[2];
-  uint64_t s_full[2];
-  uint64_t p_full[2];
-  uint64_t p_free[2];
+  uint64_t s_full[kMaxStages];
+  uint64_t p_full[kMaxStages];
   uint64_t o_full[2];
-  uint64_t xmax[2];
-  uint64_t xsum[2];
+  uint64_t xmax[2];    // of each softmax group
+  uint64_t xsum[2];    // of both, for a segment
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t seen[kMaxStages];  // bit i: rows 16 i ... 16 i + 15 of the stage are in the pool
@@ -71,13 +79,12 @@ struct Bars {
 template <int D>
 struct TC {
   static constexpr int NSUB = D / 64;                  // 64-column subtiles of a K or V tile
-  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int STAGES = D == 128 ? 3 : 6;
   static constexpr int STAGE = 2 * NSUB * kSub;        // K tile then V tile
-  static constexpr int PAD = D == 128 ? 0 : kSub;      // zero rows d = 64..127 of V^T
   static constexpr int QBYTES = NSUB * kN * 128;       // [16][d] bf16
   static constexpr int PSTRIDE = D + 4;                // floats per (slot, head) partial row
-  static constexpr int SMEM = 1024 + STAGES * STAGE + PAD + 2 * QBYTES + 2 * kPBytes +
-                              2 * 4 * kN * 4 * 2 + static_cast<int>(sizeof(Bars));
+  static constexpr int SMEM = 1024 + STAGES * STAGE + 2 * QBYTES + STAGES * kPBytes +
+                              (2 * 2 + 2 * 2 * 2) * 4 * kN * 4 + static_cast<int>(sizeof(Bars));
   static_assert(STAGES <= kMaxStages && SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -115,12 +122,14 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sKV = base;                                   // [kStages][K subtiles, V subtiles]
-  uint8_t* sPad = sKV + kStages * kStage;                // d = 64: [128 keys][64] zeros
-  uint8_t* sQ = sPad + C::PAD;                           // [2][kQBytes]
-  uint8_t* sP = sQ + 2 * kQBytes;                        // [2][kPBytes]
-  float* red_m = reinterpret_cast<float*>(sP + 2 * kPBytes);   // [2][4 warps][16 heads]
-  float* red_l = red_m + 2 * 4 * kN;                           // [2][4 warps][16 heads]
-  Bars* bars = reinterpret_cast<Bars*>(red_l + 2 * 4 * kN);
+  uint8_t* sQ = sKV + kStages * kStage;                  // [2][kQBytes]
+  uint8_t* sP = sQ + 2 * kQBytes;                        // [kStages][kPBytes]
+  // A group's exchange of maxima: [2 groups][2][4 warps][16 heads]; a segment's statistics:
+  // [2 segments][2 groups][4 warps: sums][16 heads], then the same of maxima (one row used).
+  float* red_m = reinterpret_cast<float*>(sP + kStages * kPBytes);
+  float* red_l = red_m + 2 * 2 * 4 * kN;
+  float* seg_m = red_l + 2 * 2 * 4 * kN;
+  Bars* bars = reinterpret_cast<Bars*>(seg_m + 2 * 2 * 4 * kN);
   __shared__ sched::Start start;
   __shared__ long long scan[kThreads / 32 + 1];
   volatile int* abort_flag = &bars->abort;
@@ -131,29 +140,23 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], 128);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
-      mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 128);
-      mbar_init(&bars->p_free[i], 1);
       mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->xmax[i], 128);
-      mbar_init(&bars->xsum[i], 128);
+      mbar_init(&bars->xsum[i], 256);
     }
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, 2);
     bars->abort = 0;
     bars->never = 0;
     fence_mbar_init();
   }
-  if constexpr (C::PAD > 0) {
-    for (int i = tid; i < C::PAD / 16; i += kThreads)
-      reinterpret_cast<uint4*>(sPad)[i] = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();   // read by the tensor cores
-  }
   if (warp == 2) {
-    tmem_alloc(&bars->tmem_base, 64);
+    tmem_alloc(&bars->tmem_base, 256);
     tmem_relinquish();
   }
   if (tid == 0) {
@@ -227,87 +230,76 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
       }
       ++nu;
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ MMA issuers
     if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(128, kN, false, false);
-      constexpr uint32_t idO = idesc_bf16(128, kN, true, false);
       bool ok = true;
-      // The flattened tile sequence: tile t of nt of the segment with ordinal nu.
-      struct Cur { int t, nt, nu; } cur = {0, 0, -1}, nxt;
-      auto next_tile = [&](Cur& c) -> bool {
-        if (c.nu >= 0 && c.t + 1 < c.nt) {
-          ++c.t;
-          return true;
-        }
-        if (!walk.next(sg)) return false;
-        c.t = 0;
-        c.nt = (sg.k1 - sg.k0 + kKeys - 1) / kKeys;
-        ++c.nu;
-        return true;
-      };
-      auto issue_s = [&](const Cur& c, int m) -> bool {
-        const int st = m % kStages;
-        if (c.t == 0) {
-          if (!mbar_wait(&bars->q_full[c.nu & 1], (c.nu >> 1) & 1, abort_flag, a.err, a.wait_ns))
-            return false;
-        }
-        if (!mbar_wait(&bars->full[st], (m / kStages) & 1, abort_flag, a.err, a.wait_ns))
-          return false;
-        tc_fence_after();
-        const uint64_t dK = sw128_desc(smem_u32(sKV + st * kStage), 16, 1024);
-        const uint64_t dQ = sw128_desc(smem_u32(sQ + (c.nu & 1) * kQBytes), 16, 1024);
+      int n = 0, nu = 0;
+      if (warp == 1) {
+        constexpr uint32_t idS = idesc_bf16(128, kN, false, false);
+        while (ok && walk.next(sg)) {
+          ok = mbar_wait(&bars->q_full[nu & 1], (nu >> 1) & 1, abort_flag, a.err, a.wait_ns);
+          for (int k0 = sg.k0; ok && k0 < sg.k1; k0 += kKeys, ++n) {
+            const int st = n % kStages;
+            ok = mbar_wait(&bars->full[st], (n / kStages) & 1, abort_flag, a.err, a.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dK = sw128_desc(smem_u32(sKV + st * kStage), 16, 1024);
+            const uint64_t dQ = sw128_desc(smem_u32(sQ + (nu & 1) * kQBytes), 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t offA = static_cast<uint64_t>(((kk >> 2) * kSub + (kk & 3) * 32) >> 4);
-          const uint64_t offB = static_cast<uint64_t>(((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4);
-          mma_ss(tb + (m & 1) * kN, dK + offA, dQ + offB, idS, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&bars->s_full[m & 1]);
-        if (c.t == c.nt - 1) mma_commit(&bars->q_empty[c.nu & 1]);
-        return true;
-      };
-      int n = 0;
-      bool have = next_tile(cur);
-      if (have) ok = issue_s(cur, 0);
-      while (ok && have) {
-        nxt = cur;
-        const bool have_next = next_tile(nxt);
-        if (have_next) {
-          ok = issue_s(nxt, n + 1);
-          if (!ok) break;
-        }
-        ok = mbar_wait(&bars->p_full[n & 1], (n >> 1) & 1, abort_flag, a.err, a.wait_ns);
-        if (!ok) break;
-        tc_fence_after();
-        const int st = n % kStages;
-        // A = V^T, M = 128: the second group of 64 rows is the next 64 columns of V (d =
-        // 128) or the zero block (d = 64), LBO bytes further on.
-        const uint32_t aV = smem_u32(sKV + st * kStage + C::NSUB * kSub);
-        const uint32_t lbo = C::PAD > 0 ? smem_u32(sPad) - aV : static_cast<uint32_t>(kSub);
-        const uint64_t dV = sw128_desc(aV, lbo, 1024);
-        const uint64_t dP = sw128_desc(smem_u32(sP + (n & 1) * kPBytes), 16, 1024);
-        const uint32_t tO = tb + 32 + (cur.nu & 1) * kN;
+            for (int g = 0; g < C::NSUB; ++g) {
+              uint64_t da[4], db[4];
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk) {
-          const uint64_t offA = static_cast<uint64_t>((2048 * kk) >> 4);
-          const uint64_t offB = static_cast<uint64_t>(((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4);
-          mma_ss(tO, dV + offA, dP + offB, idO, (cur.t > 0 || kk > 0) ? 1u : 0u);
+              for (int k = 0; k < 4; ++k) {
+                da[k] = dK + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
+                db[k] = dQ + static_cast<uint64_t>((g * (kN * 128) + k * 32) >> 4);
+              }
+              mma_ss_x4(tb + st * kN, da, db, idS, g > 0 ? 1u : 0u);
+            }
+            mma_commit(&bars->s_full[st]);
+            if (k0 + kKeys >= sg.k1) mma_commit(&bars->q_empty[nu & 1]);
+          }
+          ++nu;
         }
-        mma_commit(&bars->p_free[n & 1]);
-        mma_commit(&bars->empty[st]);
-        if (cur.t == cur.nt - 1) mma_commit(&bars->o_full[cur.nu & 1]);
-        cur = nxt;
-        have = have_next;
-        ++n;
+      } else {
+        constexpr uint32_t idO = idesc_bf16(128, kN, true, false);
+        while (ok && walk.next(sg)) {
+          for (int k0 = sg.k0; k0 < sg.k1; k0 += kKeys, ++n) {
+            const int st = n % kStages;
+            ok = mbar_wait(&bars->p_full[st], (n / kStages) & 1, abort_flag, a.err, a.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            // A = V^T, M = 128: the second group of 64 rows is the next 64 columns of V (d =
+            // 128) or, with no offset, the same ones again (d = 64: those rows are never read).
+            const uint64_t dV = sw128_desc(smem_u32(sKV + st * kStage + C::NSUB * kSub),
+                                           D == 128 ? kSub : 0, 1024);
+            const uint64_t dP = sw128_desc(smem_u32(sP + st * kPBytes), 16, 1024);
+            const uint32_t tO = tb + kO + ((nu & 1) * 2 + (n & 1)) * kN;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              uint64_t da[4], db[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                da[k] = dV + static_cast<uint64_t>((2048 * (4 * g + k)) >> 4);
+                db[k] = dP + static_cast<uint64_t>((g * (kN * 128) + k * 32) >> 4);
+              }
+              // a group's first tile of the segment is one of its first two
+              mma_ss_x4(tO, da, db, idO, (k0 - sg.k0 > kKeys || g > 0) ? 1u : 0u);
+            }
+            mma_commit(&bars->empty[st]);
+            if (k0 + kKeys >= sg.k1) mma_commit(&bars->o_full[nu & 1]);
+          }
+          ++nu;
+        }
       }
-      // Every MMA issued has completed before tensor memory is released.
+      // Every MMA issued by either thread has completed before tensor memory is released.
       mma_commit(&bars->drain);
       mbar_wait(&bars->drain, 0, &bars->never, nullptr, a.wait_ns);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax (thread = key row)
-    const int w4 = warp & 3;
+    // Group grp has the tiles whose number n (over all segments) is grp mod 2.
+    const int w4 = warp & 3, grp = (warp - 4) >> 2;
     const int r = 32 * w4 + lane;
     const uint32_t lane_base = tb + (static_cast<uint32_t>(32 * w4) << 16);
     bool ok = true;
@@ -319,32 +311,35 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
         m_run[h] = -INFINITY;
         l_run[h] = 0.f;
       }
+      bool first = true;
       for (int k0 = sg.k0; k0 < sg.k1; k0 += kKeys, ++n) {
+        if ((n & 1) != grp) continue;
         const int st = n % kStages;
         // The stage has landed (its MMAs wait for it too); the wait orders the row mask.
         ok = mbar_wait_warp(&bars->full[st], (n / kStages) & 1, abort_flag, a.err, a.wait_ns);
         if (!ok) break;
         const bool vis = k0 + r < sg.k1 && ((bars->seen[st] >> (r >> 4)) & 1u);
-        ok = mbar_wait_warp(&bars->s_full[n & 1], (n >> 1) & 1, abort_flag, a.err, a.wait_ns);
+        ok = mbar_wait_warp(&bars->s_full[st], (n / kStages) & 1, abort_flag, a.err, a.wait_ns);
         if (!ok) break;
         tc_fence_after();
         uint32_t sv[16];
-        tmem_ld16(lane_base + (n & 1) * kN, sv);
+        tmem_ld16(lane_base + st * kN, sv);
         tmem_wait_ld();
         float x[GP];
 #pragma unroll
         for (int h = 0; h < GP; ++h) x[h] = vis ? __uint_as_float(sv[h]) * a.c : -INFINITY;
-        // CTA-wide maximum per head: warp maxima through shared memory and an mbarrier.
-        float* rm = red_m + (n & 1) * 4 * kN;
+        // The group's maximum per head: warp maxima through shared memory and an mbarrier.
+        const int turn = (n >> 1) & 1;
+        float* rm = red_m + (grp * 2 + turn) * 4 * kN;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
           const float v = warp_max(x[h]);
           if (lane == 0) rm[w4 * kN + h] = v;
         }
-        mbar_arrive(&bars->xmax[n & 1]);
-        ok = mbar_wait_warp(&bars->xmax[n & 1], (n >> 1) & 1, abort_flag, a.err, a.wait_ns);
+        mbar_arrive(&bars->xmax[grp]);
+        ok = mbar_wait_warp(&bars->xmax[grp], turn, abort_flag, a.err, a.wait_ns);
         if (!ok) break;
-        float alpha[GP], muse[GP];
+        float alpha[GP];
         bool grow = false;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
@@ -354,18 +349,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
           alpha[h] = ch ? ex2(m_run[h] - mn) : 1.f;   // m_run = -inf gives 0
           grow |= ch;
           m_run[h] = mn;
-          muse[h] = mn == -INFINITY ? 0.f : mn;
+          x[h] -= mn == -INFINITY ? 0.f : mn;
         }
-        // P^T into this tile's P buffer once the product two tiles back has read it.
-        if (n >= 2) {
-          ok = mbar_wait_warp(&bars->p_free[n & 1], ((n >> 1) - 1) & 1, abort_flag, a.err,
-                              a.wait_ns);
-          if (!ok) break;
-        }
-        uint8_t* pt = sP + (n & 1) * kPBytes;
+        uint8_t* pt = sP + st * kPBytes;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          const float p = ex2(x[h] - muse[h]);   // x = -inf gives 0
+          const float p = ex2(x[h]);   // x = -inf gives 0
           l_run[h] = l_run[h] * alpha[h] + p;
           *reinterpret_cast<__nv_bfloat16*>(pt + nk_offset(h, r)) = __float2bfloat16_rn(p);
         }
@@ -377,15 +366,15 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
             for (int ch = 0; ch < 8; ++ch)
               *reinterpret_cast<uint4*>(vt + s * kSub + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
         }
-        // Rescale the running O^T (lane = d) when a maximum moved after the first tile; the
-        // product of the previous tile must have completed.
-        if (grow && k0 > sg.k0) {
-          ok = mbar_wait_warp(&bars->p_free[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.err,
-                              a.wait_ns);
+        // Rescale the group's O^T (lane = d) when a maximum moved after its first tile; the
+        // product of its previous tile must have completed.
+        if (grow && !first) {
+          ok = mbar_wait_warp(&bars->empty[(n - 2) % kStages], ((n - 2) / kStages) & 1, abort_flag,
+                              a.err, a.wait_ns);
           if (!ok) break;
           tc_fence_after();
           uint32_t ov[16];
-          const uint32_t oaddr = lane_base + 32 + (nu & 1) * kN;
+          const uint32_t oaddr = lane_base + kO + ((nu & 1) * 2 + grp) * kN;
           tmem_ld16(oaddr, ov);
           tmem_wait_ld();
 #pragma unroll
@@ -393,47 +382,62 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
           tmem_st16(oaddr, ov);
           tmem_wait_st();
         }
+        first = false;
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&bars->p_full[n & 1]);
+        mbar_arrive(&bars->p_full[st]);
       }
       if (!ok) break;
-      // ---- the segment's result: row sums over the CTA, then O^T columns (lane = d)
-      float* rl = red_l + (nu & 1) * 4 * kN;
+      // ---- the segment's statistics; then the groups in turn write its result
+      float* rl = red_l + (nu & 1) * 2 * 4 * kN;
+      float* sm = seg_m + (nu & 1) * 2 * 4 * kN;
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
         float v = l_run[h];
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (lane == 0) rl[w4 * kN + h] = v;
+        if (lane == 0) rl[(grp * 4 + w4) * kN + h] = v;
+        if (r == 0) sm[grp * 4 * kN + h] = m_run[h];
       }
       mbar_arrive(&bars->xsum[nu & 1]);
-      ok = mbar_wait_warp(&bars->xsum[nu & 1], (nu >> 1) & 1, abort_flag, a.err, a.wait_ns);
-      if (!ok) break;
-      ok = mbar_wait_warp(&bars->o_full[nu & 1], (nu >> 1) & 1, abort_flag, a.err, a.wait_ns);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t ov[16];
-      tmem_ld16(lane_base + 32 + (nu & 1) * kN, ov);
-      tmem_wait_ld();
-      tc_fence_before();
-      const int slot = sched::slot(sg.pair_start, start.first, blockIdx.x);
-      float* out = a.part + static_cast<size_t>(slot) * G * kPStride;
-      const size_t head0 = static_cast<size_t>(sg.b) * a.Hq + sg.head * G;
+      if ((nu & 1) == grp) {
+        ok = mbar_wait_warp(&bars->xsum[nu & 1], (nu >> 1) & 1, abort_flag, a.err, a.wait_ns);
+        if (!ok) break;
+        ok = mbar_wait_warp(&bars->o_full[nu & 1], (nu >> 1) & 1, abort_flag, a.err, a.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t o0[16], o1[16];
+        tmem_ld16(lane_base + kO + (nu & 1) * 2 * kN, o0);
+        tmem_ld16(lane_base + kO + ((nu & 1) * 2 + 1) * kN, o1);
+        tmem_wait_ld();
+        tc_fence_before();
+        const int slot = sched::slot(sg.pair_start, start.first, blockIdx.x);
+        float* out = a.part + static_cast<size_t>(slot) * G * kPStride;
+        const size_t head0 = static_cast<size_t>(sg.b) * a.Hq + sg.head * G;
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        if (h >= G) break;
-        const float l = rl[h] + rl[kN + h] + rl[2 * kN + h] + rl[3 * kN + h];
-        const float ovh = __uint_as_float(ov[h]);
-        if (sg.whole) {
-          if (r < D)
-            a.o[(head0 + h) * D + r] = __float2bfloat16_rn(l == 0.f ? 0.f : ovh / l);
-          if (r == 0) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m_run[h] + __log2f(l)) * kLn2;
-        } else {
-          if (r < D) out[h * kPStride + r] = ovh;
-          if (r == 0) {
-            out[h * kPStride + D] = m_run[h];
-            out[h * kPStride + D + 1] = l;
+        for (int h = 0; h < GP; ++h) {
+          if (h >= G) break;
+          float l[2], w[2];
+          const float m0 = sm[h], m1 = sm[4 * kN + h], M = fmaxf(m0, m1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float* li = rl + i * 4 * kN + h;
+            l[i] = li[0] + li[kN] + li[2 * kN] + li[3 * kN];
+            w[i] = ex2((i ? m1 : m0) - (M == -INFINITY ? 0.f : M));   // -inf gives 0
+          }
+          const float lt = l[0] * w[0] + l[1] * w[1];
+          // A group without a tile has left its O^T as it was.
+          const float oh = (w[0] > 0.f ? __uint_as_float(o0[h]) * w[0] : 0.f) +
+                           (w[1] > 0.f ? __uint_as_float(o1[h]) * w[1] : 0.f);
+          if (sg.whole) {
+            if (r < D) a.o[(head0 + h) * D + r] = __float2bfloat16_rn(lt == 0.f ? 0.f : oh / lt);
+            if (r == 0) a.lse[head0 + h] = lt == 0.f ? -INFINITY : (M + __log2f(lt)) * kLn2;
+          } else {
+            if (r < D) out[h * kPStride + r] = oh;
+            if (r == 0) {
+              out[h * kPStride + D] = M;
+              out[h * kPStride + D + 1] = lt;
+            }
           }
         }
       }
@@ -452,20 +456,21 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tb, 64);
+    tmem_dealloc(tb, 256);
   }
 }
 
-// One warp per (b, query head): joins the partial results of a pair that more than one CTA
-// worked on; writes o = 0, lse = -inf for an empty sequence.
-template <int D>
+// Joins the partial results of a pair that more than one CTA worked on; writes o = 0, lse = -inf
+// for an empty sequence.  W warps (1 or 8) per (b, query head), each with every W-th part.
+template <int D, int W>
 __global__ void __launch_bounds__(256) decode_paged_combine_kernel(PagedArgs a, int workers) {
   constexpr int PS = TC<D>::PSTRIDE, PER = D / 32;
+  __shared__ float red[8][D + 2];          // a warp's columns, maximum and sum
   griddep_wait();
   griddep_launch_dependents();
-  const long long row = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= static_cast<long long>(a.B) * a.Hq) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % W;
+  const long long row = blockIdx.x * static_cast<long long>(8 / W) + warp / W;
+  if (row >= static_cast<long long>(a.B) * a.Hq) return;   // W = 8: the whole block
   const int b = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
   const int G = a.Hq / a.Hkv, g = hq / G, h = hq % G;
   const long long p0 = a.prefix[b], p1 = a.prefix[b + 1], total = a.prefix[a.B];
@@ -478,36 +483,71 @@ __global__ void __launch_bounds__(256) decode_paged_combine_kernel(PagedArgs a, 
     const long long first = p0 + g * n;
     workers = sched::active(total, workers);
     const int w0 = sched::owner(first, total, workers);
-    const int w1 = sched::owner(first + n - 1, total, workers);
-    if (w0 == w1) return;   // finished by its CTA
+    const int parts = sched::owner(first + n - 1, total, workers) - w0 + 1;
+    if (parts == 1) return;   // finished by its CTA
+    // Only the first part can sit in the second of its worker's slots.
+    const int slot0 = sched::slot(first, sched::range_start(total, w0, workers), w0);
     const float* part = a.part + static_cast<size_t>(h) * PS;
     const size_t stride = static_cast<size_t>(G) * PS;
-    auto at = [&](int w) {
-      return part + sched::slot(first, sched::range_start(total, w, workers), w) * stride;
-    };
-    for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, at(w)[D]);
+    auto at = [&](int i) { return part + (i == 0 ? slot0 : 2 * (w0 + i)) * stride; };
+    // The warp's parts are sub, sub + W, ...: lane j has the statistics of the j-th of a batch.
+    for (int base = sub; base < parts; base += 32 * W) {
+      const int mine = base + lane * W;
+      const float* p = at(mine < parts ? mine : base);
+      const float m = mine < parts ? p[D] : -INFINITY, l = mine < parts ? p[D + 1] : 0.f;
+      const float mb = fmaxf(M, warp_max(m));
+      const float use = mb == -INFINITY ? 0.f : mb;
+      const float keep = ex2(M - use);           // M = -inf gives 0
+      const float wt = ex2(m - use);             // a part without a visible key weighs 0
+      M = mb;
+      lsum = lsum * keep + l * wt;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    if (M == -INFINITY) M = 0.f;
-    for (int base = w0; base <= w1; base += 32) {
-      const int w = base + lane;
-      float wt = 0.f;
-      if (w <= w1) {
-        const float* p = at(w);
-        wt = ex2(p[D] - M);     // a part without a visible key (-inf) weighs 0
-        lsum += p[D + 1] * wt;
-      }
-      const int cnt = min(32, w1 - base + 1);
-#pragma unroll 4
+      for (int i = 0; i < PER; ++i) acc[i] *= keep;
+      const int cnt = min(32, (parts - base + W - 1) / W);
+#pragma unroll 8
       for (int j = 0; j < cnt; ++j) {
         const float wj = __shfl_sync(0xffffffffu, wt, j);
-        const float* p = at(base + j) + lane * PER;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = fmaf(wj, p[i], acc[i]);
+        const float* pj = at(base + j * W) + lane * PER;
+        if constexpr (PER == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(pj);
+          acc[0] = fmaf(wj, v.x, acc[0]);
+          acc[1] = fmaf(wj, v.y, acc[1]);
+          acc[2] = fmaf(wj, v.z, acc[2]);
+          acc[3] = fmaf(wj, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(pj);
+          acc[0] = fmaf(wj, v.x, acc[0]);
+          acc[1] = fmaf(wj, v.y, acc[1]);
+        }
       }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) red[warp][lane * PER + i] = acc[i];
+    if (lane == 0) {
+      red[warp][D] = M;
+      red[warp][D + 1] = lsum;
+    }
+    __syncthreads();
+    if (sub > 0) return;
+    float mw[W];
+    M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) M = fmaxf(M, mw[w] = red[w][D]);
+    const float use = M == -INFINITY ? 0.f : M;
+    lsum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float wt = ex2(mw[w] - use);
+      lsum += red[w][D + 1] * wt;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = fmaf(red[w][lane * PER + i], wt, acc[i]);
+    }
   }
   const float inv = lsum == 0.f ? 0.f : 1.f / lsum;   // a NaN sum stays one
   __nv_bfloat16* orow = a.o + static_cast<size_t>(row) * D + lane * PER;
@@ -532,8 +572,13 @@ cudaError_t launch_g(const CUtensorMap& mk, const CUtensorMap& mv, const CUtenso
   cudaError_t e = launch_dependent(decode_paged_kernel<D, GP>, dim3(workers), dim3(kThreads),
                                    TC<D>::SMEM, s, mk, mv, mq, a);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.B) * a.Hq + 7) / 8);
-  return launch_dependent(decode_paged_combine_kernel<D>, dim3(blocks), dim3(256), 0, s, a,
+  // Few pairs: many parts each, and rows enough for one a block.
+  const long long rows = static_cast<long long>(a.B) * a.Hq;
+  if (workers > 4ll * a.B * a.Hkv)
+    return launch_dependent(decode_paged_combine_kernel<D, 8>, dim3(static_cast<unsigned>(rows)),
+                            dim3(256), 0, s, a, workers);
+  return launch_dependent(decode_paged_combine_kernel<D, 1>,
+                          dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a,
                           workers);
 }
 

@@ -11,20 +11,28 @@
 //
 // What bounds it: a token costs 1152 bytes and 2176 H operations, so H = 128 asks for 242
 // operations a byte, near the card's 295: HBM and the tensor cores are both close, and few
-// heads leave HBM alone.  All heads of a sequence are therefore the M = 128 rows of one tile
-// (rows past H compute what is never read), so a cached row is read once for all of them.
+// heads leave HBM alone.  All heads of a sequence are the M = 128 rows of one tile (rows past H
+// compute what is never read), so a cached row is read once for all of them.
 //
 // Tensor memory sets the layout: O for 128 heads x 512 columns would fill all of it.  Two CTAs
-// share a worker's keys, each forms the scores of all 576 columns and keeps O for one half of
-// the 512: 1.53 times the operations, but no exchange between the two.  512 columns then hold
-// O (256), two score tiles of 64 keys (128, P overwrites S as bf16) and the last 256 columns
-// of Q (128, the A operand of 16 of the 36 score steps); the first 320 columns of Q stay in
-// shared memory (80 KB) beside two stages of [64 keys][576] (144 KB).
-//   warp 0     producer: Q, then K tiles page by page;   warp 1  MMA issuer (one thread);
-//   warp 2     tensor memory;                            warps 4-7 softmax, thread = head.
-// Scores of tile n + 1 are issued before O += P V of tile n.  Work is shared out as
-// fa_paged_sched.cuh says, over pairs of CTAs.  Every wait is bounded; on expiry the CTA
-// records FA_ERR_TIMEOUT and leaves.
+// share a worker's keys, each forms the scores of all 576 columns and keeps O for its own half
+// of the 512: 1.53 times the operations, but no exchange between the two.  512 columns then hold
+// O (256), one score tile of 128 keys (128, P overwrites S as bf16) and the own half's 256
+// columns of Q (128, the A operand of 16 of the 36 score steps); the other 320 columns of Q stay
+// in shared memory (80 KB).  A score tile of 128 keys and not two of 64: an MMA takes the pipe
+// and its issuer 70 to 130 cycles here whether N is 64 or 128 (traced: 3950 cycles of scores a
+// 64-key tile), so half as many of them beat the overlap that two tiles would give.
+//
+// A tile of 128 keys is 144 KB, all that is left of shared memory.  Only the own half (64 KB)
+// has to stay until P V; the other 80 KB are refilled as soon as their score MMAs have run, behind
+// the rest of the tile's work, so the next tile's are there when its scores begin, and the own
+// half, fetched behind P V (from L2: the other CTA has had it), when they get to it.  One barrier
+// for the 80 KB: a wait and a commit between four MMAs cost as much as the four.
+//   warp 0     producer: Q, then the tiles page by page;  warp 1  MMA issuer (one thread);
+//   warp 2     tensor memory;                             warps 4-11 softmax, a row in 4 threads.
+// Work is shared out as fa_paged_sched.cuh says, over pairs of CTAs.  Every wait is bounded; on
+// expiry the CTA records FA_ERR_TIMEOUT and leaves.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -42,40 +50,46 @@ using sched::Segment;
 
 constexpr int kRank = FA_LATENT_RANK, kRow = FA_LATENT_RANK + FA_LATENT_ROPE;
 constexpr int kHeads = 128;                   // rows of a tile
-constexpr int kKeys = 64;                     // keys per tile
-constexpr int kGranule = 128;                 // keys of the smallest share of the work
-constexpr int kStages = 2;
-constexpr int kSubs = kRow / 64;              // 64-column subtiles of a row
-constexpr int kKSub = kKeys * 128;            // [64 keys][64 columns], 8 KB
-constexpr int kStage = kSubs * kKSub;
-constexpr int kQSubs = 5;                     // subtiles of Q in shared memory
-constexpr int kQSub = kHeads * 128;           // [128 heads][64 columns], 16 KB
+constexpr int kKeys = 128;                    // keys per tile
+constexpr int kSub = kKeys * 128;             // [128 keys][64 columns], 16 KB
 constexpr int kHalf = kRank / 2;              // columns of O per CTA
-constexpr int kThreads = 256;
-constexpr uint32_t kTS = kHalf, kTQ = kHalf + 2 * kKeys;   // columns of S and of Q's rest
+constexpr int kOwnSubs = kHalf / 64;          // subtiles of the own half
+constexpr int kOwn = kOwnSubs * kSub;
+constexpr int kRestSubs = kRow / 64 - kOwnSubs;   // the other half's, then the rotated part's
+constexpr int kQSub = kHeads * 128;           // [128 heads][64 columns], 16 KB
+constexpr int kThreads = 384;
+constexpr uint32_t kTS = kHalf, kTQ = kHalf + kKeys;       // columns of S and of Q's own half
+constexpr int kMaxWorkers = 256;              // the combine kernel's table of parts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units; exact, see fa_fwd_sm103.cu
 
 struct Bars {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
-  uint64_t q_full;      // Q's first columns have landed in shared memory
-  uint64_t q_rest;      // Q's last columns are in tensor memory
+  uint64_t own_full;
+  uint64_t own_empty;   // P V of a tile has completed
+  uint64_t rest_full;
+  uint64_t rest_empty;  // the rest's score products of a tile have completed
+  uint64_t q_full;      // Q's columns of the rest have landed in shared memory
+  uint64_t q_own;       // Q's own half is in tensor memory
   uint64_t q_empty;     // every score product of the segment has completed
-  uint64_t s_full[2];
-  uint64_t p_full[2];
-  uint64_t pv_done[2];
-  uint64_t o_full;
+  uint64_t s_full;
+  uint64_t p_full;
   uint64_t drain;
   uint32_t tmem_base;
-  uint32_t seen[kStages];  // bit i: rows 16 i ... 16 i + 15 of the stage are in the pool
+  uint32_t seen[2];  // bit i: rows 16 i ... 16 i + 15 of the tile are in the pool
   int abort;
   int never;  // stays 0: the drain wait must not be cut short by an abort
 };
 
-constexpr int kSmem = 1024 + kQSubs * kQSub + kStages * kStage + static_cast<int>(sizeof(Bars));
+constexpr int kSmem = 1024 + kRestSubs * kQSub + kOwn + kRestSubs * kSub +
+                      static_cast<int>(sizeof(Bars));
 static_assert(kSmem <= 226 * 1024, "shared memory");
+
+template <int LINES>
+__device__ __forceinline__ void prefetch_l2(const __nv_bfloat16* p) {   // LINES lines of 128 bytes
+#pragma unroll
+  for (int i = 0; i < LINES; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64 * i));
+}
 
 struct LatentArgs {
   const __nv_bfloat16* q;  // [B, H, 576]
@@ -87,9 +101,9 @@ struct LatentArgs {
   float c;                 // scale log2 e
   __nv_bfloat16* o;        // [B, H, 512]
   float* lse;
-  float* part;             // [2 workers][2 halves][H][256]
-  float2* stat;            // [2 workers][2 halves][H]: maximum, sum
-  long long* prefix;       // [B + 1] granules before each sequence
+  float* part;             // [2 workers][H][512]
+  float2* stat;            // [2 workers][2 halves][H]: maximum, sum (a half's own)
+  long long* prefix;       // [B + 1] tiles before each sequence
   int* err;
   unsigned long long wait_ns;
 };
@@ -100,30 +114,29 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = base;                        // [kQSubs][128 heads][64]
-  uint8_t* sK = sQ + kQSubs * kQSub;         // [kStages][kSubs][64 keys][64]
-  Bars* bars = reinterpret_cast<Bars*>(sK + kStages * kStage);
+  uint8_t* sQ = base;                        // [kRestSubs][128 heads][64]
+  uint8_t* sOwn = sQ + kRestSubs * kQSub;    // [kOwnSubs][128 keys][64]
+  uint8_t* sRest = sOwn + kOwn;             // [kRestSubs][128 keys][64]
+  Bars* bars = reinterpret_cast<Bars*>(sRest + kRestSubs * kSub);
   __shared__ sched::Start start;
   __shared__ long long scan[kThreads / 32 + 1];
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = blockIdx.x & 1, worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
   const int cap = a.max_pages << a.page_shift;
+  // First column of the i-th subtile of the rest: the other half's, then the rotated part's.
+  auto rest_col = [&](int i) { return i < kOwnSubs ? (1 - half) * kHalf + 64 * i : kRank; };
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], 1);
-    }
+    mbar_init(&bars->own_full, 1);
+    mbar_init(&bars->own_empty, 1);
+    mbar_init(&bars->rest_full, 1);
+    mbar_init(&bars->rest_empty, 1);
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_rest, 128);
+    mbar_init(&bars->q_own, 256);
     mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 128);
-      mbar_init(&bars->pv_done[i], 1);
-    }
-    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->s_full, 1);
+    mbar_init(&bars->p_full, 256);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     bars->never = 0;
@@ -140,10 +153,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  sched::find_start<kGranule, kThreads>(&start, scan, a.cache_len, a.B, 1, cap, worker, workers,
+  sched::find_start<kKeys, kThreads>(&start, scan, a.cache_len, a.B, 1, cap, worker, workers,
                                         blockIdx.x == 0 ? a.prefix : nullptr);
   const uint32_t tb = bars->tmem_base;
-  sched::Walk<kGranule> walk(start, a.cache_len, 1, cap);
+  sched::Walk<kKeys> walk(start, a.cache_len, 1, cap);
   Segment sg;
 
   if (warp == 0) {
@@ -151,49 +164,54 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
     const int shift = a.page_shift;
     const int rows = min(kKeys, 1 << shift);        // rows of a box
     const int boxes = kKeys / rows;
-    const uint32_t bits = (1u << (rows / 16)) - 1u; // of a box in the stage's row mask
+    const uint32_t bits = (1u << (rows / 16)) - 1u; // of a box in the tile's row mask
     bool ok = true;
-    int n = 0, nu = 0;
+    int n = 0, nu = 0;                              // tiles, segments so far
     while (ok && walk.next(sg)) {
       if (nu > 0) {
         ok = mbar_wait_warp(&bars->q_empty, (nu - 1) & 1, abort_flag, a.err, a.wait_ns);
         if (!ok) break;
       }
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full, kQSubs * kQSub);
-        for (int s = 0; s < kQSubs; ++s)
-          tma_load_3d(sQ + s * kQSub, &mq, &bars->q_full, 64 * s, sg.b * a.H, 0);
+        mbar_arrive_expect_tx(&bars->q_full, kRestSubs * kQSub);
+        for (int s = 0; s < kRestSubs; ++s)
+          tma_load_3d(sQ + s * kQSub, &mq, &bars->q_full, rest_col(s), sg.b * a.H, 0);
       }
       const int32_t* row = a.table + sg.b * a.table_stride;
-      for (int k0 = sg.k0; k0 < sg.k1; k0 += kKeys, ++n) {
-        const int st = n % kStages;
+      for (int k0 = sg.k0; ok && k0 < sg.k1; k0 += kKeys, ++n) {
         const int x = k0 + lane * rows;             // first token of box `lane`
         int p = -1;
         if (lane < boxes && x < sg.len) p = row[x >> shift];
         const bool in = p >= 0 && p < a.num_pages;
         const uint32_t pages = __ballot_sync(0xffffffffu, in);
-        if (n >= kStages) {
-          ok = mbar_wait_warp(&bars->empty[st], ((n / kStages) - 1) & 1, abort_flag, a.err,
-                              a.wait_ns);
-          if (!ok) break;
-        }
+        const uint32_t bytes = static_cast<uint32_t>(__popc(pages)) * rows * 128;  // a subtile's
+        const int in_page = (1 << shift) - 1;
         if (lane == 0) {
           uint32_t seen = 0;
           for (int i = 0; i < boxes; ++i)
             if (pages >> i & 1u) seen |= bits << (i * (rows / 16));
-          bars->seen[st] = seen;
-          mbar_arrive_expect_tx(&bars->full[st],
-                                static_cast<uint32_t>(__popc(pages)) * rows * kRow * 2);
+          bars->seen[n & 1] = seen;                 // released with own_full below
         }
+        ok = mbar_wait_warp(&bars->rest_empty, (n & 1) ^ 1, abort_flag, a.err, a.wait_ns);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->rest_full, kRestSubs * bytes);
         __syncwarp();
-        // Box i / kSubs, subtile i % kSubs, spread over the lanes.
-        for (int i0 = 0; i0 < boxes * kSubs; i0 += 32) {
-          const int i = i0 + lane, box = i / kSubs, s = i - box * kSubs;
-          const int pb = __shfl_sync(0xffffffffu, p, box & 31);
-          if (i < boxes * kSubs && (pages >> box & 1u))
-            tma_load_4d(sK + st * kStage + s * kKSub + box * rows * 128, &mc, &bars->full[st],
-                        64 * s, (k0 + box * rows) & ((1 << shift) - 1), 0, pb);
+        if (in) {
+#pragma unroll
+          for (int i = 0; i < kRestSubs; ++i)
+            tma_load_4d(sRest + i * kSub + lane * rows * 128, &mc, &bars->rest_full, rest_col(i),
+                        x & in_page, 0, p);
         }
+        ok = mbar_wait_warp(&bars->own_empty, (n & 1) ^ 1, abort_flag, a.err, a.wait_ns);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->own_full, kOwnSubs * bytes);
+        __syncwarp();
+        // Box lane / 4, subtile lane % 4 of the own half.
+        const int box = lane >> 2, s = lane & 3;
+        const int pb = __shfl_sync(0xffffffffu, p, box);
+        if (box < boxes && (pages >> box & 1u))
+          tma_load_4d(sOwn + s * kSub + box * rows * 128, &mc, &bars->own_full,
+                      half * kHalf + 64 * s, (k0 + box * rows) & in_page, 0, pb);
       }
       ++nu;
     }
@@ -202,100 +220,88 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16(128, kKeys, false, false);
       constexpr uint32_t idO = idesc_bf16(128, kHalf, false, true);
-      bool ok = true;
-      struct Cur { int t, nt, nu; } cur = {0, 0, -1}, nxt;
-      auto next_tile = [&](Cur& c) -> bool {
-        if (c.nu >= 0 && c.t + 1 < c.nt) {
-          ++c.t;
-          return true;
-        }
-        if (!walk.next(sg)) return false;
-        c.t = 0;
-        c.nt = (sg.k1 - sg.k0 + kKeys - 1) / kKeys;
-        ++c.nu;
-        return true;
-      };
       const uint64_t dQ = sw128_desc(smem_u32(sQ), 16, 1024);
-      auto issue_s = [&](const Cur& c, int m) -> bool {
-        const int st = m % kStages;
-        if (c.t == 0) {
-          if (!mbar_wait(&bars->q_full, c.nu & 1, abort_flag, a.err, a.wait_ns)) return false;
-          if (!mbar_wait(&bars->q_rest, c.nu & 1, abort_flag, a.err, a.wait_ns)) return false;
-        }
-        if (!mbar_wait(&bars->full[st], (m / kStages) & 1, abort_flag, a.err, a.wait_ns))
-          return false;
-        tc_fence_after();
-        const uint64_t dK = sw128_desc(smem_u32(sK + st * kStage), 16, 1024);
-        const uint32_t tS = tb + kTS + (m & 1) * kKeys;
+      const uint64_t dRest = sw128_desc(smem_u32(sRest), 16, 1024);
+      const uint64_t dOwn = sw128_desc(smem_u32(sOwn), 16, 1024);     // own half, K-major
+      const uint64_t dV = sw128_desc(smem_u32(sOwn), kSub, 1024);     // the same, along the keys
+      const uint32_t tS = tb + kTS;
+      bool ok = true;
+      int n = 0, nu = 0;
+      while (ok && walk.next(sg)) {
+        ok = mbar_wait(&bars->q_full, nu & 1, abort_flag, a.err, a.wait_ns) &&
+             mbar_wait(&bars->q_own, nu & 1, abort_flag, a.err, a.wait_ns);
+        for (int k0 = sg.k0; ok && k0 < sg.k1; k0 += kKeys, ++n) {
+          ok = mbar_wait(&bars->rest_full, n & 1, abort_flag, a.err, a.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < kSubs; ++g) {
-          uint64_t db[4];
+          for (int i = 0; i < kRestSubs; ++i) {
+            uint64_t da[4], db[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) db[k] = dK + static_cast<uint64_t>((g * kKSub + k * 32) >> 4);
-          if (g < kQSubs) {
-            uint64_t da[4];
+            for (int k = 0; k < 4; ++k) {
+              da[k] = dQ + static_cast<uint64_t>((i * kQSub + k * 32) >> 4);
+              db[k] = dRest + static_cast<uint64_t>((i * kSub + k * 32) >> 4);
+            }
+            mma_ss_x4(tS, da, db, idS, i > 0 ? 1u : 0u);
+          }
+          mma_commit(&bars->rest_empty);
+          ok = mbar_wait(&bars->own_full, n & 1, abort_flag, a.err, a.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              da[k] = dQ + static_cast<uint64_t>((g * kQSub + k * 32) >> 4);
-            mma_ss_x4(tS, da, db, idS, g > 0 ? 1u : 0u);
-          } else {
+          for (int g = 0; g < kOwnSubs; ++g) {
             uint32_t ta[4];
+            uint64_t db[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ta[k] = tb + kTQ + 8 * (4 * (g - kQSubs) + k);
+            for (int k = 0; k < 4; ++k) {
+              ta[k] = tb + kTQ + 8 * (4 * g + k);
+              db[k] = dOwn + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
+            }
             mma_ts_x4(tS, ta, db, idS, 1u);
           }
-        }
-        mma_commit(&bars->s_full[m & 1]);
-        if (c.t == c.nt - 1) mma_commit(&bars->q_empty);
-        return true;
-      };
-      int n = 0;
-      bool have = next_tile(cur);
-      if (have) ok = issue_s(cur, 0);
-      while (ok && have) {
-        nxt = cur;
-        const bool have_next = next_tile(nxt);
-        if (have_next) {
-          ok = issue_s(nxt, n + 1);
+          mma_commit(&bars->s_full);
+          if (k0 + kKeys >= sg.k1) mma_commit(&bars->q_empty);
+          ok = mbar_wait(&bars->p_full, n & 1, abort_flag, a.err, a.wait_ns);
           if (!ok) break;
-        }
-        ok = mbar_wait(&bars->p_full[n & 1], (n >> 1) & 1, abort_flag, a.err, a.wait_ns);
-        if (!ok) break;
-        tc_fence_after();
-        const int st = n % kStages;
-        // V: this CTA's four subtiles of the same tile, read along the keys.
-        const uint64_t dV = sw128_desc(smem_u32(sK + st * kStage + half * 4 * kKSub), kKSub, 1024);
-        uint32_t ta[4];
-        uint64_t db[4];
+          tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          ta[k] = tb + kTS + (n & 1) * kKeys + 8 * k;
-          db[k] = dV + static_cast<uint64_t>((2048 * k) >> 4);
+          for (int g = 0; g < 2; ++g) {
+            uint32_t ta[4];
+            uint64_t db[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              ta[k] = tS + 8 * (4 * g + k);
+              db[k] = dV + static_cast<uint64_t>((2048 * (4 * g + k)) >> 4);
+            }
+            mma_ts_x4(tb, ta, db, idO, (k0 > sg.k0 || g > 0) ? 1u : 0u);
+          }
+          mma_commit(&bars->own_empty);
         }
-        mma_ts_x4(tb, ta, db, idO, cur.t > 0 ? 1u : 0u);
-        mma_commit(&bars->pv_done[n & 1]);
-        mma_commit(&bars->empty[st]);
-        if (cur.t == cur.nt - 1) mma_commit(&bars->o_full);
-        cur = nxt;
-        have = have_next;
-        ++n;
+        ++nu;
       }
       // Every MMA issued has completed before tensor memory is released.
       mma_commit(&bars->drain);
       mbar_wait(&bars->drain, 0, &bars->never, nullptr, a.wait_ns);
     }
   } else if (warp >= 4) {
-    // ------------------------------------------------------------ softmax (thread = head)
-    const int w4 = warp & 3;
-    const int r = 32 * w4 + lane;
-    const uint32_t lane_base = tb + (static_cast<uint32_t>(32 * w4) << 16);
-    // The last 256 columns of the segment's queries into tensor memory.  The score products of
-    // the segment before have completed: this warp has read the last of them.
+    // ------------------------------------------------------------ softmax warps
+    // Warp 4 + q + 4h owns heads 32q + 16h + [0, 16) through the 16-lane shapes: thread t holds
+    // heads A = 32q + 16h + t/4 and B = A + 8, keys 8c + 2(t%4) + {0, 1} for c = 0..15.
+    const int q4 = warp & 3, hh = (warp - 4) >> 2, t4 = lane & 3;
+    const int rA = 32 * q4 + 16 * hh + (lane >> 2), rB = rA + 8;
+    const uint32_t quarter = tb + (static_cast<uint32_t>(32 * q4) << 16);
+    const uint32_t lane_base = quarter + (static_cast<uint32_t>(16 * hh) << 16);
+    const uint64_t c2 = f2_pack(a.c, a.c);
+    // The own half of the segment's queries into tensor memory, 128 of the 256 columns by each
+    // group of four warps.  The score products of the segment before have completed: this warp
+    // has read the last of them.
     auto write_q = [&](const Segment& s) {
+      const int r = 32 * q4 + lane;
       const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<size_t>(s.b) * a.H + (r < a.H ? r : 0)) * kRow + kQSubs * 64);
+          a.q + (static_cast<size_t>(s.b) * a.H + (r < a.H ? r : 0)) * kRow + half * kHalf +
+          128 * hh);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -305,138 +311,168 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
           w[4 * k + 2] = x.z;
           w[4 * k + 3] = x.w;
         }
-        tmem_st32(lane_base + kTQ + 32 * i, w);
+        tmem_st32(quarter + kTQ + 64 * hh + 32 * i, w);
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars->q_rest);
+      mbar_arrive(&bars->q_own);
     };
     bool ok = true;
-    int n = 0, nu = 0;
+    int n = 0;
     bool have = walk.next(sg);
     if (have) write_q(sg);
     while (ok && have) {
-      float m_run = -INFINITY, l_run = 0.f;
+      Segment nx;
+      const bool more = walk.next(nx);
+      if (more && 32 * q4 + lane < a.H)   // the next segment's queries into L2 meanwhile
+        prefetch_l2<5>(a.q + (static_cast<size_t>(nx.b) * a.H + 32 * q4 + lane) * kRow + 256 * hh);
+      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
       for (int k0 = sg.k0; k0 < sg.k1; k0 += kKeys, ++n) {
-        const int st = n % kStages;
-        // The stage has landed (its MMAs wait for it too); the wait orders the row mask.
-        ok = mbar_wait_warp(&bars->full[st], (n / kStages) & 1, abort_flag, a.err, a.wait_ns);
+        // The own half has landed (its MMAs wait for it too); the wait orders the row mask.
+        ok = mbar_wait_warp(&bars->own_full, n & 1, abort_flag, a.err, a.wait_ns);
         if (!ok) break;
-        const uint32_t seen = bars->seen[st];
+        const uint32_t seen = bars->seen[n & 1];
         const int valid = sg.k1 - k0;
-        ok = mbar_wait_warp(&bars->s_full[n & 1], (n >> 1) & 1, abort_flag, a.err, a.wait_ns);
+        ok = mbar_wait_warp(&bars->s_full, n & 1, abort_flag, a.err, a.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t tS = lane_base + kTS + (n & 1) * kKeys;
-        uint32_t sv[64];
-        tmem_ld64_wait(tS, tS + 32, sv);
-        float x[64];
+        uint32_t v[64];
+        tmem_ld_16x256b_x16_wait(lane_base + kTS, v);
+        float sv[64];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(sv[i]);
-        if (valid < kKeys || seen != 0xfu) {
+        for (int i = 0; i < 64; ++i) sv[i] = __uint_as_float(v[i]);
+        if (valid < kKeys || seen != 0xffu) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i >= valid || !((seen >> (i >> 4)) & 1u)) x[i] = -INFINITY;
+          for (int cc = 0; cc < 16; ++cc) {
+            const int key = 8 * cc + 2 * t4;
+            const bool page = (seen >> (cc >> 1)) & 1u;
+            if (!page || key >= valid) sv[4 * cc] = sv[4 * cc + 2] = -INFINITY;
+            if (!page || key + 1 >= valid) sv[4 * cc + 1] = sv[4 * cc + 3] = -INFINITY;
+          }
           // Hidden rows: zero the values this CTA multiplies, so that 0 x (anything) stays 0.
-          const int row = r & 63;
+          const int row = (tid - 128) & 127, s0 = (tid - 128) >> 7;
           if (row >= valid || !((seen >> (row >> 4)) & 1u)) {
-            uint8_t* vt = sK + st * kStage + (half * 4 + (r >> 6) * 2) * kKSub + row * 128;
+            uint8_t* vt = sOwn + s0 * 2 * kSub + row * 128;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
               for (int ch = 0; ch < 8; ++ch)
-                *reinterpret_cast<uint4*>(vt + s * kKSub + ch * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(vt + s * kSub + ch * 16) = make_uint4(0, 0, 0, 0);
           }
+          fence_proxy_async_smem();
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float ma0 = fmaxf(sv[0], sv[1]), ma1 = fmaxf(sv[4], sv[5]);
+        float mb0 = fmaxf(sv[2], sv[3]), mb1 = fmaxf(sv[6], sv[7]);
 #pragma unroll
-        for (int i = 0; i < 64; i += 8)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmax3(mx[j], x[i + 2 * j], x[i + 2 * j + 1]);
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
-        const float mn = mt > m_run + kRescaleThreshold ? mt : m_run;
-        const bool ch = mn != m_run;
-        const float alpha = ch ? ex2(m_run - mn) : 1.f;   // m_run = -inf gives 0
-        m_run = mn;
-        const float muse = mn == -INFINITY ? 0.f : mn;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int cc = 2; cc < 16; cc += 2) {
+          ma0 = fmax3(ma0, sv[4 * cc], sv[4 * cc + 1]);
+          mb0 = fmax3(mb0, sv[4 * cc + 2], sv[4 * cc + 3]);
+          ma1 = fmax3(ma1, sv[4 * cc + 4], sv[4 * cc + 5]);
+          mb1 = fmax3(mb1, sv[4 * cc + 6], sv[4 * cc + 7]);
+        }
+        float tA = fmaxf(ma0, ma1), tB = fmaxf(mb0, mb1);
+        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
+        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 1));
+        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2)) * a.c;
+        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2)) * a.c;
+        const float nA = tA > mA + kRescaleThreshold ? tA : mA;
+        const float nB = tB > mB + kRescaleThreshold ? tB : mB;
+        const bool chA = nA != mA, chB = nB != mB;
+        const float alphaA = chA ? ex2(mA - nA) : 1.f;   // m = -inf gives 0
+        const float alphaB = chB ? ex2(mB - nB) : 1.f;
+        mA = nA;
+        mB = nB;
+        const float useA = nA == -INFINITY ? 0.f : nA, useB = nB == -INFINITY ? 0.f : nB;
+        const uint64_t negA = f2_pack(-useA, -useA), negB = f2_pack(-useB, -useB);
+        uint64_t accA = f2_pack(0.f, 0.f), accB = accA;
         uint32_t pk[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float p0 = ex2(fmaf(x[2 * i], a.c, -muse));
-          const float p1 = ex2(fmaf(x[2 * i + 1], a.c, -muse));
-          sum[i & 3] += p0 + p1;
-          pk[i] = pack_bf16x2(p0, p1);
+        for (int cc = 0; cc < 16; ++cc) {
+          const float2 xa = f2_unpack(ffma2(f2_pack(sv[4 * cc], sv[4 * cc + 1]), c2, negA));
+          const float2 xb = f2_unpack(ffma2(f2_pack(sv[4 * cc + 2], sv[4 * cc + 3]), c2, negB));
+          const float pa0 = ex2(xa.x), pa1 = ex2(xa.y);
+          const float pb0 = ex2(xb.x), pb1 = ex2(xb.y);
+          accA = fadd2(accA, f2_pack(pa0, pa1));
+          accB = fadd2(accB, f2_pack(pb0, pb1));
+          pk[2 * cc] = pack_bf16x2(pa0, pa1);
+          pk[2 * cc + 1] = pack_bf16x2(pb0, pb1);
         }
-        tmem_st32(tS, pk);
-        l_run = l_run * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-        // Rescale the running O when a maximum moved after the first tile; the product of the
-        // previous tile must have completed.
-        if (k0 > sg.k0 && __any_sync(0xffffffffu, ch)) {
-          ok = mbar_wait_warp(&bars->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.err,
-                              a.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
+        // P over the first 64 columns of S in this warp's 16 lanes, which no other warp reads.
+        tmem_st_16x128b_x16(lane_base + kTS, pk);
+        const float2 sa = f2_unpack(accA), sb = f2_unpack(accB);
+        lA = lA * alphaA + (sa.x + sa.y);
+        lB = lB * alphaB + (sb.x + sb.y);
+        // Rescale the running O when a maximum moved after the first tile: its products were
+        // issued before these scores, so they have completed.
+        if (k0 > sg.k0 && __any_sync(0xffffffffu, chA || chB)) {
 #pragma unroll 1
-          for (int i = 0; i < kHalf / 32; ++i) {
-            uint32_t ov[32];
-            tmem_ld32_wait(lane_base + 32 * i, ov);
+          for (int i = 0; i < kHalf / 64; ++i) {
+            uint32_t o[32];
+            tmem_ld_16x256b_x8_wait(lane_base + 64 * i, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
-            tmem_st32(lane_base + 32 * i, ov);
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint(__uint_as_float(o[k]) * ((k & 2) ? alphaB : alphaA));
+            tmem_st_16x256b_x8(lane_base + 64 * i, o);
           }
         }
         tmem_wait_st();
-        fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&bars->p_full[n & 1]);
+        mbar_arrive(&bars->p_full);
       }
       if (!ok) break;
       // The next segment's queries first: the issuer's next scores wait for them.
-      Segment nx;
-      have = walk.next(nx);
+      have = more;
       if (have) write_q(nx);
-      ok = mbar_wait_warp(&bars->o_full, nu & 1, abort_flag, a.err, a.wait_ns);
+      ok = mbar_wait_warp(&bars->own_empty, (n - 1) & 1, abort_flag, a.err, a.wait_ns);
       if (!ok) break;
       tc_fence_after();
-      const int slot = 2 * sched::slot(sg.pair_start, start.first, worker) + half;
-      const size_t head = static_cast<size_t>(sg.b) * a.H + r;
-      const size_t prow = static_cast<size_t>(slot) * a.H + r;
-      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;   // a NaN sum stays one
+      lA += __shfl_xor_sync(0xffffffffu, lA, 1);
+      lB += __shfl_xor_sync(0xffffffffu, lB, 1);
+      lA += __shfl_xor_sync(0xffffffffu, lA, 2);
+      lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+      const float invA = lA == 0.f ? 0.f : 1.f / lA;        // a NaN sum stays one
+      const float invB = lB == 0.f ? 0.f : 1.f / lB;
+      const size_t head0 = static_cast<size_t>(sg.b) * a.H;
+      const int slot = sched::slot(sg.pair_start, start.first, worker);
+      const size_t prow0 = static_cast<size_t>(slot) * a.H;
 #pragma unroll 1
-      for (int i = 0; i < kHalf / 32; ++i) {
+      for (int i = 0; i < kHalf / 64; ++i) {
         uint32_t ov[32];
         __syncwarp();
-        tmem_ld32_wait(lane_base + 32 * i, ov);
-        if (r < a.H) {
-          if (sg.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.o + head * kRank + half * kHalf + 32 * i);
+        tmem_ld_16x256b_x8_wait(lane_base + 64 * i, ov);
+        const int col = half * kHalf + 64 * i + 2 * t4;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+        for (int ab = 0; ab < 2; ++ab) {
+          const int r = ab ? rB : rA;
+          const float inv = ab ? invB : invA;
+          if (r >= a.H) continue;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = pack_bf16x2(__uint_as_float(ov[8 * k + 2 * j]) * inv,
-                                   __uint_as_float(ov[8 * k + 2 * j + 1]) * inv);
-              dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.part + prow * kHalf + 32 * i);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[k] = make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+          for (int cc = 0; cc < 8; ++cc) {
+            const float x0 = __uint_as_float(ov[4 * cc + 2 * ab]);
+            const float x1 = __uint_as_float(ov[4 * cc + 2 * ab + 1]);
+            if (sg.whole)
+              *reinterpret_cast<uint32_t*>(a.o + (head0 + r) * kRank + col + 8 * cc) =
+                  pack_bf16x2(x0 * inv, x1 * inv);
+            else
+              *reinterpret_cast<float2*>(a.part + (prow0 + r) * kRank + col + 8 * cc) =
+                  make_float2(x0, x1);
           }
         }
       }
       tc_fence_before();
-      if (r < a.H) {
-        if (!sg.whole)
-          a.stat[prow] = make_float2(m_run, l_run);
-        else if (half == 0)
-          a.lse[head] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * kLn2;
+      if (t4 == 0) {
+#pragma unroll
+        for (int ab = 0; ab < 2; ++ab) {
+          const int r = ab ? rB : rA;
+          const float m = ab ? mB : mA, l = ab ? lB : lA;
+          if (r >= a.H) continue;
+          if (!sg.whole)
+            a.stat[(static_cast<size_t>(slot) * 2 + half) * a.H + r] = make_float2(m, l);
+          else if (half == 0)
+            a.lse[head0 + r] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        }
       }
       sg = nx;
-      ++nu;
     }
   }
 
@@ -455,50 +491,98 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
   }
 }
 
-// One block per (b, h), four columns a thread: joins the parts of a sequence that more than
-// one worker had; o = 0, lse = -inf for an empty sequence.
-__global__ void __launch_bounds__(128) latent_combine_kernel(LatentArgs a, int workers) {
+// One block per (b, h): joins the parts of a sequence that more than one worker had; o = 0,
+// lse = -inf for an empty sequence.  Each half of the columns has statistics of its own (its
+// CTAs add the score products in another order): THREADS / 2 threads form a half's weights, and
+// the rows are added by groups of 128 threads (four columns a thread), each part to one group.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) latent_combine_kernel(LatentArgs a, int workers) {
+  constexpr int GROUPS = THREADS / 128, PER = THREADS / 2;
+  __shared__ float weight[2][kMaxWorkers];
+  __shared__ float red[2][THREADS / 32];
+  __shared__ float4 rows[GROUPS][128];
   griddep_wait();
   griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int col = 4 * threadIdx.x, half = col / kHalf;
+  const size_t head = blockIdx.x;
   const long long p0 = a.prefix[b], p1 = a.prefix[b + 1], total = a.prefix[a.B];
+  if (p0 == p1) {
+    if (tid < kRank / 8)
+      reinterpret_cast<uint4*>(a.o + head * kRank)[tid] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) a.lse[head] = -INFINITY;
+    return;
+  }
+  workers = sched::active(total, workers);
+  const int w0 = sched::owner(p0, total, workers);
+  const int parts = sched::owner(p1 - 1, total, workers) - w0 + 1;
+  if (parts == 1) return;   // finished by its CTAs
+  // Only the first part can sit in the second of its worker's slots.
+  const int slot0 = sched::slot(p0, sched::range_start(total, w0, workers), w0);
+  auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
+  const int half = tid / PER, ht = tid - half * PER;
+  auto stat = [&](int i) { return a.stat[(static_cast<size_t>(slot(i)) * 2 + half) * a.H + h]; };
+  float M = -INFINITY;
+  for (int i = ht; i < parts; i += PER) M = fmaxf(M, stat(i).x);
+  M = warp_max(M);
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+  M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER / 32; ++i) M = fmaxf(M, red[0][half * (PER / 32) + i]);
+  if (M == -INFINITY) M = 0.f;
+  float l = 0.f;
+  for (int i = ht; i < parts; i += PER) {
+    const float2 s = stat(i);
+    const float w = ex2(s.x - M);   // a part without a visible key (-inf) weighs 0
+    weight[half][i] = w;
+    l += s.y * w;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  const int g = tid >> 7, col = tid & 127, hc = col >> 6;   // columns 4 col ... of half hc
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float M = -INFINITY, l = 0.f;
-  if (p1 > p0) {
-    workers = sched::active(total, workers);
-    const int w0 = sched::owner(p0, total, workers), w1 = sched::owner(p1 - 1, total, workers);
-    if (w0 == w1) return;   // finished by its CTAs
-    auto row = [&](int w) {
-      const int slot = 2 * sched::slot(p0, sched::range_start(total, w, workers), w) + half;
-      return static_cast<size_t>(slot) * a.H + h;
-    };
-    for (int w = w0; w <= w1; ++w) M = fmaxf(M, a.stat[row(w)].x);
-    if (M == -INFINITY) M = 0.f;
-    for (int w = w0; w <= w1; ++w) {
-      const size_t i = row(w);
-      const float2 s = a.stat[i];
-      const float wt = ex2(s.x - M);   // a part without a visible key (-inf) weighs 0
-      const float4 v = *reinterpret_cast<const float4*>(a.part + i * kHalf + (col & (kHalf - 1)));
-      l += s.y * wt;
-      acc.x = fmaf(wt, v.x, acc.x);
-      acc.y = fmaf(wt, v.y, acc.y);
-      acc.z = fmaf(wt, v.z, acc.z);
-      acc.w = fmaf(wt, v.w, acc.w);
+#pragma unroll 8
+  for (int i = g; i < parts; i += GROUPS) {
+    const float w = weight[hc][i];
+    const float4 v = reinterpret_cast<const float4*>(
+        a.part + (static_cast<size_t>(slot(i)) * a.H + h) * kRank)[col];
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  if constexpr (GROUPS > 1) {
+    rows[g][col] = acc;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+      const float4 v = rows[i][col];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
     }
   }
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER / 32; ++i) l += red[1][hc * (PER / 32) + i];
   const float inv = l == 0.f ? 0.f : 1.f / l;   // a NaN sum stays one
-  const size_t head = blockIdx.x;
-  *reinterpret_cast<uint2*>(a.o + head * kRank + col) =
+  reinterpret_cast<uint2*>(a.o + head * kRank)[col] =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (threadIdx.x == 0) a.lse[head] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
+  if (tid == 0) a.lse[head] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;   // of half 0
 }
 
-int latent_workers() { return sm_count() / 2; }
+int max_workers() { return std::min(sm_count() / 2, kMaxWorkers); }
 
-size_t part_bytes(int H) { return static_cast<size_t>(2 * latent_workers()) * H * kRank * 4; }
+size_t part_bytes(int H) {
+  return 2 * static_cast<size_t>(max_workers()) * H * kRank * sizeof(float);
+}
 size_t stat_bytes(int H) {
-  return round_up(static_cast<size_t>(2 * latent_workers()) * 2 * H * sizeof(float2), 256);
+  return round_up(2 * static_cast<size_t>(max_workers()) * 2 * H * sizeof(float2), 256);
 }
 
 }  // namespace
@@ -532,15 +616,19 @@ cudaError_t launch_latent_decode(const void* q, const void* cache, long long pag
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
-  // No more workers than there can be granules.
+  // No more workers than there can be tiles.
   const long long most = static_cast<long long>(B) *
-                         (((static_cast<long long>(max_pages) << page_shift) + kGranule - 1) / kGranule);
-  const int workers = most < latent_workers() ? static_cast<int>(most) : latent_workers();
+                         (((static_cast<long long>(max_pages) << page_shift) + kKeys - 1) / kKeys);
+  const int workers = static_cast<int>(std::min<long long>(most, max_workers()));
   cudaError_t e = launch_dependent(latent_decode_kernel, dim3(2 * workers), dim3(kThreads), kSmem,
                                    s, mc, mq, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(latent_combine_kernel, dim3(static_cast<unsigned>(B) * H), dim3(128), 0,
-                          s, a, workers);
+  // Few sequences: many parts each.
+  const dim3 grid(static_cast<unsigned>(B) * H);
+  return workers > 8 * B ? launch_dependent(latent_combine_kernel<512>, grid, dim3(512), 0, s, a,
+                                            workers)
+                         : launch_dependent(latent_combine_kernel<128>, grid, dim3(128), 0, s, a,
+                                            workers);
 }
 
 }  // namespace fa

@@ -548,75 +548,82 @@ def fa_grad_finish(out, acc, stream=None) -> None:
 
 # ----------------------------------------------------------- paged cache
 
-def _same_gpu(*ts):
-    """Every tensor lies on the current CUDA device, where the library launches."""
-    here = None
+def _same_gpu(stream, *ts) -> int:
+    """Every tensor lies on the current CUDA device, where the library launches; returns the
+    handle of ``stream`` (None: the device's current stream)."""
+    here = ts[0].get_device()
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("the library takes CUDA tensors (device memory); got a "
-                             f"{t.device.type} tensor")
-        if here is None:
-            here = torch.cuda.current_device()
-        if t.device.index != here:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}: "
-                             "enter torch.cuda.device(...) for it")
+        if t.get_device() != here or here < 0:
+            bad = next((t for t in ts if not t.is_cuda), None)
+            if bad is not None:
+                raise ValueError("the library takes CUDA tensors (device memory); got a "
+                                 f"{bad.device.type} tensor")
+            raise ValueError(f"tensors on {ts[0].device} and {t.device}: one device a call")
+    if here != torch.cuda.current_device():
+        raise ValueError(f"tensors on {ts[0].device}, but the current device is cuda:"
+                         f"{torch.cuda.current_device()}: enter torch.cuda.device(...) for them")
+    if stream is None:
+        # the handle alone: making a Stream object of it takes longer than the launch
+        return torch._C._cuda_getCurrentRawStream(here)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _shaped(name, t, shape, dtype):
-    """``t`` is dense and has the shape (None: any size) and type named."""
+    """``t`` is dense and has the shape and type named."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must be {list(shape)} (None: any size), not {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(name, t, shape, dtype=torch.bfloat16):
     """Elements between the first index's entries of ``t``, whose other dimensions are dense (a
     slice of a larger tensor along them is taken as it is)."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must be {list(shape)} (None: any size), not {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
     dense = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and st != dense:
-            raise ValueError(f"{name} must be dense behind its first dimension")
+    for n in shape[1:]:
         dense *= n
-    return t.stride(0) if t.shape[0] > 1 else dense   # a single entry's stride says nothing
+    if not t.is_contiguous():
+        inner = 1
+        for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+            if n != 1 and st != inner:
+                raise ValueError(f"{name} must be dense behind its first dimension")
+            inner *= n
+        if shape[0] > 1:
+            return t.stride(0)
+    return dense   # a single entry's stride says nothing
 
 
-def _table(block_table, B):
-    if block_table.dtype != torch.int32:
+def _table(t, B):
+    shape = t.shape
+    if t.dtype is not torch.int32:
         raise TypeError("block_table must be torch.int32")
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1:
-        raise ValueError(f"block_table must be [{B}, max_pages], not {list(block_table.shape)}")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    if len(shape) != 2 or shape[0] != B or shape[1] < 1:
+        raise ValueError(f"block_table must be [{B}, max_pages], not {list(shape)}")
+    if t.is_contiguous():
+        return shape[1]
+    if shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("block_table rows must be dense")
-    return block_table.stride(0) if B > 1 else block_table.shape[1]
+    return t.stride(0) if B > 1 else shape[1]   # a single row's stride says nothing
 
 
-class _Helper:
-    """Where an allocating helper runs: its outputs and scratch memory belong to the stream the
-    kernels run on, and inputs made on another stream are kept until that work is done."""
-
-    def __init__(self, stream, *inputs):
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
-        self.ctx = torch.cuda.stream(stream)
-        if stream is not None and stream != torch.cuda.current_stream():
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
-
-    def __enter__(self):
-        self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+def _on_stream(stream, fn, *args, **kw):
+    """An allocating helper on a stream that was named: its outputs and scratch memory belong to
+    that stream, and inputs made on another are kept until its work is done."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream != torch.cuda.current_stream():
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def fa_paged_tables(cache_len, new_len, free_pages, block_table, total_len, token_start, slots,
@@ -626,22 +633,22 @@ def fa_paged_tables(cache_len, new_len, free_pages, block_table, total_len, toke
     cache_len, new_len [B], free_pages [F] in; block_table [B, max_pages] in and out; out:
     total_len [B], token_start [B + 1], slots [T], pages_taken [1].
     """
-    B = cache_len.shape[0] if cache_len.dim() else 0
-    i32 = torch.int32
-    for name, t, n in (("cache_len", cache_len, B), ("new_len", new_len, B),
-                       ("free_pages", free_pages, None), ("total_len", total_len, B),
-                       ("token_start", token_start, B + 1), ("slots", slots, None),
-                       ("pages_taken", pages_taken, 1)):
-        _shaped(name, t, (n,), i32)
+    B, i32 = cache_len.numel(), torch.int32
+    F, T = free_pages.numel(), slots.numel()
+    _shaped("cache_len", cache_len, (B,), i32)
+    _shaped("new_len", new_len, (B,), i32)
+    _shaped("free_pages", free_pages, (F,), i32)
+    _shaped("total_len", total_len, (B,), i32)
+    _shaped("token_start", token_start, (B + 1,), i32)
+    _shaped("slots", slots, (T,), i32)
+    _shaped("pages_taken", pages_taken, (1,), i32)
     stride = _table(block_table, B)
-    _same_gpu(cache_len, new_len, free_pages, block_table, total_len, token_start, slots,
-              pages_taken)
+    handle = _same_gpu(stream, cache_len, new_len, free_pages, block_table, total_len,
+                       token_start, slots, pages_taken)
     st = load().fa_paged_tables(cache_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
-                                free_pages.numel(), block_table.data_ptr(), stride,
-                                block_table.shape[1], total_len.data_ptr(),
-                                token_start.data_ptr(), slots.data_ptr(), slots.numel(),
-                                pages_taken.data_ptr(), B, int(page_size), int(num_pages),
-                                _stream(stream))
+                                F, block_table.data_ptr(), stride, block_table.shape[1],
+                                total_len.data_ptr(), token_start.data_ptr(), slots.data_ptr(), T,
+                                pages_taken.data_ptr(), B, page_size, num_pages, handle)
     if st != FA_OK:
         raise FaError(st, "fa_paged_tables")
 
@@ -653,32 +660,34 @@ def paged_tables(cache_len, new_len, free_pages, block_table, page_size: int, nu
     Returns (total_len, token_start, slots, pages_taken); ``num_slots`` rows of slots, those
     behind the last new token -1.
     """
-    B = cache_len.shape[0]
-    with _Helper(stream, cache_len, new_len, free_pages, block_table):
-        n = int(num_slots)
-        buf = torch.empty(2 * B + 2 + n, dtype=torch.int32, device=cache_len.device)
-        total, start = buf[:B], buf[B:2 * B + 1]
-        taken, slots = buf[2 * B + 1:2 * B + 2], buf[2 * B + 2:]
-        fa_paged_tables(cache_len, new_len, free_pages, block_table, total, start, slots, taken,
-                        page_size, num_pages)
+    if stream is not None:
+        return _on_stream(stream, paged_tables, cache_len, new_len, free_pages, block_table,
+                          page_size, num_pages, num_slots)
+    B = cache_len.numel()
+    buf = torch.empty(2 * B + 2 + num_slots, dtype=torch.int32, device=cache_len.device)
+    total, start, taken, slots = buf.split((B, B + 1, 1, num_slots))
+    fa_paged_tables(cache_len, new_len, free_pages, block_table, total, start, slots, taken,
+                    page_size, num_pages)
     return total, start, slots, taken
 
 
 def fa_paged_append(k, v, k_cache, v_cache, slots, stream=None) -> None:
     """Rows k, v [T, Hkv, d] (bf16, any stride between tokens) into slots [T] (int32) of the pools
     k_cache, v_cache [num_pages, Hkv, page_size, d] (equal strides)."""
-    T, Hkv, d = k.shape
-    P, page = k_cache.shape[0], k_cache.shape[2] if k_cache.dim() == 4 else 0
-    ks, vs = _rows("k", k, (T, Hkv, d)), _rows("v", v, (T, Hkv, d))
-    kp, vp = (_rows(n, c, (P, Hkv, page, d)) for n, c in (("k_cache", k_cache),
-                                                          ("v_cache", v_cache)))
-    if kp != vp:
+    rows, pool = k.shape, k_cache.shape
+    if len(rows) != 3 or len(pool) != 4 or pool[1] != rows[1] or pool[3] != rows[2]:
+        raise ValueError("k must be [T, Hkv, d] and k_cache [num_pages, Hkv, page_size, d]; got "
+                         f"{list(rows)} and {list(pool)}")
+    T, Hkv, d = rows
+    ks, vs = _rows("k", k, rows), _rows("v", v, rows)
+    kp = _rows("k_cache", k_cache, pool)
+    if kp != _rows("v_cache", v_cache, pool):
         raise ValueError("k_cache and v_cache must have the same stride between pages")
     _shaped("slots", slots, (T,), torch.int32)
-    _same_gpu(k, v, k_cache, v_cache, slots)
+    handle = _same_gpu(stream, k, v, k_cache, v_cache, slots)
     st = load().fa_paged_append(k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(),
-                                v_cache.data_ptr(), kp, slots.data_ptr(), T, P, Hkv, page, d,
-                                _stream(stream))
+                                v_cache.data_ptr(), kp, slots.data_ptr(), T, pool[0], Hkv,
+                                pool[2], d, handle)
     if st != FA_OK:
         raise FaError(st, "fa_paged_append")
 
@@ -701,37 +710,39 @@ def fa_decode_paged(q, k, v, block_table, cache_len, o, lse, workspace, scale=No
                     stream=None) -> None:
     """q [B, Hq, d] over the pools k, v [num_pages, Hkv, page_size, d] (bf16) through block_table
     [B, max_pages] and cache_len [B] (int32); o [B, Hq, d] bf16 and lse [B, Hq] fp32 out."""
-    bf16 = torch.bfloat16
-    _shaped("q", q, (None, None, None), bf16)
-    B, Hq, d = q.shape
-    kp, vp = (_rows(n, c, (None, None, None, d)) for n, c in (("k", k), ("v", v)))
-    if kp != vp or k.shape != v.shape:
-        raise ValueError("k and v must have the same shape and stride between pages")
-    P, Hkv, page, _ = k.shape
+    heads, pool = q.shape, k.shape
+    if len(heads) != 3 or len(pool) != 4 or pool[3] != heads[2]:
+        raise ValueError("q must be [B, Hq, d] and k [num_pages, Hkv, page_size, d]; got "
+                         f"{list(heads)} and {list(pool)}")
+    B, Hq, d = heads
+    P, Hkv, page, _ = pool
+    _shaped("q", q, heads, torch.bfloat16)
+    kp = _rows("k", k, pool)
+    if kp != _rows("v", v, pool):
+        raise ValueError("k and v must have the same stride between pages")
     stride = _table(block_table, B)
     _shaped("cache_len", cache_len, (B,), torch.int32)
-    _shaped("o", o, (B, Hq, d), bf16)
+    _shaped("o", o, heads, torch.bfloat16)
     _shaped("lse", lse, (B, Hq), torch.float32)
-    _same_gpu(q, k, v, block_table, cache_len, o, lse, workspace)
-    scale = 1.0 / d ** 0.5 if scale is None else float(scale)
+    handle = _same_gpu(stream, q, k, v, block_table, cache_len, o, lse, workspace)
     st = load().fa_decode_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), kp,
                                 block_table.data_ptr(), stride, block_table.shape[1],
                                 cache_len.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, P,
-                                page, d, scale, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream(stream))
+                                page, d, 1.0 / d ** 0.5 if scale is None else scale,
+                                workspace.data_ptr(), workspace.nbytes, handle)
     if st != FA_OK:
         raise FaError(st, "fa_decode_paged")
 
 
 def decode_paged(q, k, v, block_table, cache_len, scale=None, workspace=None, stream=None):
     """Allocate o, lse (and the workspace unless given) and run fa_decode_paged."""
-    B, Hq, d = q.shape
-    with _Helper(stream, q, k, v, block_table, cache_len, workspace):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = alloc_decode_paged_workspace(B, Hq, k.shape[1], d, q.device)
-        fa_decode_paged(q, k, v, block_table, cache_len, o, lse, workspace, scale)
+    if stream is not None:
+        return _on_stream(stream, decode_paged, q, k, v, block_table, cache_len, scale, workspace)
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = alloc_decode_paged_workspace(*q.shape[:2], k.shape[1], q.shape[2], q.device)
+    fa_decode_paged(q, k, v, block_table, cache_len, o, lse, workspace, scale)
     return o, lse
 
 
@@ -741,14 +752,22 @@ def _latent_shapes(q, k_nope, k_rope, v, kv_len):
     if q.dim() != 4:
         raise ValueError(f"q must be [B, H, N, {LATENT_QK}], not {list(q.shape)}")
     B, H, N, _ = q.shape
-    dt = q.dtype
+    code, dt = _dtype_code(q), q.dtype
     _shaped("q", q, (B, H, N, LATENT_QK), dt)
     _shaped("k_nope", k_nope, (B, H, N, LATENT_NOPE), dt)
     _shaped("k_rope", k_rope, (B, N, LATENT_ROPE), dt)
     _shaped("v", v, (B, H, N, LATENT_V), dt)
     if kv_len is not None:
         _shaped("kv_len", kv_len, (B,), torch.int32)
-    return B, H, N, _dtype_code(q)
+    return B, H, N, code
+
+
+def _given(*ts):
+    return (t for t in ts if t is not None)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def fa_latent_fwd(q, k_nope, k_rope, v, o, o_acc, lse, causal: bool = False, kv_len=None,
@@ -761,11 +780,11 @@ def fa_latent_fwd(q, k_nope, k_rope, v, o, o_acc, lse, causal: bool = False, kv_
     if o_acc is not None:
         _shaped("o_acc", o_acc, (B, H, N, LATENT_V), torch.float32)
     _shaped("lse", lse, (B, H, N), torch.float32)
-    _same_gpu(q, k_nope, k_rope, v, o, o_acc, lse, kv_len)
-    scale = 1.0 / LATENT_QK ** 0.5 if scale is None else float(scale)
-    st = load().fa_latent_fwd(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(o_acc),
-                              _ptr(lse), B, H, N, int(causal), _ptr(kv_len), scale, code,
-                              _stream(stream))
+    handle = _same_gpu(stream, *_given(q, k_nope, k_rope, v, o, o_acc, lse, kv_len))
+    st = load().fa_latent_fwd(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
+                              o.data_ptr(), _at(o_acc), lse.data_ptr(), B, H, N, int(causal),
+                              _at(kv_len), 1.0 / LATENT_QK ** 0.5 if scale is None else scale,
+                              code, handle)
     if st != FA_OK:
         raise FaError(st, "fa_latent_fwd")
 
@@ -773,14 +792,14 @@ def fa_latent_fwd(q, k_nope, k_rope, v, o, o_acc, lse, causal: bool = False, kv_
 def latent_forward(q, k_nope, k_rope, v, causal: bool = False, kv_len=None, scale=None,
                    need_grad: bool = False, stream=None):
     """Allocate and run fa_latent_fwd.  Returns (o, lse), with ``need_grad`` (o, lse, o_acc)."""
-    B, H, N, _ = q.shape
-    with _Helper(stream, q, k_nope, k_rope, v, kv_len):
-        o = torch.empty_like(v)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-        o_acc = None
-        if need_grad and q.dtype != torch.float32:
-            o_acc = torch.empty(v.shape, dtype=torch.float32, device=q.device)
-        fa_latent_fwd(q, k_nope, k_rope, v, o, o_acc, lse, causal, kv_len, scale)
+    if stream is not None:
+        return _on_stream(stream, latent_forward, q, k_nope, k_rope, v, causal, kv_len, scale,
+                          need_grad)
+    o, o_acc = torch.empty_like(v), None
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    if need_grad and q.dtype != torch.float32:
+        o_acc = torch.empty(v.shape, dtype=torch.float32, device=q.device)
+    fa_latent_fwd(q, k_nope, k_rope, v, o, o_acc, lse, causal, kv_len, scale)
     if not need_grad:
         return o, lse
     return o, lse, o if o_acc is None else o_acc   # fp32: o is its own unrounded form
@@ -807,13 +826,15 @@ def fa_latent_bwd(q, k_nope, k_rope, v, o_acc, lse, do, dq, dk_nope, dk_rope, dv
     _shaped("lse", lse, (B, H, N), torch.float32)
     for name, t, like in (("do", do, v), ("dq", dq, q), ("dk_nope", dk_nope, k_nope),
                           ("dk_rope", dk_rope, k_rope), ("dv", dv, v)):
-        _shaped(name, t, tuple(like.shape), q.dtype)
-    _same_gpu(q, k_nope, k_rope, v, o_acc, lse, do, dq, dk_nope, dk_rope, dv, workspace, kv_len)
-    scale = 1.0 / LATENT_QK ** 0.5 if scale is None else float(scale)
-    st = load().fa_latent_bwd(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o_acc), _ptr(lse),
-                              _ptr(do), _ptr(dq), _ptr(dk_nope), _ptr(dk_rope), _ptr(dv), B, H, N,
-                              int(causal), _ptr(kv_len), scale, code, _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
+        _shaped(name, t, like.shape, q.dtype)
+    handle = _same_gpu(stream, *_given(q, k_nope, k_rope, v, o_acc, lse, do, dq, dk_nope, dk_rope,
+                                       dv, workspace, kv_len))
+    st = load().fa_latent_bwd(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
+                              o_acc.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+                              dk_nope.data_ptr(), dk_rope.data_ptr(), dv.data_ptr(), B, H, N,
+                              int(causal), _at(kv_len),
+                              1.0 / LATENT_QK ** 0.5 if scale is None else scale, code,
+                              workspace.data_ptr(), workspace.nbytes, handle)
     if st != FA_OK:
         raise FaError(st, "fa_latent_bwd")
 
@@ -822,27 +843,33 @@ def latent_backward(q, k_nope, k_rope, v, o_acc, lse, do, causal: bool = False, 
                     scale=None, workspace=None, stream=None):
     """Allocate the gradients (and the workspace unless given) and run fa_latent_bwd.
     Returns (dq, dk_nope, dk_rope, dv)."""
-    B, H, N, _ = q.shape
-    with _Helper(stream, q, k_nope, k_rope, v, o_acc, lse, do, kv_len, workspace):
-        dq, dkn, dkr, dv = (torch.empty_like(t) for t in (q, k_nope, k_rope, v))
-        if workspace is None:
-            workspace = alloc_latent_workspace(B, H, N, q.device)
-        fa_latent_bwd(q, k_nope, k_rope, v, o_acc, lse, do, dq, dkn, dkr, dv, workspace, causal,
-                      kv_len, scale)
+    if stream is not None:
+        return _on_stream(stream, latent_backward, q, k_nope, k_rope, v, o_acc, lse, do, causal,
+                          kv_len, scale, workspace)
+    dq, dkn, dkr, dv = (torch.empty_like(t) for t in (q, k_nope, k_rope, v))
+    if workspace is None:
+        workspace = alloc_latent_workspace(*q.shape[:3], q.device)
+    fa_latent_bwd(q, k_nope, k_rope, v, o_acc, lse, do, dq, dkn, dkr, dv, workspace, causal,
+                  kv_len, scale)
     return dq, dkn, dkr, dv
+
+
+def _latent_pool(cache):
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] != LATENT_ROW:
+        raise ValueError(f"cache must be [num_pages, page_size, {LATENT_ROW}], not {list(shape)}")
+    return _rows("cache", cache, shape)
 
 
 def fa_latent_append(c, k_rope, cache, slots, stream=None) -> None:
     """Latent rows c [T, 512] and k_rope [T, 64] (bf16, any stride between tokens) into slots [T]
     (int32) of the pool cache [num_pages, page_size, 576]."""
-    T = c.shape[0]
+    T, ps = slots.numel(), _latent_pool(cache)
     cs, rs = _rows("c", c, (T, LATENT_RANK)), _rows("k_rope", k_rope, (T, LATENT_ROPE))
-    ps = _rows("cache", cache, (None, None, LATENT_ROW))
     _shaped("slots", slots, (T,), torch.int32)
-    _same_gpu(c, k_rope, cache, slots)
+    handle = _same_gpu(stream, c, k_rope, cache, slots)
     st = load().fa_latent_append(c.data_ptr(), k_rope.data_ptr(), cs, rs, cache.data_ptr(), ps,
-                                 slots.data_ptr(), T, cache.shape[0], cache.shape[1],
-                                 _stream(stream))
+                                 slots.data_ptr(), T, cache.shape[0], cache.shape[1], handle)
     if st != FA_OK:
         raise FaError(st, "fa_latent_append")
 
@@ -866,32 +893,33 @@ def fa_latent_decode(q, cache, block_table, cache_len, o, lse, workspace, scale=
     """Absorbed latent decode: q [B, H, 576] over the pool cache [num_pages, page_size, 576]
     (bf16) through block_table [B, max_pages] and cache_len [B] (int32); o [B, H, 512] bf16 and
     lse [B, H] fp32 out."""
-    bf16 = torch.bfloat16
-    _shaped("q", q, (None, None, LATENT_ROW), bf16)
+    if q.dim() != 3 or q.shape[2] != LATENT_ROW:
+        raise ValueError(f"q must be [B, H, {LATENT_ROW}], not {list(q.shape)}")
     B, H, _ = q.shape
-    ps = _rows("cache", cache, (None, None, LATENT_ROW))
-    stride = _table(block_table, B)
+    _shaped("q", q, q.shape, torch.bfloat16)
+    ps, stride = _latent_pool(cache), _table(block_table, B)
     _shaped("cache_len", cache_len, (B,), torch.int32)
-    _shaped("o", o, (B, H, LATENT_RANK), bf16)
+    _shaped("o", o, (B, H, LATENT_RANK), torch.bfloat16)
     _shaped("lse", lse, (B, H), torch.float32)
-    _same_gpu(q, cache, block_table, cache_len, o, lse, workspace)
-    scale = 1.0 / LATENT_QK ** 0.5 if scale is None else float(scale)
+    handle = _same_gpu(stream, q, cache, block_table, cache_len, o, lse, workspace)
     st = load().fa_latent_decode(q.data_ptr(), cache.data_ptr(), ps, block_table.data_ptr(), stride,
                                  block_table.shape[1], cache_len.data_ptr(), o.data_ptr(),
-                                 lse.data_ptr(), B, H, cache.shape[0], cache.shape[1], scale,
-                                 workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(stream))
+                                 lse.data_ptr(), B, H, cache.shape[0], cache.shape[1],
+                                 1.0 / LATENT_QK ** 0.5 if scale is None else scale,
+                                 workspace.data_ptr(), workspace.nbytes, handle)
     if st != FA_OK:
         raise FaError(st, "fa_latent_decode")
 
 
 def latent_decode(q, cache, block_table, cache_len, scale=None, workspace=None, stream=None):
     """Allocate o, lse (and the workspace unless given) and run fa_latent_decode."""
-    B, H, _ = q.shape
-    with _Helper(stream, q, cache, block_table, cache_len, workspace):
-        o = torch.empty((B, H, LATENT_RANK), dtype=q.dtype, device=q.device)
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = alloc_latent_decode_workspace(B, H, q.device)
-        fa_latent_decode(q, cache, block_table, cache_len, o, lse, workspace, scale)
+    if stream is not None:
+        return _on_stream(stream, latent_decode, q, cache, block_table, cache_len, scale,
+                          workspace)
+    B, H = q.shape[:2]
+    o = torch.empty((B, H, LATENT_RANK), dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = alloc_latent_decode_workspace(B, H, q.device)
+    fa_latent_decode(q, cache, block_table, cache_len, o, lse, workspace, scale)
     return o, lse
