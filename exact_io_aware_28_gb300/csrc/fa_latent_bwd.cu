@@ -2,27 +2,29 @@
 // accumulation.  The formulas stand in fa_latent_simt.cu.
 //
 // Two kernels of one template, without atomics (the result does not depend on scheduling):
-//   dK, dV  a CTA owns 128 keys of a head (k, v stay in shared memory) and streams the query
-//           blocks of 64 rows that may see them:
+//   dK, dV  a CTA owns 128 keys of a head (k, v stay in shared memory) and streams the blocks of
+//           128 query rows that may see them:
 //             S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;
-//   dQ      a CTA owns 128 query rows (q, dO stay) and streams key blocks of 64:
+//   dQ      a CTA owns 128 query rows (q, dO stay) and streams key blocks of 128:
 //             S = Q K^T, dP = dO V^T, dQ += dS K.
 // Seven products instead of five (S and dP are formed twice: 1152 columns of MMA a pair against
 // 832), because dK (192) + dV (128) + dQ (192) and two score tiles do not fit tensor memory's 512
 // columns, and dQ needs no fp32 sums through global memory this way.
 //
-// What bounds it: the score products, whose N = 64 makes shared memory feed 6 KB an MMA of 32
-// cycles' work (48 cycles at 128 B a cycle), about 1600 + 1344 cycles a 128 x 64 block.
-//
-// Both score operands of the streamed side come from one stage: X (192 columns: q or k) and Y
-// (128: dO or v) lie as [64 rows][64 columns] subtiles that the score products read K-major and
-// the gradient products MN-major.  Tensor memory: the accumulators, then regions of 64 columns
-// for S and dP, whose rows P and dS overwrite as bf16 (the A operand of the gradient products).
-// dK, dV has three regions: S(n) sits in region 2n mod 3 and dP(n) in 2n + 1 mod 3, so S(n + 1)
-// starts while block n is in the softmax and dP(n + 1) takes the region that P(n) leaves after
-// its product.  dQ has four.
+// What bounds it: the one thread that issues, and the pipe behind it.  An MMA costs 65 to 90
+// cycles whether N is 64 or 128, so the blocks are 128 wide although tensor memory then holds one
+// score tile at a time (64-wide blocks, two in flight, measured 3.2k + 2.6k cycles a 128 x 64
+// block against NEWKV + NEWDQ a 128 x 128 block).
+//   dK, dV  columns: dV 128, dK 192, one region of 128 for S^T, then dP^T (once the softmax warps
+//           have S^T in registers), then dS^T in place; 64 for P^T.
+//   dQ      columns: dQ 192, S 128, dP 128, dS 64: S(n + 1) and dP(n + 1) start as soon as the
+//           softmax warps have read S(n) and dP(n).
+// Of shared memory the owned rows hold 80 KB; the streamed side X (q or k, 192 columns: scores
+// early, gradient product late) has two stages of 48 KB and Y (dO or v, 128) one of 32.  Both
+// lie as [128 rows][64 columns] subtiles that the score products read K-major and the gradient
+// products MN-major.
 //   warp 0 producer; warp 1 MMA issuer; warp 2 tensor memory and (dK, dV) the block's lse and
-//   D; warps 4-11 softmax, two threads a row, 32 columns each.
+//   D; warps 4-11 softmax, two threads a row, 64 columns each.
 // Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and exits.
 #include <atomic>
 
@@ -37,26 +39,27 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kRows = 128;              // rows a CTA owns
-constexpr int kCols = 64;               // rows of a streamed block
+constexpr int kRows = 128;              // rows a CTA owns, rows of a streamed block
 constexpr int kXSubs = (FA_LATENT_NOPE + FA_LATENT_ROPE) / 64, kYSubs = FA_LATENT_V / 64;
 constexpr int kQK = FA_LATENT_NOPE + FA_LATENT_ROPE, kV = FA_LATENT_V;
-constexpr int kFSub = kRows * 128;      // [128 rows][64] subtile of the owned side, 16 KB
-constexpr int kSSub = kCols * 128;      // [64 rows][64] subtile of the streamed side, 8 KB
-constexpr int kFixed = (kXSubs + kYSubs) * kFSub;
-constexpr int kStage = (kXSubs + kYSubs) * kSSub;
-constexpr int kStages = 3;
+constexpr int kSub = kRows * 128;       // [128 rows][64] subtile, 16 KB
+constexpr int kX = kXSubs * kSub, kY = kYSubs * kSub;
+constexpr int kXStages = 2;
 constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Bars {
   uint64_t fixed_full;
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
-  uint64_t s_full[2];
-  uint64_t dp_full[2];
-  uint64_t p_ready[2];
-  uint64_t ds_ready[2];
+  uint64_t x_full[kXStages];
+  uint64_t x_empty[kXStages];  // the block's last product has completed
+  uint64_t y_full;
+  uint64_t y_empty;
+  uint64_t s_full;
+  uint64_t s_read;             // the softmax warps have the scores in registers
+  uint64_t dp_full;
+  uint64_t p_ready;
+  uint64_t ds_ready;
+  uint64_t grad_done;          // dQ's product of the block has completed
   uint64_t acc_full;
   uint64_t drain;
   uint32_t tmem_base;
@@ -65,12 +68,12 @@ struct Bars {
 };
 
 struct Stats {                          // of a streamed query block (dK, dV)
-  float lse2[kCols];                    // lse log2 e; +inf for rows that see no key or none are
-  float D[kCols];
+  float lse2[kRows];                    // lse log2 e; +inf for rows that see no key or none are
+  float D[kRows];
 };
 
-constexpr int kSmem = 1024 + kFixed + kStages * kStage +
-                      kStages * static_cast<int>(sizeof(Stats)) + static_cast<int>(sizeof(Bars));
+constexpr int kSmem = 1024 + kX + kY + kXStages * kX + kY +
+                      kXStages * static_cast<int>(sizeof(Stats)) + static_cast<int>(sizeof(Bars));
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct BwdArgs {
@@ -88,21 +91,25 @@ __device__ __forceinline__ float exponent_of(float lse) {
 }
 
 // DQ = false: X = q, Y = dO streamed, k and v owned.  DQ = true: k, v streamed, q and dO owned.
-// Maps: boxes of 128 rows on the owned side, of 64 on the streamed side.
 template <bool DQ>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkn,
                   const __grid_constant__ CUtensorMap mkr, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ CUtensorMap mdo, BwdArgs a, LatentProblem p) {
   constexpr uint32_t kAccX = DQ ? 0 : kV;            // columns of dQ or dK (dV sits before dK)
-  constexpr uint32_t kRegions = kAccX + kQK;         // first column of the S and dP regions
+  constexpr uint32_t kS = kAccX + kQK;               // the scores
+  constexpr uint32_t kDP = DQ ? kS + 128 : kS;       // dP
+  constexpr uint32_t kDS = DQ ? kDP + 128 : kDP;     // dS as bf16, 64 rows' pairs ...
+  constexpr uint32_t kDSHalf = DQ ? 32 : 64;         // ... this many columns apart
+  constexpr uint32_t kP = kS + 128;                  // dK, dV: P^T as bf16
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sF = base;                                // owned rows: X subtiles, Y subtiles
-  uint8_t* sS = sF + kFixed;                         // [kStages] X subtiles, Y subtiles
-  Stats* stats = reinterpret_cast<Stats*>(sS + kStages * kStage);
-  Bars* bars = reinterpret_cast<Bars*>(stats + kStages);
+  uint8_t* sX = sF + kX + kY;                        // [kXStages]
+  uint8_t* sY = sX + kXStages * kX;
+  Stats* stats = reinterpret_cast<Stats*>(sY + kY);
+  Bars* bars = reinterpret_cast<Bars*>(stats + kXStages);
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -123,16 +130,18 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
 
   if (tid == 0) {
     mbar_init(&bars->fixed_full, 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->full[s], DQ ? 1 : 33);
-      mbar_init(&bars->empty[s], 1);
+    for (int s = 0; s < kXStages; ++s) {
+      mbar_init(&bars->x_full[s], DQ ? 1 : 33);
+      mbar_init(&bars->x_empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->dp_full[i], 1);
-      mbar_init(&bars->p_ready[i], 256);
-      mbar_init(&bars->ds_ready[i], 256);
-    }
+    mbar_init(&bars->y_full, 1);
+    mbar_init(&bars->y_empty, 1);
+    mbar_init(&bars->s_full, 1);
+    mbar_init(&bars->s_read, 256);
+    mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->p_ready, 256);
+    mbar_init(&bars->ds_ready, 256);
+    mbar_init(&bars->grad_done, 1);
     mbar_init(&bars->acc_full, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -154,111 +163,130 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     L = p.kv_len[seq];
     L = L < 0 ? 0 : (L > p.N ? p.N : L);
   }
-  // The streamed rows [begin, end) in blocks of 64.
+  // The streamed rows [begin, end) in blocks of 128.
   const int begin = !DQ && p.causal ? row0 : 0;
   const int end = DQ ? (p.causal ? min(L, row0 + kRows) : L) : (row0 < L ? p.N : begin);
-  const int blocks = end > begin ? (end - begin + kCols - 1) / kCols : 0;
+  const int blocks = end > begin ? (end - begin + kRows - 1) / kRows : 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && blocks > 0) {
-      const auto load = [&](uint8_t* dst, int sub, uint64_t* bar, int row, bool keys) {
+      const auto load_x = [&](uint8_t* dst, uint64_t* bar, int row, bool keys) {
         if (keys) {
           tma_load_3d(dst, &mkn, bar, 0, row, bh);
-          tma_load_3d(dst + sub, &mkn, bar, 64, row, bh);
-          tma_load_3d(dst + 2 * sub, &mkr, bar, 0, row, seq);
-          tma_load_3d(dst + 3 * sub, &mv, bar, 0, row, bh);
-          tma_load_3d(dst + 4 * sub, &mv, bar, 64, row, bh);
+          tma_load_3d(dst + kSub, &mkn, bar, 64, row, bh);
+          tma_load_3d(dst + 2 * kSub, &mkr, bar, 0, row, seq);
         } else {
-          tma_load_3d(dst, &mq, bar, 0, row, bh);
-          tma_load_3d(dst + sub, &mq, bar, 64, row, bh);
-          tma_load_3d(dst + 2 * sub, &mq, bar, 128, row, bh);
-          tma_load_3d(dst + 3 * sub, &mdo, bar, 0, row, bh);
-          tma_load_3d(dst + 4 * sub, &mdo, bar, 64, row, bh);
+          for (int s = 0; s < kXSubs; ++s) tma_load_3d(dst + s * kSub, &mq, bar, 64 * s, row, bh);
         }
       };
-      mbar_arrive_expect_tx(&bars->fixed_full, kFixed);
-      load(sF, kFSub, &bars->fixed_full, row0, !DQ);
+      const auto load_y = [&](uint8_t* dst, uint64_t* bar, int row, bool keys) {
+        for (int s = 0; s < kYSubs; ++s)
+          tma_load_3d(dst + s * kSub, keys ? &mv : &mdo, bar, 64 * s, row, bh);
+      };
+      mbar_arrive_expect_tx(&bars->fixed_full, kX + kY);
+      load_x(sF, &bars->fixed_full, row0, !DQ);
+      load_y(sF + kX, &bars->fixed_full, row0, !DQ);
       for (int n = 0; n < blocks; ++n) {
-        const int st = n % kStages;
-        if (!mbar_wait(&bars->empty[st], ((n / kStages) & 1) ^ 1, abort_flag, p.err, p.wait_ns))
+        const int st = n % kXStages, row = begin + n * kRows;
+        if (!mbar_wait(&bars->x_empty[st], ((n / kXStages) & 1) ^ 1, abort_flag, p.err, p.wait_ns))
           break;
-        mbar_arrive_expect_tx(&bars->full[st], kStage);
-        load(sS + st * kStage, kSSub, &bars->full[st], begin + n * kCols, DQ);
+        mbar_arrive_expect_tx(&bars->x_full[st], kX);
+        load_x(sX + st * kX, &bars->x_full[st], row, DQ);
+        if (!mbar_wait(&bars->y_empty, (n & 1) ^ 1, abort_flag, p.err, p.wait_ns)) break;
+        mbar_arrive_expect_tx(&bars->y_full, kY);
+        load_y(sY, &bars->y_full, row, DQ);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16(kRows, kCols, false, false);
+      constexpr uint32_t idS = idesc_bf16(kRows, kRows, false, false);
       constexpr uint32_t idX = idesc_bf16(kRows, kQK, false, true);
       constexpr uint32_t idV = idesc_bf16(kRows, kV, false, true);
       const uint64_t dF = sw128_desc(smem_u32(sF), 16, 1024);
-      const uint64_t dSk = sw128_desc(smem_u32(sS), 16, 1024);     // streamed, K-major
-      const uint64_t dSm = sw128_desc(smem_u32(sS), kSSub, 1024);  // streamed, MN-major
-      auto s_col = [&](int n) { return tb + kRegions + 64 * (DQ ? (n & 1) : (2 * n) % 3); };
-      auto dp_col = [&](int n) { return tb + kRegions + 64 * (DQ ? 2 + (n & 1) : (2 * n + 1) % 3); };
-      // Score product over subtiles [s0, s1) of both sides.
-      auto scores = [&](uint32_t d, int st, int s0, int s1) {
+      const uint64_t dXk = sw128_desc(smem_u32(sX), 16, 1024);      // streamed, K-major
+      const uint64_t dYk = sw128_desc(smem_u32(sY), 16, 1024);
+      const uint64_t dXm = sw128_desc(smem_u32(sX), kSub, 1024);    // streamed, MN-major
+      const uint64_t dYm = sw128_desc(smem_u32(sY), kSub, 1024);
+      // Score product over `subs` subtiles from descriptors a0 and b0 on.
+      auto scores = [&](uint32_t d, uint64_t a0, uint64_t b0, int subs) {
 #pragma unroll
-        for (int g = s0; g < s1; ++g) {
+        for (int g = 0; g < subs; ++g) {
           uint64_t da[4], db[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            da[k] = dF + static_cast<uint64_t>((g * kFSub + k * 32) >> 4);
-            db[k] = dSk + static_cast<uint64_t>((st * kStage + g * kSSub + k * 32) >> 4);
+            da[k] = a0 + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
+            db[k] = b0 + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
           }
-          mma_ss_x4(d, da, db, idS, g > s0 ? 1u : 0u);
+          mma_ss_x4(d, da, db, idS, g > 0 ? 1u : 0u);
         }
       };
-      // Gradient product: A from the bf16 pairs in region `t` (32 rows of the block in its
-      // columns 0-15, 32 in 32-47), B the stage's subtiles from `sub` on, along the rows.
-      auto grads = [&](uint32_t d, uint32_t t, int st, int sub, uint32_t id, bool acc) {
-        uint32_t ta[4];
-        uint64_t db[4];
+      // Gradient product: A from the bf16 pairs at `t` (64 rows of the block each `half` columns),
+      // B the stage's subtiles along the rows.
+      auto grads = [&](uint32_t d, uint32_t t, uint32_t half, uint64_t b0, uint32_t id, bool acc) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          ta[k] = t + 32 * (k >> 1) + 8 * (k & 1);
-          db[k] = dSm + static_cast<uint64_t>((st * kStage + sub * kSSub + 2048 * k) >> 4);
+        for (int g = 0; g < 2; ++g) {
+          uint32_t ta[4];
+          uint64_t db[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            ta[k] = t + g * half + 8 * k;
+            db[k] = b0 + static_cast<uint64_t>((2048 * (4 * g + k)) >> 4);
+          }
+          mma_ts_x4(d, ta, db, id, (acc || g > 0) ? 1u : 0u);
         }
-        mma_ts_x4(d, ta, db, id, acc ? 1u : 0u);
       };
       auto start_s = [&](int n) -> bool {
-        const int st = n % kStages;
-        if (!mbar_wait(&bars->full[st], (n / kStages) & 1, abort_flag, p.err, p.wait_ns))
+        const int st = n % kXStages;
+        if (!mbar_wait(&bars->x_full[st], (n / kXStages) & 1, abort_flag, p.err, p.wait_ns))
           return false;
         tc_fence_after();
-        scores(s_col(n), st, 0, kXSubs);
-        mma_commit(&bars->s_full[n & 1]);
+        scores(tb + kS, dF, dXk + static_cast<uint64_t>((st * kX) >> 4), kXSubs);
+        mma_commit(&bars->s_full);
         return true;
       };
-      auto start_dp = [&](int n) {
-        scores(dp_col(n), n % kStages, kXSubs, kXSubs + kYSubs);
-        mma_commit(&bars->dp_full[n & 1]);
+      auto start_dp = [&](int n) -> bool {
+        if (!mbar_wait(&bars->y_full, n & 1, abort_flag, p.err, p.wait_ns)) return false;
+        tc_fence_after();
+        scores(tb + kDP, dF + (kX >> 4), dYk, kYSubs);
+        mma_commit(&bars->dp_full);
+        if (DQ) mma_commit(&bars->y_empty);
+        return true;
+      };
+      auto wait = [&](uint64_t* bar, int n) -> bool {
+        if (!mbar_wait(bar, n & 1, abort_flag, p.err, p.wait_ns)) return false;
+        tc_fence_after();
+        return true;
       };
       bool ok = blocks > 0;
       if (ok) ok = mbar_wait(&bars->fixed_full, 0, abort_flag, p.err, p.wait_ns);
       if (ok) ok = start_s(0);
-      if (ok) start_dp(0);
+      if (ok && DQ) ok = start_dp(0);
       for (int n = 0; ok && n < blocks; ++n) {
-        const int st = n % kStages;
-        if (n + 1 < blocks) {
-          ok = start_s(n + 1);
-          if (!ok) break;
-          if (DQ) start_dp(n + 1);
-        }
-        if (!DQ) {
-          ok = mbar_wait(&bars->p_ready[n & 1], (n >> 1) & 1, abort_flag, p.err, p.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
-          grads(tb, s_col(n), st, kXSubs, idV, n > 0);
-          if (n + 1 < blocks) start_dp(n + 1);
-        }
-        ok = mbar_wait(&bars->ds_ready[n & 1], (n >> 1) & 1, abort_flag, p.err, p.wait_ns);
+        const int st = n % kXStages;
+        const uint64_t dXs = dXm + static_cast<uint64_t>((st * kX) >> 4);
+        ok = wait(&bars->s_read, n);
         if (!ok) break;
-        tc_fence_after();
-        grads(tb + kAccX, dp_col(n), st, 0, idX, n > 0);
-        mma_commit(&bars->empty[st]);
+        if (DQ) {
+          if (n + 1 < blocks) ok = start_s(n + 1);
+          ok = ok && wait(&bars->ds_ready, n);
+          if (ok && n + 1 < blocks) ok = start_dp(n + 1);
+          if (!ok) break;
+          grads(tb, tb + kDS, kDSHalf, dXs, idX, n > 0);
+          mma_commit(&bars->grad_done);
+          mma_commit(&bars->x_empty[st]);
+        } else {
+          ok = start_dp(n) && wait(&bars->p_ready, n);
+          if (!ok) break;
+          grads(tb, tb + kP, 32, dYm, idV, n > 0);
+          mma_commit(&bars->y_empty);
+          ok = wait(&bars->ds_ready, n);
+          if (!ok) break;
+          grads(tb + kAccX, tb + kDS, kDSHalf, dXs, idX, n > 0);
+          mma_commit(&bars->x_empty[st]);
+          if (n + 1 < blocks) ok = start_s(n + 1);
+        }
       }
       if (ok) mma_commit(&bars->acc_full);
       // Every MMA issued has completed before tensor memory is released.
@@ -271,28 +299,28 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       const size_t rows = static_cast<size_t>(bh) * p.N;
       bool ok = true;
       for (int n = 0; ok && n < blocks; ++n) {
-        const int st = n % kStages;
-        float l2[2], Dr[2];
+        const int st = n % kXStages;
+        float l2[4], Dr[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = begin + n * kCols + 32 * i + lane;
+        for (int i = 0; i < 4; ++i) {
+          const int row = begin + n * kRows + 32 * i + lane;
           l2[i] = row < p.N ? exponent_of(a.lse[rows + row]) : INFINITY;
           Dr[i] = row < p.N ? a.D[rows + row] : 0.f;
         }
-        ok = mbar_wait_warp(&bars->empty[st], ((n / kStages) & 1) ^ 1, abort_flag, p.err,
+        ok = mbar_wait_warp(&bars->x_empty[st], ((n / kXStages) & 1) ^ 1, abort_flag, p.err,
                             p.wait_ns);
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
           stats[st].lse2[32 * i + lane] = l2[i];
           stats[st].D[32 * i + lane] = Dr[i];
         }
-        mbar_arrive(&bars->full[st]);
+        mbar_arrive(&bars->x_full[st]);
       }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax warps
-    // Thread = row r of the owned side, columns 32 half ... + 31 of the streamed block.
+    // Thread = row r of the owned side, columns 64 half ... + 63 of the streamed block.
     const int w4 = warp & 3, half = (warp - 4) >> 2;
     const int r = 32 * w4 + lane, row = row0 + r;
     const uint32_t lane_base = tb + (static_cast<uint32_t>(32 * w4) << 16);
@@ -304,29 +332,23 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     }
     bool ok = true;
     for (int n = 0; ok && n < blocks; ++n) {
-      const int st = n % kStages;
-      const int col0 = begin + n * kCols + 32 * half;   // this thread's first streamed row
-      if (!DQ || begin + (n + 1) * kCols > L) {
+      const int st = n % kXStages;
+      const int col0 = begin + n * kRows + 64 * half;   // this thread's first streamed row
+      const bool tail = DQ && begin + (n + 1) * kRows > L;
+      if (!DQ || tail) {
         // The stage has landed (its MMAs wait for it too); the wait orders the statistics.
-        ok = mbar_wait_warp(&bars->full[st], (n / kStages) & 1, abort_flag, p.err, p.wait_ns);
+        ok = mbar_wait_warp(&bars->x_full[st], (n / kXStages) & 1, abort_flag, p.err, p.wait_ns);
         if (!ok) break;
       }
-      ok = mbar_wait_warp(&bars->s_full[n & 1], (n >> 1) & 1, abort_flag, p.err, p.wait_ns);
+      ok = mbar_wait_warp(&bars->s_full, n & 1, abort_flag, p.err, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tS = lane_base + kRegions + 64 * (DQ ? (n & 1) : (2 * n) % 3) + 32 * half;
-      const uint32_t tD =
-          lane_base + kRegions + 64 * (DQ ? 2 + (n & 1) : (2 * n + 1) % 3) + 32 * half;
-      uint32_t sv[32];
-      tmem_ld32_wait(tS, sv);
-      float P[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float l2 = DQ ? row_l2 : stats[st].lse2[32 * half + i];
-        P[i] = ex2(fmaf(__uint_as_float(sv[i]), c, -l2));
-      }
+      uint32_t sv[64];
+      tmem_ld64_wait(lane_base + kS + 64 * half, lane_base + kS + 64 * half + 32, sv);
+      tc_fence_before();
+      mbar_arrive(&bars->s_read);
       // Visible: key < L, and key <= query where causal.
-      int lo = 0, hi = 32;                        // visible columns of this thread's 32
+      int lo = 0, hi = 64;                        // visible columns of this thread's 64
       if (DQ) {
         hi = min(hi, L - col0);
         if (p.causal) hi = min(hi, row - col0 + 1);
@@ -334,52 +356,79 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         if (row >= L) hi = 0;
         if (p.causal) lo = max(lo, row - col0);
       }
-      const bool edge = lo > 0 || hi < 32;
+      const bool edge = lo > 0 || hi < 64;
+      float P[64];
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        float4 l2 = make_float4(row_l2, row_l2, row_l2, row_l2);
+        if (!DQ) l2 = *reinterpret_cast<const float4*>(&stats[st].lse2[64 * half + i]);
+        P[i] = ex2(fmaf(__uint_as_float(sv[i]), c, -l2.x));
+        P[i + 1] = ex2(fmaf(__uint_as_float(sv[i + 1]), c, -l2.y));
+        P[i + 2] = ex2(fmaf(__uint_as_float(sv[i + 2]), c, -l2.z));
+        P[i + 3] = ex2(fmaf(__uint_as_float(sv[i + 3]), c, -l2.w));
+      }
       if (edge) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 64; ++i)
           if (i < lo || i >= hi) P[i] = 0.f;
       }
-      uint32_t pk[16];
       if (!DQ) {
+        uint32_t pk[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(P[2 * i], P[2 * i + 1]);
-        tmem_st16(tS, pk);
+        for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(P[2 * i], P[2 * i + 1]);
+        tmem_st32(lane_base + kP + 32 * half, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars->p_ready[n & 1]);
+        mbar_arrive(&bars->p_ready);
       }
-      ok = mbar_wait_warp(&bars->dp_full[n & 1], (n >> 1) & 1, abort_flag, p.err, p.wait_ns);
+      ok = mbar_wait_warp(&bars->dp_full, n & 1, abort_flag, p.err, p.wait_ns);
       if (!ok) break;
+      if (DQ && n > 0) {   // dS of the block before has been read
+        ok = mbar_wait_warp(&bars->grad_done, (n - 1) & 1, abort_flag, p.err, p.wait_ns);
+        if (!ok) break;
+      }
       tc_fence_after();
-      tmem_ld32_wait(tD, sv);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float D = DQ ? row_D : stats[st].D[32 * half + i];
-        P[i] *= __uint_as_float(sv[i]) - D;
+      for (int q = 0; q < 2; ++q) {
+        uint32_t dv[32], pk[16];
+        tmem_ld32_wait(lane_base + kDP + 64 * half + 32 * q, dv);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float4 D = make_float4(row_D, row_D, row_D, row_D);
+          if (!DQ) D = *reinterpret_cast<const float4*>(&stats[st].D[64 * half + 32 * q + i]);
+          P[32 * q + i] *= __uint_as_float(dv[i]) - D.x;
+          P[32 * q + i + 1] *= __uint_as_float(dv[i + 1]) - D.y;
+          P[32 * q + i + 2] *= __uint_as_float(dv[i + 2]) - D.z;
+          P[32 * q + i + 3] *= __uint_as_float(dv[i + 3]) - D.w;
+        }
+        if (edge) {   // a hidden key's v may hold anything
+#pragma unroll
+          for (int i = 32 * q; i < 32 * q + 32; ++i)
+            if (i < lo || i >= hi) P[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          pk[i] = pack_bf16x2(P[32 * q + 2 * i], P[32 * q + 2 * i + 1]);
+        // In place (dK, dV): columns of this thread's own that it has read.
+        tmem_st16(lane_base + kDS + kDSHalf * half + 16 * q, pk);
       }
-      if (edge) {   // a hidden key's v may hold anything
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < lo || i >= hi) P[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(P[2 * i], P[2 * i + 1]);
-      tmem_st16(tD, pk);
-      if (DQ && begin + (n + 1) * kCols > L) {
+      if (tail) {
         // Keys past the length: zero their rows before dS K reads them, so that 0 x (anything)
         // stays 0 (the scores of this block have been formed).
-        const int t = tid - 128, key = t >> 2;
-        if (begin + n * kCols + key >= L && (t & 3) < kXSubs) {
-          uint4* kr = reinterpret_cast<uint4*>(sS + st * kStage + (t & 3) * kSSub + key * 128);
+        const int key = (tid - 128) >> 1;
+        if (begin + n * kRows + key >= L) {
+          uint8_t* kr = sX + st * kX + key * 128 + 64 * (tid & 1);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) kr[i] = make_uint4(0u, 0u, 0u, 0u);
+          for (int s = 0; s < kXSubs; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<uint4*>(kr + s * kSub)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&bars->ds_ready[n & 1]);
+      mbar_arrive(&bars->ds_ready);
     }
     // ------------------------------------------------------------ epilogue
     if (ok && blocks > 0) {
@@ -425,7 +474,7 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   if (bars->abort && tid == 0) {
-    // Let any bulk copy still in flight land before the CTA's shared memory is released.
+    // Let any copy still in flight land before the CTA's shared memory is released.
     const uint64_t t0 = globaltimer();
     while (globaltimer() - t0 < 1000000ull) {
     }
@@ -441,12 +490,10 @@ template <bool DQ>
 cudaError_t launch_one(const LatentProblem& p, const void* q, const void* kn, const void* kr,
                        const void* v, const void* dO, const BwdArgs& a, cudaStream_t s) {
   CUtensorMap mq, mkn, mkr, mv, mdo;
-  const int BH = p.B * p.H, q_rows = DQ ? kRows : kCols, k_rows = DQ ? kCols : kRows;
-  if (!make_head_map_rows(&mq, q, BH, p.N, kQK, q_rows) ||
-      !make_head_map_rows(&mkn, kn, BH, p.N, FA_LATENT_NOPE, k_rows) ||
-      !make_head_map_rows(&mkr, kr, p.B, p.N, FA_LATENT_ROPE, k_rows) ||
-      !make_head_map_rows(&mv, v, BH, p.N, kV, k_rows) ||
-      !make_head_map_rows(&mdo, dO, BH, p.N, kV, q_rows))
+  const int BH = p.B * p.H;
+  if (!make_head_map(&mq, q, BH, p.N, kQK) || !make_head_map(&mkn, kn, BH, p.N, FA_LATENT_NOPE) ||
+      !make_head_map(&mkr, kr, p.B, p.N, FA_LATENT_ROPE) ||
+      !make_head_map(&mv, v, BH, p.N, kV) || !make_head_map(&mdo, dO, BH, p.N, kV))
     return cudaErrorInvalidValue;
   static std::atomic<bool> attr_set[64];  // per device; a race repeats the same call
   int dev = 0;
