@@ -17,13 +17,13 @@
 // block against NEWKV + NEWDQ a 128 x 128 block).
 //   dK, dV  columns: dV 128, dK 192, one region of 128 for S^T, then dP^T (once the softmax warps
 //           have S^T in registers), then dS^T in place; 64 for P^T.
-//   dQ      columns: dQ 192, S 128, dP 128, dS 64: S(n + 1) and dP(n + 1) start as soon as the
-//           softmax warps have read S(n) and dP(n).
-// Of shared memory the owned rows hold 80 KB; the streamed side X (q or k, 192 columns: scores
-// early, gradient product late) has two stages of 48 KB and Y (dO or v, 128) one of 32.  Both
-// lie as [128 rows][64 columns] subtiles that the score products read K-major and the gradient
+//   dQ      columns: dQ 192, S 128, dP 128 (dS in place), the owned dO 64 as an A operand:
+//           S(n + 1) starts as soon as the softmax warps have read S(n).
+// Of shared memory the owned rows hold 80 KB (dQ: 48, which makes room for a third stage of X);
+// the streamed side X (q or k, 192 columns: scores early, gradient product late) has two or three
+// stages of 48 KB and Y (dO or v, 128) one of 32.  Both lie as [128 rows][64 columns] subtiles that the score products read K-major and the gradient
 // products MN-major.
-//   warp 0 producer; warp 1 MMA issuer; warp 2 tensor memory and (dK, dV) the block's lse and
+//   warp 0 producer; warps 1, 3 MMA issuers; warp 2 tensor memory and (dK, dV) the block's lse and
 //   D; warps 4-11 softmax, two threads a row, 64 columns each.
 // Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and exits.
 #include <atomic>
@@ -44,14 +44,14 @@ constexpr int kXSubs = (FA_LATENT_NOPE + FA_LATENT_ROPE) / 64, kYSubs = FA_LATEN
 constexpr int kQK = FA_LATENT_NOPE + FA_LATENT_ROPE, kV = FA_LATENT_V;
 constexpr int kSub = kRows * 128;       // [128 rows][64] subtile, 16 KB
 constexpr int kX = kXSubs * kSub, kY = kYSubs * kSub;
-constexpr int kXStages = 2;
+constexpr int kMaxXStages = 3;
 constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Bars {
   uint64_t fixed_full;
-  uint64_t x_full[kXStages];
-  uint64_t x_empty[kXStages];  // the block's last product has completed
+  uint64_t x_full[kMaxXStages];
+  uint64_t x_empty[kMaxXStages];  // the block's last product has completed
   uint64_t y_full;
   uint64_t y_empty;
   uint64_t s_full;
@@ -59,7 +59,7 @@ struct Bars {
   uint64_t dp_full;
   uint64_t p_ready;
   uint64_t ds_ready;
-  uint64_t grad_done;          // dQ's product of the block has completed
+  uint64_t do_ready;           // dQ: the owned dO is in tensor memory
   uint64_t acc_full;
   uint64_t drain;
   uint32_t tmem_base;
@@ -72,11 +72,18 @@ struct Stats {                          // of a streamed query block (dK, dV)
   float D[kRows];
 };
 
-constexpr int kSmem = 1024 + kX + kY + kXStages * kX + kY +
-                      kXStages * static_cast<int>(sizeof(Stats)) + static_cast<int>(sizeof(Bars));
-static_assert(kSmem <= 227 * 1024, "shared memory");
+template <bool DQ>
+struct Lay {
+  static constexpr int XS = DQ ? 3 : 2;                 // stages of X
+  static constexpr int FIXED = DQ ? kX : kX + kY;       // owned rows in shared memory
+  static constexpr int SMEM = 1024 + FIXED + XS * kX + kY +
+                              (DQ ? 0 : XS * static_cast<int>(sizeof(Stats))) +
+                              static_cast<int>(sizeof(Bars));
+  static_assert(XS <= kMaxXStages && SMEM <= 227 * 1024, "shared memory");
+};
 
 struct BwdArgs {
+  const __nv_bfloat16* dO;
   const float* lse;
   const float* D;
   __nv_bfloat16* dq;       // dQ kernel
@@ -99,17 +106,19 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
   constexpr uint32_t kAccX = DQ ? 0 : kV;            // columns of dQ or dK (dV sits before dK)
   constexpr uint32_t kS = kAccX + kQK;               // the scores
   constexpr uint32_t kDP = DQ ? kS + 128 : kS;       // dP
-  constexpr uint32_t kDS = DQ ? kDP + 128 : kDP;     // dS as bf16, 64 rows' pairs ...
-  constexpr uint32_t kDSHalf = DQ ? 32 : 64;         // ... this many columns apart
+  constexpr uint32_t kDS = kDP;                      // dS as bf16 in place, ...
+  constexpr uint32_t kDSHalf = 64;                   // ... each 64 columns' pairs at their start
   constexpr uint32_t kP = kS + 128;                  // dK, dV: P^T as bf16
+  constexpr uint32_t kDO = kDP + 128;                // dQ: the owned dO
+  constexpr int kXStages = Lay<DQ>::XS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sF = base;                                // owned rows: X subtiles, Y subtiles
-  uint8_t* sX = sF + kX + kY;                        // [kXStages]
+  uint8_t* sF = base;                                // owned rows: X subtiles (dK, dV: then Y)
+  uint8_t* sX = sF + Lay<DQ>::FIXED;                 // [kXStages]
   uint8_t* sY = sX + kXStages * kX;
   Stats* stats = reinterpret_cast<Stats*>(sY + kY);
-  Bars* bars = reinterpret_cast<Bars*>(stats + kXStages);
+  Bars* bars = reinterpret_cast<Bars*>(stats + (DQ ? 0 : kXStages));
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -141,9 +150,9 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->p_ready, 256);
     mbar_init(&bars->ds_ready, 256);
-    mbar_init(&bars->grad_done, 1);
+    mbar_init(&bars->do_ready, 256);
     mbar_init(&bars->acc_full, 1);
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, DQ ? 2 : 1);
     bars->abort = 0;
     bars->never = 0;
     fence_mbar_init();
@@ -184,9 +193,9 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         for (int s = 0; s < kYSubs; ++s)
           tma_load_3d(dst + s * kSub, keys ? &mv : &mdo, bar, 64 * s, row, bh);
       };
-      mbar_arrive_expect_tx(&bars->fixed_full, kX + kY);
+      mbar_arrive_expect_tx(&bars->fixed_full, Lay<DQ>::FIXED);
       load_x(sF, &bars->fixed_full, row0, !DQ);
-      load_y(sF + kX, &bars->fixed_full, row0, !DQ);
+      if (!DQ) load_y(sF + kX, &bars->fixed_full, row0, true);
       for (int n = 0; n < blocks; ++n) {
         const int st = n % kXStages, row = begin + n * kRows;
         if (!mbar_wait(&bars->x_empty[st], ((n / kXStages) & 1) ^ 1, abort_flag, p.err, p.wait_ns))
@@ -198,8 +207,10 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         load_y(sY, &bars->y_full, row, DQ);
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp == 1 || (DQ && warp == 3)) {
+    // ------------------------------------------------------------ MMA issuers
+    // dK, dV: one thread, since S^T follows dK in the region dS^T leaves.  dQ: one for the scores,
+    // which wait for their keys, and one for dQ and then dP in the region dS leaves.
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16(kRows, kRows, false, false);
       constexpr uint32_t idX = idesc_bf16(kRows, kQK, false, true);
@@ -249,7 +260,21 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       auto start_dp = [&](int n) -> bool {
         if (!mbar_wait(&bars->y_full, n & 1, abort_flag, p.err, p.wait_ns)) return false;
         tc_fence_after();
-        scores(tb + kDP, dF + (kX >> 4), dYk, kYSubs);
+        if (DQ) {   // A = dO from tensor memory
+#pragma unroll
+          for (int g = 0; g < kYSubs; ++g) {
+            uint32_t ta[4];
+            uint64_t db[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              ta[k] = tb + kDO + 8 * (4 * g + k);
+              db[k] = dYk + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
+            }
+            mma_ts_x4(tb + kDP, ta, db, idS, g > 0 ? 1u : 0u);
+          }
+        } else {
+          scores(tb + kDP, dF + (kX >> 4), dYk, kYSubs);
+        }
         mma_commit(&bars->dp_full);
         if (DQ) mma_commit(&bars->y_empty);
         return true;
@@ -260,36 +285,41 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         return true;
       };
       bool ok = blocks > 0;
-      if (ok) ok = mbar_wait(&bars->fixed_full, 0, abort_flag, p.err, p.wait_ns);
-      if (ok) ok = start_s(0);
-      if (ok && DQ) ok = start_dp(0);
-      for (int n = 0; ok && n < blocks; ++n) {
-        const int st = n % kXStages;
-        const uint64_t dXs = dXm + static_cast<uint64_t>((st * kX) >> 4);
-        ok = wait(&bars->s_read, n);
-        if (!ok) break;
-        if (DQ) {
-          if (n + 1 < blocks) ok = start_s(n + 1);
-          ok = ok && wait(&bars->ds_ready, n);
-          if (ok && n + 1 < blocks) ok = start_dp(n + 1);
+      if (DQ && warp == 3) {
+        ok = ok && mbar_wait(&bars->do_ready, 0, abort_flag, p.err, p.wait_ns) && start_dp(0);
+        for (int n = 0; ok && n < blocks; ++n) {
+          const int st = n % kXStages;
+          ok = mbar_wait(&bars->x_full[st], (n / kXStages) & 1, abort_flag, p.err, p.wait_ns) &&
+               wait(&bars->ds_ready, n);
           if (!ok) break;
-          grads(tb, tb + kDS, kDSHalf, dXs, idX, n > 0);
-          mma_commit(&bars->grad_done);
+          grads(tb, tb + kDS, kDSHalf, dXm + static_cast<uint64_t>((st * kX) >> 4), idX, n > 0);
           mma_commit(&bars->x_empty[st]);
-        } else {
-          ok = start_dp(n) && wait(&bars->p_ready, n);
+          if (n + 1 < blocks) ok = start_dp(n + 1);   // over dS, behind the product that reads it
+        }
+      } else if (DQ) {
+        ok = ok && mbar_wait(&bars->fixed_full, 0, abort_flag, p.err, p.wait_ns);
+        for (int n = 0; ok && n < blocks; ++n) {
+          if (n > 0) ok = wait(&bars->s_read, n - 1);
+          ok = ok && start_s(n);
+        }
+      } else {
+        ok = ok && mbar_wait(&bars->fixed_full, 0, abort_flag, p.err, p.wait_ns) && start_s(0);
+        for (int n = 0; ok && n < blocks; ++n) {
+          const int st = n % kXStages;
+          ok = wait(&bars->s_read, n) && start_dp(n) && wait(&bars->p_ready, n);
           if (!ok) break;
           grads(tb, tb + kP, 32, dYm, idV, n > 0);
           mma_commit(&bars->y_empty);
           ok = wait(&bars->ds_ready, n);
           if (!ok) break;
-          grads(tb + kAccX, tb + kDS, kDSHalf, dXs, idX, n > 0);
+          grads(tb + kAccX, tb + kDS, kDSHalf, dXm + static_cast<uint64_t>((st * kX) >> 4), idX,
+                n > 0);
           mma_commit(&bars->x_empty[st]);
           if (n + 1 < blocks) ok = start_s(n + 1);
         }
       }
-      if (ok) mma_commit(&bars->acc_full);
-      // Every MMA issued has completed before tensor memory is released.
+      if (ok && warp == (DQ ? 3 : 1)) mma_commit(&bars->acc_full);
+      // Every MMA issued by either thread has completed before tensor memory is released.
       mma_commit(&bars->drain);
       mbar_wait(&bars->drain, 0, &bars->never, nullptr, p.wait_ns);
     }
@@ -329,6 +359,24 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     if (DQ && row < p.N) {
       row_l2 = exponent_of(a.lse[static_cast<size_t>(bh) * p.N + row]);
       row_D = a.D[static_cast<size_t>(bh) * p.N + row];
+    }
+    if (DQ && blocks > 0) {
+      // The owned dO, this thread's 64 columns of its row, as the A operand of dP.
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.dO + (static_cast<size_t>(bh) * p.N + (row < p.N ? row : 0)) * kV + 64 * half);
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = row < p.N ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+      tmem_st32(lane_base + kDO + 32 * half, w);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars->do_ready);
     }
     bool ok = true;
     for (int n = 0; ok && n < blocks; ++n) {
@@ -383,10 +431,6 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       }
       ok = mbar_wait_warp(&bars->dp_full, n & 1, abort_flag, p.err, p.wait_ns);
       if (!ok) break;
-      if (DQ && n > 0) {   // dS of the block before has been read
-        ok = mbar_wait_warp(&bars->grad_done, (n - 1) & 1, abort_flag, p.err, p.wait_ns);
-        if (!ok) break;
-      }
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -409,7 +453,7 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           pk[i] = pack_bf16x2(P[32 * q + 2 * i], P[32 * q + 2 * i + 1]);
-        // In place (dK, dV): columns of this thread's own that it has read.
+        // In place: columns of this thread's own that it has read.
         tmem_st16(lane_base + kDS + kDSHalf * half + 16 * q, pk);
       }
       if (tail) {
@@ -500,13 +544,13 @@ cudaError_t launch_one(const LatentProblem& p, const void* q, const void* kn, co
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
     cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel<DQ>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DQ>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   const long long tiles = (p.N + kRows - 1) / kRows;
   return launch_dependent(latent_bwd_kernel<DQ>, dim3(static_cast<unsigned>(BH * tiles)),
-                          dim3(kThreads), kSmem, s, mq, mkn, mkr, mv, mdo, a, p);
+                          dim3(kThreads), Lay<DQ>::SMEM, s, mq, mkn, mkr, mv, mdo, a, p);
 }
 
 }  // namespace
@@ -515,7 +559,7 @@ cudaError_t launch_latent_bwd_sm103(const LatentProblem& p, const void* q, const
                                     const void* kr, const void* v, const float* lse,
                                     const void* dO, const float* Dsum, void* dq, void* dkn,
                                     float* dkr_part, void* dv, cudaStream_t s) {
-  BwdArgs a{lse, Dsum, static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dkn), dkr_part,
+  BwdArgs a{static_cast<const __nv_bfloat16*>(dO), lse, Dsum, static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dkn), dkr_part,
             static_cast<__nv_bfloat16*>(dv)};
   cudaError_t e = launch_one<false>(p, q, kn, kr, v, dO, a, s);
   if (e != cudaSuccess) return e;
