@@ -11,10 +11,10 @@
 // 832), because dK (192) + dV (128) + dQ (192) and two score tiles do not fit tensor memory's 512
 // columns, and dQ needs no fp32 sums through global memory this way.
 //
-// What bounds it: the one thread that issues, and the pipe behind it.  An MMA costs 65 to 90
-// cycles whether N is 64 or 128, so the blocks are 128 wide although tensor memory then holds one
-// score tile at a time (64-wide blocks, two in flight, measured 3.2k + 2.6k cycles a 128 x 64
-// block against NEWKV + NEWDQ a 128 x 128 block).
+// What bounds it: the issue and the pipe.  An MMA costs 65 to 90 cycles whether N is 64 or 128, so
+// the blocks are 128 wide although tensor memory then holds one score tile at a time: 4.3k (dK, dV)
+// + 2.7k (dQ) cycles a 128 x 128 block traced, against 6.4k + 5.2k with 64-wide blocks, two in
+// flight.  dK, dV: 2.9k of MMAs and the chain S^T, softmax, dP^T, softmax, dK between them.
 //   dK, dV  columns: dV 128, dK 192, one region of 128 for S^T, then dP^T (once the softmax warps
 //           have S^T in registers), then dS^T in place; 64 for P^T.
 //   dQ      columns: dQ 192, S 128, dP 128 (dS in place), the owned dO 64 as an A operand:

@@ -1,6 +1,8 @@
 // Absorbed latent decode over a paged latent cache: one new query token per sequence, up to
 // 128 heads that all read the sequence's one latent row a token.
 //
+// More than 16 heads; fa_latent_decode_few.cu has the others.
+//
 // Mathematics.  A cached row is (c, r), c the latent vector (512) that stands for keys and
 // values of every head and r the rotated key part (64) the heads share.  With the key
 // up-projection absorbed into the query, s_hj = scale q_h . (c_j, r_j) over 576 columns and
@@ -39,6 +41,7 @@
 #include <math.h>
 
 #include "fa_internal.cuh"
+#include "fa_latent_decode.cuh"
 #include "fa_paged_sched.cuh"
 #include "sm103_ptx.cuh"
 
@@ -59,7 +62,7 @@ constexpr int kRestSubs = kRow / 64 - kOwnSubs;   // the other half's, then the 
 constexpr int kQSub = kHeads * 128;           // [128 heads][64 columns], 16 KB
 constexpr int kThreads = 384;
 constexpr uint32_t kTS = kHalf, kTQ = kHalf + kKeys;       // columns of S and of Q's own half
-constexpr int kMaxWorkers = 256;              // the combine kernel's table of parts
+constexpr int kMaxWorkers = 512;              // the combine kernel's table of parts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units; exact, see fa_fwd_sm103.cu
@@ -90,23 +93,6 @@ __device__ __forceinline__ void prefetch_l2(const __nv_bfloat16* p) {   // LINES
 #pragma unroll
   for (int i = 0; i < LINES; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64 * i));
 }
-
-struct LatentArgs {
-  const __nv_bfloat16* q;  // [B, H, 576]
-  const int32_t* table;
-  long long table_stride;
-  int max_pages, page_shift, num_pages;
-  const int32_t* cache_len;
-  int B, H;
-  float c;                 // scale log2 e
-  __nv_bfloat16* o;        // [B, H, 512]
-  float* lse;
-  float* part;             // [2 workers][H][512]
-  float2* stat;            // [2 workers][2 halves][H]: maximum, sum (a half's own)
-  long long* prefix;       // [B + 1] tiles before each sequence
-  int* err;
-  unsigned long long wait_ns;
-};
 
 __global__ void __launch_bounds__(kThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap mq,
@@ -576,13 +562,17 @@ __global__ void __launch_bounds__(THREADS) latent_combine_kernel(LatentArgs a, i
   if (tid == 0) a.lse[head] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;   // of half 0
 }
 
-int max_workers() { return std::min(sm_count() / 2, kMaxWorkers); }
+// Up to 16 heads leave the tensor cores idle here (M = 128): fa_latent_decode_few.cu.
+bool few_heads(int H) { return H <= kFewHeads; }
+
+// Workers, and with it two parts' room each: pairs of CTAs, or CTAs.
+int max_workers(int H) { return std::min(few_heads(H) ? sm_count() : sm_count() / 2, kMaxWorkers); }
 
 size_t part_bytes(int H) {
-  return 2 * static_cast<size_t>(max_workers()) * H * kRank * sizeof(float);
+  return 2 * static_cast<size_t>(max_workers(H)) * H * kRank * sizeof(float);
 }
 size_t stat_bytes(int H) {
-  return round_up(2 * static_cast<size_t>(max_workers()) * 2 * H * sizeof(float2), 256);
+  return round_up(2 * static_cast<size_t>(max_workers(H)) * 2 * H * sizeof(float2), 256);
 }
 
 }  // namespace
@@ -601,27 +591,32 @@ cudaError_t launch_latent_decode(const void* q, const void* cache, long long pag
                num_pages, cache_len, B, H, scale * kLog2e, static_cast<__nv_bfloat16*>(o), lse,
                reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + part_bytes(H)),
                reinterpret_cast<long long*>(ws + part_bytes(H) + stat_bytes(H)), err, wait_ns};
+  // No more workers than there can be tiles.
+  const int keys = few_heads(H) ? kFewKeys : kKeys;
+  const long long most = static_cast<long long>(B) *
+                         (((static_cast<long long>(max_pages) << page_shift) + keys - 1) / keys);
+  const int workers = static_cast<int>(std::min<long long>(most, max_workers(H)));
   CUtensorMap mc, mq;
   const int page = 1 << page_shift;
-  if (!make_page_map(&mc, cache, num_pages, 1, page, kRow, page_stride,
-                     page < kKeys ? page : kKeys) ||
-      !make_head_map_rows(&mq, q, 1, B * H, kRow, kHeads))
+  if (!make_page_map(&mc, cache, num_pages, 1, page, kRow, page_stride, page < keys ? page : keys))
     return cudaErrorInvalidValue;
-  static std::atomic<bool> attr_set[64];  // per device; a race repeats the same call
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev].store(true);
+  cudaError_t e;
+  if (few_heads(H)) {
+    e = launch_latent_decode_few(mc, a, workers, s);
+  } else {
+    if (!make_head_map_rows(&mq, q, 1, B * H, kRow, kHeads)) return cudaErrorInvalidValue;
+    static std::atomic<bool> attr_set[64];  // per device; a race repeats the same call
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
+      e = cudaFuncSetAttribute(latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSmem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) attr_set[dev].store(true);
+    }
+    e = launch_dependent(latent_decode_kernel, dim3(2 * workers), dim3(kThreads), kSmem, s, mc, mq,
+                         a);
   }
-  // No more workers than there can be tiles.
-  const long long most = static_cast<long long>(B) *
-                         (((static_cast<long long>(max_pages) << page_shift) + kKeys - 1) / kKeys);
-  const int workers = static_cast<int>(std::min<long long>(most, max_workers()));
-  cudaError_t e = launch_dependent(latent_decode_kernel, dim3(2 * workers), dim3(kThreads), kSmem,
-                                   s, mc, mq, a);
   if (e != cudaSuccess) return e;
   // Few sequences: many parts each.
   const dim3 grid(static_cast<unsigned>(B) * H);

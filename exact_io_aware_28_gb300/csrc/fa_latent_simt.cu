@@ -12,9 +12,12 @@
 // The heads' shares of dK_rope go to the workspace in fp32 and are added in order of the heads,
 // so the result does not depend on scheduling.
 //
-// This path serves fp32 tensors.  Four threads per row, each owning every fourth column; a CTA
-// owns 64 rows and walks the other operand in tiles of 32 rows in shared memory.  Scores are in
-// the log2 domain (scale log2 e folded into the row held in registers).
+// This path serves fp32 tensors and runs at the rate of the FMA pipes, if shared memory lets it:
+// a dot product per thread reads as many words as it does multiply-adds (549 us for a training
+// step of 2 x 3 heads x 333 rows).  So both products of a tile are register tiles: a CTA of
+// 16 x 16 threads owns 16 RT rows and streams 64 rows at a time; a thread forms RT x 4 scores
+// from four columns of a row per 16-byte load, and RT x 4 of every 64 columns of the result from
+// P or dS in shared memory (203 us).  Scores are in the log2 domain.
 #include <math.h>
 
 #include "fa_internal.cuh"
@@ -27,11 +30,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kNope = FA_LATENT_NOPE, kRope = FA_LATENT_ROPE, kQK = kNope + kRope;
 constexpr int kV = FA_LATENT_V;
-constexpr int kTPR = 4;        // threads per row
-constexpr int kRows = 64;      // rows owned by one CTA
-constexpr int kTile = 32;      // rows of the other operand staged per shared-memory tile
-constexpr int kThreads = kRows * kTPR;
-constexpr int kNQ = kQK / kTPR, kNV = kV / kTPR;   // columns per thread
+constexpr int kCols = 64;      // rows of the streamed side per tile
+constexpr int kThreads = 256;  // 16 x 16
+// Row strides in shared memory: 16 bytes past a multiple of 128, so that eight rows' pieces of
+// 16 bytes lie in different banks.
+constexpr int kSX = kQK + 4, kSY = kV + 4, kSP = kCols + 4;
 
 __device__ __forceinline__ int key_limit(const LatentProblem& p, int b) {
   if (!p.kv_len) return p.N;
@@ -39,204 +42,292 @@ __device__ __forceinline__ int key_limit(const LatentProblem& p, int b) {
   return L < 0 ? 0 : (L > p.N ? p.N : L);
 }
 
-__device__ __forceinline__ float group_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
+// Sum and maximum over the 16 threads that share a row.
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+__device__ __forceinline__ float row_max(float x) {
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
   return x;
 }
 
-// Column c of key j's row of head bh.
-__device__ __forceinline__ float key_at(const LatentProblem& p, const float* kn, const float* kr,
-                                        int bh, int b, int j, int c) {
-  return c < kNope ? kn[(static_cast<size_t>(bh) * p.N + j) * kNope + c]
-                   : kr[(static_cast<size_t>(b) * p.N + j) * kRope + c - kNope];
+// `count` rows of `src` from row r0 on (W columns each) into `dst`; rows from `limit` on are 0.
+template <int W, int STRIDE>
+__device__ __forceinline__ void load_rows(float* dst, const float* src, int r0, int limit,
+                                          int count) {
+  for (int e = threadIdx.x; e < count * (W / 4); e += kThreads) {
+    const int i = e / (W / 4), c = e % (W / 4);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + i < limit) x = reinterpret_cast<const float4*>(src + static_cast<size_t>(r0 + i) * W)[c];
+    *reinterpret_cast<float4*>(dst + i * STRIDE + 4 * c) = x;
+  }
 }
 
+// The rows (k_nope, k_rope) of a head's keys.
+__device__ __forceinline__ void load_keys(float* dst, const float* kn, const float* kr, int r0,
+                                          int limit, int count) {
+  load_rows<kNope, kSX>(dst, kn, r0, limit, count);
+  load_rows<kRope, kSX>(dst + kNope, kr, r0, limit, count);
+}
+
+// acc[i][j] = own row (RT ty + i) . streamed row (tx + 16 j) over W columns.
+template <int RT, int W, int STRIDE>
+__device__ __forceinline__ void dots(float (&acc)[RT][4], const float* own, const float* str) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < W; k += 4) {
+    float4 a[RT], b[4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      a[i] = *reinterpret_cast<const float4*>(own + (RT * ty + i) * STRIDE + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      b[j] = *reinterpret_cast<const float4*>(str + (tx + 16 * j) * STRIDE + k);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y,
+                    fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, acc[i][j]))));
+  }
+}
+
+// acc[i][4 g + c] += sum over the tile's rows j of w[RT ty + i][j] x[j][64 g + 4 tx + c].
+template <int RT, int G, int STRIDE>
+__device__ __forceinline__ void mix(float (&acc)[RT][4 * G], const float* w, const float* x) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+  for (int j = 0; j < kCols; j += 4) {
+    float a[RT][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const float4 x4 = *reinterpret_cast<const float4*>(w + (RT * ty + i) * kSP + j);
+      a[i][0] = x4.x;
+      a[i][1] = x4.y;
+      a[i][2] = x4.z;
+      a[i][3] = x4.w;
+    }
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float4 b = *reinterpret_cast<const float4*>(x + (j + jj) * STRIDE + 64 * g + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          acc[i][4 * g] = fmaf(a[i][jj], b.x, acc[i][4 * g]);
+          acc[i][4 * g + 1] = fmaf(a[i][jj], b.y, acc[i][4 * g + 1]);
+          acc[i][4 * g + 2] = fmaf(a[i][jj], b.z, acc[i][4 * g + 2]);
+          acc[i][4 * g + 3] = fmaf(a[i][jj], b.w, acc[i][4 * g + 3]);
+        }
+      }
+  }
+}
+
+template <int RT>
+constexpr int fwd_smem() {
+  return (16 * RT * (kSX + kSP) + kCols * (kSX + kSY)) * static_cast<int>(sizeof(float));
+}
+template <int RT>
+constexpr int bwd_smem() {
+  return (16 * RT * (kSX + kSY + 2 * kSP) + kCols * (kSX + kSY + 2)) *
+         static_cast<int>(sizeof(float));
+}
+static_assert(bwd_smem<4>() <= 227 * 1024, "shared memory");
+
+template <int RT>
 __global__ void __launch_bounds__(kThreads)
 latent_fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn,
+                       const float* __restrict__ kr, const float* __restrict__ v, float* o,
+                       float* o_acc, float* __restrict__ lse, LatentProblem p) {
+  constexpr int R = 16 * RT;
+  extern __shared__ float4 smem4[];
+  float* qs = reinterpret_cast<float*>(smem4);   // [R][kSX]
+  float* ps = qs + R * kSX;                      // [R][kSP]
+  float* ks = ps + R * kSP;                      // [64][kSX]
+  float* vs = ks + kCols * kSX;                  // [64][kSY]
+  const int N = p.N, bh = blockIdx.y, b = bh / p.H;
+  const size_t head = static_cast<size_t>(bh) * N, seq = static_cast<size_t>(b) * N;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int row0 = (gridDim.x - 1 - blockIdx.x) * R;       // the longest (causal) rows first
+  const float c = p.scale * kLog2e;
+  load_rows<kQK, kSX>(qs, q + head * kQK, row0, N, R);
+  float acc[RT][8], m[RT], l[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  }
+  int kend = key_limit(p, b);
+  if (p.causal) kend = min(kend, row0 + R);
+  for (int k0 = 0; k0 < kend; k0 += kCols) {
+    __syncthreads();
+    load_keys(ks, kn + head * kNope, kr + seq * kRope, k0, kend, kCols);
+    load_rows<kV, kSY>(vs, v + head * kV, k0, kend, kCols);
+    __syncthreads();
+    float s[RT][4];
+    dots<RT, kQK, kSX>(s, qs, ks);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int row = row0 + RT * ty + i;
+      const int lim = p.causal ? min(kend, row + 1) : kend;
+      float mt = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = k0 + tx + 16 * j < lim ? s[i][j] * c : -INFINITY;
+        mt = fmaxf(mt, s[i][j]);
+      }
+      mt = fmaxf(m[i], row_max(mt));
+      const float use = mt == -INFINITY ? 0.f : mt;
+      const float alpha = exp2f(m[i] - use);      // m = -inf gives 0
+      m[i] = mt;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float pj = exp2f(s[i][j] - use);
+        sum += pj;
+        ps[(RT * ty + i) * kSP + tx + 16 * j] = pj;
+      }
+      l[i] = fmaf(l[i], alpha, sum);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] *= alpha;
+    }
+    __syncthreads();
+    mix<RT, 2, kSY>(acc, ps, vs);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int row = row0 + RT * ty + i;
+    const float lt = row_sum(l[i]);
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;   // a NaN sum stays one
+    if (row >= N) continue;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float4 x = make_float4(acc[i][4 * g] * inv, acc[i][4 * g + 1] * inv,
+                                   acc[i][4 * g + 2] * inv, acc[i][4 * g + 3] * inv);
+      const size_t at = (head + row) * kV + 64 * g + 4 * tx;
+      *reinterpret_cast<float4*>(o + at) = x;
+      if (o_acc) *reinterpret_cast<float4*>(o_acc + at) = x;
+    }
+    if (tx == 0) lse[head + row] = lt == 0.f ? -INFINITY : (m[i] + log2f(lt)) * kLn2;
+  }
+}
+
+// DQ = false: the CTA owns keys and streams queries (dK, dV); DQ = true: the other way (dQ).
+template <bool DQ, int RT>
+__global__ void __launch_bounds__(kThreads)
+latent_bwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn,
                        const float* __restrict__ kr, const float* __restrict__ v,
-                       float* __restrict__ o, float* __restrict__ o_acc, float* __restrict__ lse,
-                       LatentProblem p) {
-  __shared__ float ks[kTile][kQK];
-  __shared__ float vs[kTile][kV];
+                       const float* __restrict__ lse, const float* __restrict__ dO,
+                       const float* __restrict__ Dsum, float* __restrict__ dq,
+                       float* __restrict__ dkn, float* __restrict__ dkr_part,
+                       float* __restrict__ dv, LatentProblem p) {
+  constexpr int R = 16 * RT;
+  extern __shared__ float4 smem4[];
+  float* ox = reinterpret_cast<float*>(smem4);   // owned: q or k, [R][kSX]
+  float* oy = ox + R * kSX;                      // owned: dO or v, [R][kSY]
+  float* ps = oy + R * kSY;                      // [R][kSP], P (dK, dV)
+  float* ds = ps + R * kSP;                      // [R][kSP], dS
+  float* sx = ds + R * kSP;                      // streamed: k or q, [64][kSX]
+  float* sy = sx + kCols * kSX;                  // streamed: v or dO, [64][kSY]
+  float* sl = sy + kCols * kSY;                  // streamed rows' lse and D (dK, dV)
+  float* sd = sl + kCols;
   const int N = p.N, bh = blockIdx.y, b = bh / p.H;
-  const size_t rows0 = static_cast<size_t>(bh) * N;
-  const int tid = threadIdx.x, part = tid % kTPR;
-  const int row0 = blockIdx.x * kRows, row = row0 + tid / kTPR;
-  const bool valid_row = row < N;
-  const float c = p.scale * kLog2e;
-  float qr[kNQ], acc[kNV];
-#pragma unroll
-  for (int t = 0; t < kNQ; ++t)
-    qr[t] = valid_row ? q[(rows0 + row) * kQK + part + kTPR * t] * c : 0.f;
-#pragma unroll
-  for (int t = 0; t < kNV; ++t) acc[t] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  int kend = key_limit(p, b);
-  if (p.causal) kend = min(kend, min(N, row0 + kRows));
-  for (int k0 = 0; k0 < kend; k0 += kTile) {
-    const int jmax = min(kTile, kend - k0);
-    __syncthreads();
-    for (int e = tid; e < jmax * kQK; e += kThreads)
-      ks[e / kQK][e % kQK] = key_at(p, kn, kr, bh, b, k0 + e / kQK, e % kQK);
-    for (int e = tid; e < jmax * kV; e += kThreads)
-      vs[e / kV][e % kV] = v[(rows0 + k0 + e / kV) * kV + e % kV];
-    __syncthreads();
-    for (int j = 0; j < jmax; ++j) {
-      float s = 0.f;
-#pragma unroll
-      for (int t = 0; t < kNQ; ++t) s = fmaf(qr[t], ks[j][part + kTPR * t], s);
-      s = group_sum(s);
-      if (!valid_row || (p.causal && k0 + j > row)) continue;
-      if (s > m) {
-        const float alpha = exp2f(m - s);
-        l *= alpha;
-#pragma unroll
-        for (int t = 0; t < kNV; ++t) acc[t] *= alpha;
-        m = s;
-      }
-      const float pj = exp2f(s - m);
-      l += pj;
-#pragma unroll
-      for (int t = 0; t < kNV; ++t) acc[t] = fmaf(pj, vs[j][part + kTPR * t], acc[t]);
-    }
-  }
-  if (valid_row) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int t = 0; t < kNV; ++t) {
-      const size_t at = (rows0 + row) * kV + part + kTPR * t;
-      o[at] = acc[t] * inv;
-      if (o_acc) o_acc[at] = acc[t] * inv;
-    }
-    if (part == 0) lse[rows0 + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  }
-}
-
-// Key-outer: one CTA owns 64 keys of one head and walks every query row that may see them.
-__global__ void __launch_bounds__(kThreads)
-latent_dkdv_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn,
-                        const float* __restrict__ kr, const float* __restrict__ v,
-                        const float* __restrict__ lse, const float* __restrict__ dO,
-                        const float* __restrict__ Dsum, float* __restrict__ dkn,
-                        float* __restrict__ dkr_part, float* __restrict__ dv, LatentProblem p) {
-  __shared__ float qs[kTile][kQK];
-  __shared__ float dos[kTile][kV];
-  __shared__ float lses[kTile], Ds[kTile];
-  const int N = p.N, bh = blockIdx.y, b = bh / p.H;
-  const size_t rows0 = static_cast<size_t>(bh) * N;
-  const int tid = threadIdx.x, part = tid % kTPR;
-  const int key0 = blockIdx.x * kRows, key = key0 + tid / kTPR;
+  const size_t head = static_cast<size_t>(bh) * N, seq = static_cast<size_t>(b) * N;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  // The tiles with the most work first (causal: early keys, late queries).
+  const int row0 = (DQ ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * R;
   const int L = key_limit(p, b);
-  const bool live_key = key < L;
   const float c = p.scale * kLog2e;
-  float kreg[kNQ], vr[kNV], dka[kNQ], dva[kNV];
+  float ax[RT][12], ay[RT][8];                   // dQ or dK; dV
 #pragma unroll
-  for (int t = 0; t < kNQ; ++t) {
-    kreg[t] = live_key ? key_at(p, kn, kr, bh, b, key, part + kTPR * t) * c : 0.f;
-    dka[t] = 0.f;
+  for (int i = 0; i < RT; ++i) {
+#pragma unroll
+    for (int j = 0; j < 12; ++j) ax[i][j] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ay[i][j] = 0.f;
   }
+  float own_lse[RT], own_D[RT];
+  if constexpr (DQ) {
+    load_rows<kQK, kSX>(ox, q + head * kQK, row0, N, R);
+    load_rows<kV, kSY>(oy, dO + head * kV, row0, N, R);
 #pragma unroll
-  for (int t = 0; t < kNV; ++t) {
-    vr[t] = live_key ? v[(rows0 + key) * kV + part + kTPR * t] : 0.f;
-    dva[t] = 0.f;
+    for (int i = 0; i < RT; ++i) {
+      const int row = row0 + RT * ty + i;
+      own_lse[i] = row < N ? lse[head + row] : -INFINITY;
+      own_D[i] = row < N ? Dsum[head + row] : 0.f;
+    }
+  } else {
+    load_keys(ox, kn + head * kNope, kr + seq * kRope, row0, L, R);
+    load_rows<kV, kSY>(oy, v + head * kV, row0, L, R);
   }
-  if (key0 < L) {
-    for (int i0 = p.causal ? key0 : 0; i0 < N; i0 += kTile) {
-      const int imax = min(kTile, N - i0);
-      __syncthreads();
-      for (int e = tid; e < imax * kQK; e += kThreads)
-        qs[e / kQK][e % kQK] = q[(rows0 + i0) * kQK + e];
-      for (int e = tid; e < imax * kV; e += kThreads)
-        dos[e / kV][e % kV] = dO[(rows0 + i0) * kV + e];
-      if (tid < imax) {
-        lses[tid] = lse[rows0 + i0 + tid];
-        Ds[tid] = Dsum[rows0 + i0 + tid];
-      }
-      __syncthreads();
-      for (int ii = 0; ii < imax; ++ii) {
-        float s = 0.f, dp = 0.f;
-#pragma unroll
-        for (int t = 0; t < kNQ; ++t) s = fmaf(kreg[t], qs[ii][part + kTPR * t], s);
-#pragma unroll
-        for (int t = 0; t < kNV; ++t) dp = fmaf(vr[t], dos[ii][part + kTPR * t], dp);
-        s = group_sum(s);
-        dp = group_sum(dp);
-        if (!live_key || (p.causal && key > i0 + ii)) continue;
-        const float pij = exp2f(fmaf(-kLog2e, lses[ii], s));
-        const float ds = pij * (dp - Ds[ii]);
-#pragma unroll
-        for (int t = 0; t < kNV; ++t) dva[t] = fmaf(pij, dos[ii][part + kTPR * t], dva[t]);
-#pragma unroll
-        for (int t = 0; t < kNQ; ++t) dka[t] = fmaf(ds, qs[ii][part + kTPR * t], dka[t]);
+  int begin = 0, end = DQ ? L : (row0 < L ? N : 0);
+  if (p.causal && DQ) end = min(end, row0 + R);
+  if (p.causal && !DQ) begin = row0 / kCols * kCols;
+  for (int c0 = begin; c0 < end; c0 += kCols) {
+    __syncthreads();
+    if constexpr (DQ) {
+      load_keys(sx, kn + head * kNope, kr + seq * kRope, c0, end, kCols);
+      load_rows<kV, kSY>(sy, v + head * kV, c0, end, kCols);
+    } else {
+      load_rows<kQK, kSX>(sx, q + head * kQK, c0, end, kCols);
+      load_rows<kV, kSY>(sy, dO + head * kV, c0, end, kCols);
+      if (threadIdx.x < kCols) {
+        const int row = c0 + threadIdx.x;
+        sl[threadIdx.x] = row < N ? lse[head + row] : -INFINITY;
+        sd[threadIdx.x] = row < N ? Dsum[head + row] : 0.f;
       }
     }
-  }
-  if (key < N) {
-#pragma unroll
-    for (int t = 0; t < kNV; ++t) dv[(rows0 + key) * kV + part + kTPR * t] = dva[t];
-#pragma unroll
-    for (int t = 0; t < kNQ; ++t) {
-      const int cc = part + kTPR * t;
-      if (cc < kNope) dkn[(rows0 + key) * kNope + cc] = dka[t] * p.scale;
-      else dkr_part[(rows0 + key) * kRope + cc - kNope] = dka[t] * p.scale;
-    }
-  }
-}
-
-// Query-outer: one CTA owns 64 query rows and walks every key they may see.
-__global__ void __launch_bounds__(kThreads)
-latent_dq_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn,
-                      const float* __restrict__ kr, const float* __restrict__ v,
-                      const float* __restrict__ lse, const float* __restrict__ dO,
-                      const float* __restrict__ Dsum, float* __restrict__ dq, LatentProblem p) {
-  __shared__ float ks[kTile][kQK];
-  __shared__ float vs[kTile][kV];
-  const int N = p.N, bh = blockIdx.y, b = bh / p.H;
-  const size_t rows0 = static_cast<size_t>(bh) * N;
-  const int tid = threadIdx.x, part = tid % kTPR;
-  const int row0 = blockIdx.x * kRows, row = row0 + tid / kTPR;
-  const bool valid_row = row < N;
-  const float c = p.scale * kLog2e;
-  float qr[kNQ], dor[kNV], acc[kNQ];
-#pragma unroll
-  for (int t = 0; t < kNQ; ++t) {
-    qr[t] = valid_row ? q[(rows0 + row) * kQK + part + kTPR * t] * c : 0.f;
-    acc[t] = 0.f;
-  }
-#pragma unroll
-  for (int t = 0; t < kNV; ++t)
-    dor[t] = valid_row ? dO[(rows0 + row) * kV + part + kTPR * t] : 0.f;
-  const float row_lse = valid_row ? lse[rows0 + row] : -INFINITY;
-  const float Di = valid_row ? Dsum[rows0 + row] : 0.f;
-  int kend = key_limit(p, b);
-  if (p.causal) kend = min(kend, min(N, row0 + kRows));
-  for (int k0 = 0; k0 < kend; k0 += kTile) {
-    const int jmax = min(kTile, kend - k0);
     __syncthreads();
-    for (int e = tid; e < jmax * kQK; e += kThreads)
-      ks[e / kQK][e % kQK] = key_at(p, kn, kr, bh, b, k0 + e / kQK, e % kQK);
-    for (int e = tid; e < jmax * kV; e += kThreads)
-      vs[e / kV][e % kV] = v[(rows0 + k0 + e / kV) * kV + e % kV];
-    __syncthreads();
-    for (int j = 0; j < jmax; ++j) {
-      float s = 0.f, dp = 0.f;
+    float s[RT][4], dp[RT][4];
+    dots<RT, kQK, kSX>(s, ox, sx);
+    dots<RT, kV, kSY>(dp, oy, sy);
 #pragma unroll
-      for (int t = 0; t < kNQ; ++t) s = fmaf(qr[t], ks[j][part + kTPR * t], s);
+    for (int i = 0; i < RT; ++i) {
+      const int own = row0 + RT * ty + i;
 #pragma unroll
-      for (int t = 0; t < kNV; ++t) dp = fmaf(dor[t], vs[j][part + kTPR * t], dp);
-      s = group_sum(s);
-      dp = group_sum(dp);
-      if (!valid_row || (p.causal && k0 + j > row)) continue;
-      const float ds = exp2f(fmaf(-kLog2e, row_lse, s)) * (dp - Di);
-#pragma unroll
-      for (int t = 0; t < kNQ; ++t) acc[t] = fmaf(ds, ks[j][part + kTPR * t], acc[t]);
+      for (int j = 0; j < 4; ++j) {
+        const int col = c0 + tx + 16 * j;
+        const int key = DQ ? col : own, row = DQ ? own : col;
+        const float rl = DQ ? own_lse[i] : sl[tx + 16 * j];   // -inf: no key seen, or no such row
+        const float rd = DQ ? own_D[i] : sd[tx + 16 * j];
+        const bool seen = key < L && !(p.causal && key > row) && rl != -INFINITY;
+        const float pij = seen ? exp2f(fmaf(-kLog2e, rl, s[i][j] * c)) : 0.f;
+        if (!DQ) ps[(RT * ty + i) * kSP + tx + 16 * j] = pij;
+        ds[(RT * ty + i) * kSP + tx + 16 * j] = seen ? pij * (dp[i][j] - rd) : 0.f;
+      }
     }
+    __syncthreads();
+    mix<RT, 3, kSX>(ax, ds, sx);
+    if constexpr (!DQ) mix<RT, 2, kSY>(ay, ps, sy);
   }
-  if (valid_row) {
 #pragma unroll
-    for (int t = 0; t < kNQ; ++t)
-      dq[(rows0 + row) * kQK + part + kTPR * t] = acc[t] * p.scale;
+  for (int i = 0; i < RT; ++i) {
+    const int own = row0 + RT * ty + i;
+    if (own >= N) continue;
+    const size_t at = head + own;
+#pragma unroll
+    for (int g = 0; g < 3; ++g) {
+      const float4 x = make_float4(ax[i][4 * g] * p.scale, ax[i][4 * g + 1] * p.scale,
+                                   ax[i][4 * g + 2] * p.scale, ax[i][4 * g + 3] * p.scale);
+      float* dst = DQ ? dq + at * kQK + 64 * g
+                      : g < 2 ? dkn + at * kNope + 64 * g : dkr_part + at * kRope;
+      *reinterpret_cast<float4*>(dst + 4 * tx) = x;
+    }
+    if constexpr (!DQ) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        *reinterpret_cast<float4*>(dv + at * kV + 64 * g + 4 * tx) =
+            make_float4(ay[i][4 * g], ay[i][4 * g + 1], ay[i][4 * g + 2], ay[i][4 * g + 3]);
+    }
   }
 }
 
@@ -297,32 +388,65 @@ latent_rope_sum_kernel(const float* __restrict__ part, T* __restrict__ dkr, int 
 
 }  // namespace
 
+namespace {
+
+// Rows per thread: four (64-row CTAs) where that still gives every SM two CTAs, else two.
+bool wide_rows(const LatentProblem& p) {
+  return static_cast<long long>(p.B) * p.H * ((p.N + 63) / 64) >= 2ll * sm_count();
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_tiles(void (*kernel)(KArgs...), int smem, int rows, const LatentProblem& p,
+                         cudaStream_t s, Args... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((p.N + rows - 1) / rows, p.B * p.H);
+  kernel<<<grid, kThreads, smem, s>>>(args..., p);
+  return cudaGetLastError();
+}
+
+template <int RT>
+cudaError_t fwd_rows(const LatentProblem& p, const float* q, const float* kn, const float* kr,
+                     const float* v, float* o, float* o_acc, float* lse, cudaStream_t s) {
+  return launch_tiles(latent_fwd_simt_kernel<RT>, fwd_smem<RT>(), 16 * RT, p, s, q, kn, kr, v, o,
+                      o_acc, lse);
+}
+
+template <int RT>
+cudaError_t bwd_rows(const LatentProblem& p, const float* q, const float* kn, const float* kr,
+                     const float* v, const float* lse, const float* dO, const float* Dsum,
+                     float* dq, float* dkn, float* dkr_part, float* dv, cudaStream_t s) {
+  cudaError_t e = launch_tiles(latent_bwd_simt_kernel<false, RT>, bwd_smem<RT>(), 16 * RT, p, s, q,
+                               kn, kr, v, lse, dO, Dsum, dq, dkn, dkr_part, dv);
+  if (e != cudaSuccess) return e;
+  return launch_tiles(latent_bwd_simt_kernel<true, RT>, bwd_smem<RT>(), 16 * RT, p, s, q, kn, kr, v,
+                      lse, dO, Dsum, dq, dkn, dkr_part, dv);
+}
+
+}  // namespace
+
 cudaError_t launch_latent_fwd_simt(const LatentProblem& p, const void* q, const void* kn,
                                    const void* kr, const void* v, void* o, float* o_acc,
                                    float* lse, cudaStream_t s) {
-  const dim3 grid((p.N + kRows - 1) / kRows, p.B * p.H);
-  latent_fwd_simt_kernel<<<grid, kThreads, 0, s>>>(
-      static_cast<const float*>(q), static_cast<const float*>(kn), static_cast<const float*>(kr),
-      static_cast<const float*>(v), static_cast<float*>(o), o_acc, lse, p);
-  return cudaGetLastError();
+  const float *qf = static_cast<const float*>(q), *knf = static_cast<const float*>(kn);
+  const float *krf = static_cast<const float*>(kr), *vf = static_cast<const float*>(v);
+  float* of = static_cast<float*>(o);
+  return wide_rows(p) ? fwd_rows<4>(p, qf, knf, krf, vf, of, o_acc, lse, s)
+                      : fwd_rows<2>(p, qf, knf, krf, vf, of, o_acc, lse, s);
 }
 
 cudaError_t launch_latent_bwd_simt(const LatentProblem& p, const void* q, const void* kn,
                                    const void* kr, const void* v, const float* lse,
                                    const void* dO, const float* Dsum, void* dq, void* dkn,
                                    float* dkr_part, void* dv, cudaStream_t s) {
-  const dim3 grid((p.N + kRows - 1) / kRows, p.B * p.H);
   const float *qf = static_cast<const float*>(q), *knf = static_cast<const float*>(kn);
   const float *krf = static_cast<const float*>(kr), *vf = static_cast<const float*>(v);
   const float* dof = static_cast<const float*>(dO);
-  latent_dkdv_simt_kernel<<<grid, kThreads, 0, s>>>(qf, knf, krf, vf, lse, dof, Dsum,
-                                                    static_cast<float*>(dkn), dkr_part,
-                                                    static_cast<float*>(dv), p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  latent_dq_simt_kernel<<<grid, kThreads, 0, s>>>(qf, knf, krf, vf, lse, dof, Dsum,
-                                                  static_cast<float*>(dq), p);
-  return cudaGetLastError();
+  float *dqf = static_cast<float*>(dq), *dknf = static_cast<float*>(dkn);
+  float* dvf = static_cast<float*>(dv);
+  return wide_rows(p)
+             ? bwd_rows<4>(p, qf, knf, krf, vf, lse, dof, Dsum, dqf, dknf, dkr_part, dvf, s)
+             : bwd_rows<2>(p, qf, knf, krf, vf, lse, dof, Dsum, dqf, dknf, dkr_part, dvf, s);
 }
 
 cudaError_t launch_latent_rowdot(const LatentProblem& p, fa_dtype dt, const float* o_acc,
