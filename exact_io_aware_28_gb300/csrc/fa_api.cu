@@ -462,7 +462,8 @@ fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
   fa_status st = check_pool(num_pages, page_size, 8, 8);
   if (st == FA_OK) st = check_table(block_table, table_stride, max_pages, page_size);
   if (st != FA_OK) return st;
-  if (B > 8192 || (long long)B * max_pages * page_size >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (B > 8192 || n_slots > (1 << 30) || (long long)B * max_pages * page_size >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
   if (bad4(cache_len) || bad4(new_len) || bad4(total_len) || bad4(token_start) ||
       bad4(pages_taken))
     return FA_ERR_INVALID_ARG;
@@ -472,9 +473,12 @@ fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
   const long long n_in[3] = {B, B, n_free};
   const int32_t* outs[5] = {total_len, token_start, slots, pages_taken, block_table};
   const long long n_out[5] = {B, B + 1ll, n_slots, 1, (B - 1) * table_stride + max_pages};
-  for (int i = 0; i < 3; ++i)
-    for (int j = 0; j < 5; ++j)
+  for (int j = 0; j < 5; ++j) {
+    for (int i = 0; i < 3; ++i)
       if (overlap(ins[i], n_in[i], outs[j], n_out[j])) return FA_ERR_INVALID_ARG;
+    for (int i = 0; i < j; ++i)
+      if (overlap(outs[i], n_out[i], outs[j], n_out[j])) return FA_ERR_INVALID_ARG;
+  }
   return to_status(launch_paged_tables(cache_len, new_len, free_pages, n_free, block_table,
                                        table_stride, max_pages, total_len, token_start, slots,
                                        n_slots, pages_taken, B, page_shift(page_size), num_pages,

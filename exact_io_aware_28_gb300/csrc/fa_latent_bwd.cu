@@ -215,37 +215,39 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       constexpr uint32_t idS = idesc_bf16(kRows, kRows, false, false);
       constexpr uint32_t idX = idesc_bf16(kRows, kQK, false, true);
       constexpr uint32_t idV = idesc_bf16(kRows, kV, false, true);
-      const uint64_t dF = sw128_desc(smem_u32(sF), 16, 1024);
-      const uint64_t dXk = sw128_desc(smem_u32(sX), 16, 1024);      // streamed, K-major
-      const uint64_t dYk = sw128_desc(smem_u32(sY), 16, 1024);
-      const uint64_t dXm = sw128_desc(smem_u32(sX), kSub, 1024);    // streamed, MN-major
-      const uint64_t dYm = sw128_desc(smem_u32(sY), kSub, 1024);
+      // Descriptors by their low words (the start address); the high words hold the strides, alike
+      // for K-major and for MN-major operands.
+      auto low = [](const uint8_t* p, uint32_t lbo) {
+        return static_cast<uint32_t>(sw128_desc(smem_u32(p), lbo, 1024));
+      };
+      const uint32_t hi = static_cast<uint32_t>(sw128_desc(0, 16, 1024) >> 32);
+      const uint32_t dF = low(sF, 16), dXk = low(sX, 16), dYk = low(sY, 16);   // K-major
+      const uint32_t dXm = low(sX, kSub), dYm = low(sY, kSub);                 // MN-major
       // Score product over `subs` subtiles from descriptors a0 and b0 on.
-      auto scores = [&](uint32_t d, uint64_t a0, uint64_t b0, int subs) {
+      auto scores = [&](uint32_t d, uint32_t a0, uint32_t b0, int subs) {
 #pragma unroll
         for (int g = 0; g < subs; ++g) {
-          uint64_t da[4], db[4];
+          uint32_t da[4], db[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            da[k] = a0 + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
-            db[k] = b0 + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
+            da[k] = a0 + ((g * kSub + k * 32) >> 4);
+            db[k] = b0 + ((g * kSub + k * 32) >> 4);
           }
-          mma_ss_x4(d, da, db, idS, g > 0 ? 1u : 0u);
+          mma_ss_x4_lo(d, da, hi, db, hi, idS, g > 0 ? 1u : 0u);
         }
       };
       // Gradient product: A from the bf16 pairs at `t` (64 rows of the block each `half` columns),
       // B the stage's subtiles along the rows.
-      auto grads = [&](uint32_t d, uint32_t t, uint32_t half, uint64_t b0, uint32_t id, bool acc) {
+      auto grads = [&](uint32_t d, uint32_t t, uint32_t half, uint32_t b0, uint32_t id, bool acc) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          uint32_t ta[4];
-          uint64_t db[4];
+          uint32_t ta[4], db[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             ta[k] = t + g * half + 8 * k;
-            db[k] = b0 + static_cast<uint64_t>((2048 * (4 * g + k)) >> 4);
+            db[k] = b0 + ((2048 * (4 * g + k)) >> 4);
           }
-          mma_ts_x4(d, ta, db, id, (acc || g > 0) ? 1u : 0u);
+          mma_ts_x4_lo(d, ta, db, hi, id, (acc || g > 0) ? 1u : 0u);
         }
       };
       auto start_s = [&](int n) -> bool {
@@ -253,7 +255,7 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         if (!mbar_wait(&bars->x_full[st], (n / kXStages) & 1, abort_flag, p.err, p.wait_ns))
           return false;
         tc_fence_after();
-        scores(tb + kS, dF, dXk + static_cast<uint64_t>((st * kX) >> 4), kXSubs);
+        scores(tb + kS, dF, dXk + ((st * kX) >> 4), kXSubs);
         mma_commit(&bars->s_full);
         return true;
       };
@@ -263,14 +265,13 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         if (DQ) {   // A = dO from tensor memory
 #pragma unroll
           for (int g = 0; g < kYSubs; ++g) {
-            uint32_t ta[4];
-            uint64_t db[4];
+            uint32_t ta[4], db[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               ta[k] = tb + kDO + 8 * (4 * g + k);
-              db[k] = dYk + static_cast<uint64_t>((g * kSub + k * 32) >> 4);
+              db[k] = dYk + ((g * kSub + k * 32) >> 4);
             }
-            mma_ts_x4(tb + kDP, ta, db, idS, g > 0 ? 1u : 0u);
+            mma_ts_x4_lo(tb + kDP, ta, db, hi, idS, g > 0 ? 1u : 0u);
           }
         } else {
           scores(tb + kDP, dF + (kX >> 4), dYk, kYSubs);
@@ -292,7 +293,7 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           ok = mbar_wait(&bars->x_full[st], (n / kXStages) & 1, abort_flag, p.err, p.wait_ns) &&
                wait(&bars->ds_ready, n);
           if (!ok) break;
-          grads(tb, tb + kDS, kDSHalf, dXm + static_cast<uint64_t>((st * kX) >> 4), idX, n > 0);
+          grads(tb, tb + kDS, kDSHalf, dXm + ((st * kX) >> 4), idX, n > 0);
           mma_commit(&bars->x_empty[st]);
           if (n + 1 < blocks) ok = start_dp(n + 1);   // over dS, behind the product that reads it
         }
@@ -312,7 +313,7 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           mma_commit(&bars->y_empty);
           ok = wait(&bars->ds_ready, n);
           if (!ok) break;
-          grads(tb + kAccX, tb + kDS, kDSHalf, dXm + static_cast<uint64_t>((st * kX) >> 4), idX,
+          grads(tb + kAccX, tb + kDS, kDSHalf, dXm + ((st * kX) >> 4), idX,
                 n > 0);
           mma_commit(&bars->x_empty[st]);
           if (n + 1 < blocks) ok = start_s(n + 1);

@@ -169,6 +169,10 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       const uint64_t dQ = sw128_desc(smem_u32(sQ + t * kQTile), 16, 1024);  // K-major Q_t
       const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);               // K-major K stages
       const uint64_t dV = sw128_desc(smem_u32(sV), kSub, 1024);             // MN-major V
+      // Descriptors differ in their low words only (the start address).
+      const uint32_t loQ = static_cast<uint32_t>(dQ), loK = static_cast<uint32_t>(dK);
+      const uint32_t loV = static_cast<uint32_t>(dV);
+      const uint32_t hiK = static_cast<uint32_t>(dK >> 32), hiV = static_cast<uint32_t>(dV >> 32);
       const uint32_t tS = tb + t * 128, tO = tb + 256 + t * 128;
       int last = -1;
       for (int j = jend - 1; j >= 0 && last < 0; --j)
@@ -184,17 +188,17 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         ++nk;
         tc_fence_after();
         if (need(p, u, t, j)) {
-          const uint64_t dKs = dK + static_cast<uint64_t>((st * kQTile) >> 4);
+          const uint32_t loKs = loK + ((st * kQTile) >> 4);
 #pragma unroll
           for (int g = 0; g < kQKSubs; ++g) {
-            uint64_t da[4], db[4];
+            uint32_t da[4], db[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint64_t off = static_cast<uint64_t>((g * kSub + k * 32) >> 4);
-              da[k] = dQ + off;
-              db[k] = dKs + off;
+              const uint32_t off = (g * kSub + k * 32) >> 4;
+              da[k] = loQ + off;
+              db[k] = loKs + off;
             }
-            mma_ss_x4(tS, da, db, idS, g > 0 ? 1u : 0u);
+            mma_ss_x4_lo(tS, da, hiK, db, hiK, idS, g > 0 ? 1u : 0u);
           }
           mma_commit(&bars->s_full[t]);
         }
@@ -215,14 +219,13 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           tc_fence_after();
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            uint32_t ta[4];
-            uint64_t db[4];
+            uint32_t ta[4], db[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               ta[k] = tS + 8 * (4 * g + k);
-              db[k] = dV + static_cast<uint64_t>((2048 * (4 * g + k)) >> 4);
+              db[k] = loV + ((2048 * (4 * g + k)) >> 4);
             }
-            mma_ts_x4(tO, ta, db, idO, (npv > 0 || g > 0) ? 1u : 0u);
+            mma_ts_x4_lo(tO, ta, db, hiV, idO, (npv > 0 || g > 0) ? 1u : 0u);
           }
           ++npv;
           if (j == last) mma_commit(&bars->o_done[t]);

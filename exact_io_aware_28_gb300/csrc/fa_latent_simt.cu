@@ -223,13 +223,13 @@ latent_fwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn
 
 // DQ = false: the CTA owns keys and streams queries (dK, dV); DQ = true: the other way (dQ).
 template <bool DQ, int RT>
-__global__ void __launch_bounds__(kThreads)
-latent_bwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn,
-                       const float* __restrict__ kr, const float* __restrict__ v,
-                       const float* __restrict__ lse, const float* __restrict__ dO,
-                       const float* __restrict__ Dsum, float* __restrict__ dq,
-                       float* __restrict__ dkn, float* __restrict__ dkr_part,
-                       float* __restrict__ dv, LatentProblem p) {
+__device__ __forceinline__ void bwd_tile(const float* __restrict__ q, const float* __restrict__ kn,
+                                         const float* __restrict__ kr, const float* __restrict__ v,
+                                         const float* __restrict__ lse,
+                                         const float* __restrict__ dO,
+                                         const float* __restrict__ Dsum, float* __restrict__ dq,
+                                         float* __restrict__ dkn, float* __restrict__ dkr_part,
+                                         float* __restrict__ dv, const LatentProblem& p) {
   constexpr int R = 16 * RT;
   extern __shared__ float4 smem4[];
   float* ox = reinterpret_cast<float*>(smem4);   // owned: q or k, [R][kSX]
@@ -331,6 +331,21 @@ latent_bwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn
   }
 }
 
+// Both in one grid (z): neither needs the other, and short sequences do not fill the card twice.
+template <int RT>
+__global__ void __launch_bounds__(kThreads)
+latent_bwd_simt_kernel(const float* __restrict__ q, const float* __restrict__ kn,
+                       const float* __restrict__ kr, const float* __restrict__ v,
+                       const float* __restrict__ lse, const float* __restrict__ dO,
+                       const float* __restrict__ Dsum, float* __restrict__ dq,
+                       float* __restrict__ dkn, float* __restrict__ dkr_part,
+                       float* __restrict__ dv, LatentProblem p) {
+  if (blockIdx.z == 0)
+    bwd_tile<false, RT>(q, kn, kr, v, lse, dO, Dsum, dq, dkn, dkr_part, dv, p);
+  else
+    bwd_tile<true, RT>(q, kn, kr, v, lse, dO, Dsum, dq, dkn, dkr_part, dv, p);
+}
+
 __device__ __forceinline__ float4 load4(const float* p) {
   return *reinterpret_cast<const float4*>(p);
 }
@@ -396,11 +411,11 @@ bool wide_rows(const LatentProblem& p) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_tiles(void (*kernel)(KArgs...), int smem, int rows, const LatentProblem& p,
-                         cudaStream_t s, Args... args) {
+cudaError_t launch_tiles(void (*kernel)(KArgs...), int smem, int rows, int passes,
+                         const LatentProblem& p, cudaStream_t s, Args... args) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((p.N + rows - 1) / rows, p.B * p.H);
+  const dim3 grid((p.N + rows - 1) / rows, p.B * p.H, passes);
   kernel<<<grid, kThreads, smem, s>>>(args..., p);
   return cudaGetLastError();
 }
@@ -408,18 +423,15 @@ cudaError_t launch_tiles(void (*kernel)(KArgs...), int smem, int rows, const Lat
 template <int RT>
 cudaError_t fwd_rows(const LatentProblem& p, const float* q, const float* kn, const float* kr,
                      const float* v, float* o, float* o_acc, float* lse, cudaStream_t s) {
-  return launch_tiles(latent_fwd_simt_kernel<RT>, fwd_smem<RT>(), 16 * RT, p, s, q, kn, kr, v, o,
-                      o_acc, lse);
+  return launch_tiles(latent_fwd_simt_kernel<RT>, fwd_smem<RT>(), 16 * RT, 1, p, s, q, kn, kr, v,
+                      o, o_acc, lse);
 }
 
 template <int RT>
 cudaError_t bwd_rows(const LatentProblem& p, const float* q, const float* kn, const float* kr,
                      const float* v, const float* lse, const float* dO, const float* Dsum,
                      float* dq, float* dkn, float* dkr_part, float* dv, cudaStream_t s) {
-  cudaError_t e = launch_tiles(latent_bwd_simt_kernel<false, RT>, bwd_smem<RT>(), 16 * RT, p, s, q,
-                               kn, kr, v, lse, dO, Dsum, dq, dkn, dkr_part, dv);
-  if (e != cudaSuccess) return e;
-  return launch_tiles(latent_bwd_simt_kernel<true, RT>, bwd_smem<RT>(), 16 * RT, p, s, q, kn, kr, v,
+  return launch_tiles(latent_bwd_simt_kernel<RT>, bwd_smem<RT>(), 16 * RT, 2, p, s, q, kn, kr, v,
                       lse, dO, Dsum, dq, dkn, dkr_part, dv);
 }
 

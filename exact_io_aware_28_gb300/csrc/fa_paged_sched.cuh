@@ -64,6 +64,7 @@ __device__ __forceinline__ void find_start(Start* out, long long* scratch,
   const int per = (B + THREADS - 1) / THREADS;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long sum = 0;
+#pragma unroll 4
   for (int b = b0; b < b1; ++b)
     sum += static_cast<long long>(granules<KEYS>(clamp_len(cache_len, b, cap))) * heads;
   long long incl = sum;
@@ -134,12 +135,11 @@ struct Walk {
       const int n = granules<KEYS>(L);
       const long long all = static_cast<long long>(n) * heads;
       if (at < before + all) {
-        const int in = static_cast<int>(at - before);
         sg.b = b;
-        sg.head = in / n;
+        sg.head = static_cast<int>((at - before) / n);
         sg.len = L;
         sg.pair_start = before + static_cast<long long>(sg.head) * n;
-        const int g0 = in - sg.head * n;
+        const int g0 = static_cast<int>(at - sg.pair_start);
         const int g1 = static_cast<int>(min(static_cast<long long>(n), last - sg.pair_start));
         sg.k0 = g0 * KEYS;
         sg.k1 = min(g1 * KEYS, L);

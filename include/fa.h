@@ -27,8 +27,9 @@
  * by the caller; the library allocates no device memory per call.  Tensor pointers must be
  * 16-byte aligned.  Calls are asynchronous on `stream` (a cudaStream_t passed as void*;
  * NULL is the legacy default stream): outputs are valid once the stream has synchronised.
- * The kernels of fa_fwd, fa_fwd_dropout and the three backward stages are launched with
- * programmatic stream serialization: one may be scheduled while the previous kernel in the
+ * The kernels of fa_fwd, fa_fwd_dropout, the three backward stages and of the paged-cache and
+ * latent entry points (fp32 latent attention excepted) are launched with programmatic stream
+ * serialization: one may be scheduled while the previous kernel in the
  * stream is still running, but it reads and writes global memory only after that kernel
  * has completed, so stream order holds as for ordinary launches (also inside a captured
  * CUDA graph, which keeps the attribute).
@@ -348,9 +349,9 @@ fa_status fa_grad_finish(void* out, const float* acc, long long n, fa_dtype dtyp
  *   slots       out: int32 [n_slots], the slot of every packed new token; -1 for a token in a hole
  *                 and for the rows behind the last token.  May be shorter than the tokens are.
  *   pages_taken out: int32 [1], pages the step needs; more than n_free: the list was too short.
- * Requests take pages in order.  FA_ERR_INVALID_ARG if cache_len, new_len or free_pages shares
- * memory with an output.
- * FA_ERR_UNSUPPORTED for B > 8192 or B * max_pages * page_size >= 2^31.
+ * Requests take pages in order.  FA_ERR_INVALID_ARG if an output shares memory with an input or
+ * another output.  FA_ERR_UNSUPPORTED for B > 8192, n_slots > 2^30 or
+ * B * max_pages * page_size >= 2^31.
  */
 fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
                           const int32_t* free_pages, int n_free, int32_t* block_table,

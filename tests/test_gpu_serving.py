@@ -130,7 +130,7 @@ def test_two_streams_with_a_workspace_each():
 
 
 def test_inputs_of_another_stream_may_be_dropped():
-    # the helper keeps its inputs' memory until the named stream's work is done
+    # the default stream by its handle; the helper keeps its inputs' memory until the named stream's work is done
     side = torch.cuda.Stream()
     g = _gen(6)
     base = torch.randn(1, 4, 700, 192, generator=g).bfloat16().cuda()
@@ -146,7 +146,10 @@ def test_inputs_of_another_stream_may_be_dropped():
         torch.cuda.current_stream().wait_stream(side)
         ref = (o, lse) if ref is None else ref
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    x = [t.contiguous() for t in (base, base[..., :128], base[:, 0, :, :64], base[..., 64:])]
+    o, lse = fa.latent_forward(*x, True, stream=0)
     _ok()
+    assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
 
 
 def test_expanded_and_absorbed_forms_agree():

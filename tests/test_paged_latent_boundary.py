@@ -36,6 +36,8 @@ TABLES = dict(cl=A, nl=A + 0x1000, free=A + 0x2000, n_free=8, table=A + 0x3000, 
     ({"total": A}, INV),                    # in place over an input that other blocks still read
     ({"start": A + 0x1000 - 16}, INV), ({"slots": A + 0x2010}, INV), ({"taken": A + 12}, INV),
     ({"table": A + 0x2000 - 4 * (3 * 16 + 15)}, INV),
+    ({"slots": A + 0x4008}, INV), ({"taken": A + 0x3000}, INV),   # outputs over one another
+    ({"n_slots": (1 << 30) + 1, "slots": A + (1 << 33)}, UNS),
 ])
 def test_tables_rejects(kw, code):
     assert _call("fa_paged_tables", TABLES, kw) == code
