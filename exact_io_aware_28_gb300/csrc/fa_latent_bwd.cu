@@ -1,7 +1,7 @@
 // Expanded latent attention, backward, on sm_103a tensor cores (tcgen05 + TMA), bf16 in, fp32
 // accumulation.  The formulas stand in fa_latent_simt.cu.
 //
-// Two kernels of one template, without atomics (the result does not depend on scheduling):
+// Two kinds of CTAs of one template, without atomics (the result does not depend on scheduling):
 //   dK, dV  a CTA owns 128 keys of a head (k, v stay in shared memory) and streams the blocks of
 //           128 query rows that may see them:
 //             S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;
@@ -98,11 +98,12 @@ __device__ __forceinline__ float exponent_of(float lse) {
 }
 
 // DQ = false: X = q, Y = dO streamed, k and v owned.  DQ = true: k, v streamed, q and dO owned.
+// `cta`: its number among those of its kind.
 template <bool DQ>
-__global__ void __launch_bounds__(kThreads, 1)
-latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkn,
-                  const __grid_constant__ CUtensorMap mkr, const __grid_constant__ CUtensorMap mv,
-                  const __grid_constant__ CUtensorMap mdo, BwdArgs a, LatentProblem p) {
+__device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap& mkn,
+                                        const CUtensorMap& mkr, const CUtensorMap& mv,
+                                        const CUtensorMap& mdo, const BwdArgs& a,
+                                        const LatentProblem& p, int cta) {
   constexpr uint32_t kAccX = DQ ? 0 : kV;            // columns of dQ or dK (dV sits before dK)
   constexpr uint32_t kS = kAccX + kQK;               // the scores
   constexpr uint32_t kDP = DQ ? kS + 128 : kS;       // dP
@@ -130,7 +131,7 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
   {
     const int G = static_cast<int>(max(1ll, min(static_cast<long long>(bhs),
                                                 (64ll << 20) / (640ll * p.N))));
-    const int x = blockIdx.x, g = x / (G * tiles), r = x - g * G * tiles;
+    const int g = cta / (G * tiles), r = cta - g * G * tiles;
     const int Gg = min(G, bhs - g * G);
     bh = g * G + r % Gg;
     row0 = (DQ ? tiles - 1 - r / Gg : r / Gg) * kRows;
@@ -531,9 +532,29 @@ latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
   }
 }
 
-template <bool DQ>
-cudaError_t launch_one(const LatentProblem& p, const void* q, const void* kn, const void* kr,
-                       const void* v, const void* dO, const BwdArgs& a, cudaStream_t s) {
+// Both kinds in one grid, dK, dV first (their CTAs take longer): neither needs the other, and the
+// second fills the SMs that the first leaves idle at its end (short sequences: from the start).
+__global__ void __launch_bounds__(kThreads, 1)
+latent_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkn,
+                  const __grid_constant__ CUtensorMap mkr, const __grid_constant__ CUtensorMap mv,
+                  const __grid_constant__ CUtensorMap mdo, BwdArgs a, LatentProblem p) {
+  const int half = gridDim.x / 2, cta = blockIdx.x;
+  if (cta < half)
+    bwd_cta<false>(mq, mkn, mkr, mv, mdo, a, p, cta);
+  else
+    bwd_cta<true>(mq, mkn, mkr, mv, mdo, a, p, cta - half);
+}
+
+constexpr int kSmem = Lay<false>::SMEM > Lay<true>::SMEM ? Lay<false>::SMEM : Lay<true>::SMEM;
+
+}  // namespace
+
+cudaError_t launch_latent_bwd_sm103(const LatentProblem& p, const void* q, const void* kn,
+                                    const void* kr, const void* v, const float* lse,
+                                    const void* dO, const float* Dsum, void* dq, void* dkn,
+                                    float* dkr_part, void* dv, cudaStream_t s) {
+  BwdArgs a{static_cast<const __nv_bfloat16*>(dO), lse, Dsum, static_cast<__nv_bfloat16*>(dq),
+            static_cast<__nv_bfloat16*>(dkn), dkr_part, static_cast<__nv_bfloat16*>(dv)};
   CUtensorMap mq, mkn, mkr, mv, mdo;
   const int BH = p.B * p.H;
   if (!make_head_map(&mq, q, BH, p.N, kQK) || !make_head_map(&mkn, kn, BH, p.N, FA_LATENT_NOPE) ||
@@ -544,27 +565,14 @@ cudaError_t launch_one(const LatentProblem& p, const void* q, const void* kn, co
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel<DQ>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DQ>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   const long long tiles = (p.N + kRows - 1) / kRows;
-  return launch_dependent(latent_bwd_kernel<DQ>, dim3(static_cast<unsigned>(BH * tiles)),
-                          dim3(kThreads), Lay<DQ>::SMEM, s, mq, mkn, mkr, mv, mdo, a, p);
-}
-
-}  // namespace
-
-cudaError_t launch_latent_bwd_sm103(const LatentProblem& p, const void* q, const void* kn,
-                                    const void* kr, const void* v, const float* lse,
-                                    const void* dO, const float* Dsum, void* dq, void* dkn,
-                                    float* dkr_part, void* dv, cudaStream_t s) {
-  BwdArgs a{static_cast<const __nv_bfloat16*>(dO), lse, Dsum, static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dkn), dkr_part,
-            static_cast<__nv_bfloat16*>(dv)};
-  cudaError_t e = launch_one<false>(p, q, kn, kr, v, dO, a, s);
-  if (e != cudaSuccess) return e;
-  return launch_one<true>(p, q, kn, kr, v, dO, a, s);
+  return launch_dependent(latent_bwd_kernel, dim3(static_cast<unsigned>(2 * BH * tiles)),
+                          dim3(kThreads), kSmem, s, mq, mkn, mkr, mv, mdo, a, p);
 }
 
 }  // namespace fa

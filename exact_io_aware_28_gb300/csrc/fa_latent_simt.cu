@@ -17,7 +17,7 @@
 // step of 2 x 3 heads x 333 rows).  So both products of a tile are register tiles: a CTA of
 // 16 x 16 threads owns 16 RT rows and streams 64 rows at a time; a thread forms RT x 4 scores
 // from four columns of a row per 16-byte load, and RT x 4 of every 64 columns of the result from
-// P or dS in shared memory (203 us).  Scores are in the log2 domain.
+// P or dS in shared memory (140 us).  Scores are in the log2 domain.
 #include <math.h>
 
 #include "fa_internal.cuh"
