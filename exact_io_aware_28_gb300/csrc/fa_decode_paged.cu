@@ -29,8 +29,8 @@
 // Work: fa_paged_sched.cuh cuts the line of all tiles into one range per CTA, one CTA per SM.
 // A pair inside one range is finished there; only pairs that a range's end cuts go through the
 // workspace and the combine kernel, at most two partial results a CTA.
-//   warp 0     producer (a lane per page);      warps 1, 3  MMA issuers (one thread each);
-//   warp 2     tensor memory;                   warps 4-11  softmax, thread = key row.
+//   warps 0, 2 producers (a lane per page);     warps 1, 3  MMA issuers (one thread each);
+//   warps 4-11 softmax, thread = key row.
 // Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and leaves.
 #include <atomic>
 
@@ -138,7 +138,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->full[s], 2);
       mbar_init(&bars->empty[s], 1);
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_full[s], 128);
@@ -175,10 +175,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   sched::Walk<kKeys> walk(start, a.cache_len, a.Hkv, cap);
   Segment sg;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    // Lane i < boxes takes the i-th page of every tile (all of a tile's rows when pages hold
-    // 128 tokens or more).
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA producers
+    // Warp 0 has the queries and the keys, warp 2 the values: one warp issues a box in some 70
+    // cycles, and small pages make many.  Lane i < boxes takes the i-th page of every tile (all of
+    // a tile's rows when pages hold 128 tokens or more).
+    const bool keys = warp == 0;
+    const CUtensorMap* map = keys ? &mk : &mv;
     const int shift = a.page_shift;
     const int rows = min(kKeys, 1 << shift);        // rows of a box
     const int boxes = kKeys / rows;
@@ -187,11 +190,11 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     int n = 0, nu = 0;
     while (ok && walk.next(sg)) {
       const int qb = nu & 1;
-      if (nu >= 2) {
+      if (keys && nu >= 2) {
         ok = mbar_wait_warp(&bars->q_empty[qb], ((nu >> 1) - 1) & 1, abort_flag, a.err, a.wait_ns);
         if (!ok) break;
       }
-      if (lane == 0) {
+      if (keys && lane == 0) {
         mbar_arrive_expect_tx(&bars->q_full[qb], kQBytes);
         for (int s = 0; s < C::NSUB; ++s)
           tma_load_3d(sQ + qb * kQBytes + s * (kN * 128), &mq, &bars->q_full[qb], 64 * s,
@@ -211,21 +214,22 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
           if (!ok) break;
         }
         if (lane == 0) {
-          uint32_t seen = 0;
-          for (int i = 0; i < boxes; ++i)
-            if (pages >> i & 1u) seen |= bits << (i * (rows / 16));
-          bars->seen[st] = seen;
+          if (keys) {
+            uint32_t seen = 0;
+            for (int i = 0; i < boxes; ++i)
+              if (pages >> i & 1u) seen |= bits << (i * (rows / 16));
+            bars->seen[st] = seen;
+          }
           mbar_arrive_expect_tx(&bars->full[st],
-                                static_cast<uint32_t>(__popc(pages)) * rows * D * 4);
+                                static_cast<uint32_t>(__popc(pages)) * rows * D * 2);
         }
         __syncwarp();
         if (in) {
-          uint8_t* dst = sKV + st * kStage + lane * rows * 128;
+          uint8_t* dst = sKV + st * kStage + (keys ? 0 : C::NSUB) * kSub + lane * rows * 128;
           const int y = x & ((1 << shift) - 1);     // its first row within the page
-          for (int s = 0; s < C::NSUB; ++s) {
-            tma_load_4d(dst + s * kSub, &mk, &bars->full[st], 64 * s, y, sg.head, p);
-            tma_load_4d(dst + (C::NSUB + s) * kSub, &mv, &bars->full[st], 64 * s, y, sg.head, p);
-          }
+#pragma unroll
+          for (int s = 0; s < C::NSUB; ++s)
+            tma_load_4d(dst + s * kSub, map, &bars->full[st], 64 * s, y, sg.head, p);
         }
       }
       ++nu;
