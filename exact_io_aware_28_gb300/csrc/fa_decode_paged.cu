@@ -6,7 +6,7 @@
 // in the pool, in one pass with a running maximum m and sum l per head (log2 domain, c = scale
 // log2 e); parts of a sequence computed by different CTAs join as o = sum 2^(m_i - M) o_i /
 // sum 2^(m_i - M) l_i.  m, l, the scores and o are fp32; P is rounded once to bf16 as an
-// operand of P V (half a step, 2^-9 of each weight's magnitude class, as the output's own).
+// operand of P V: each weight is off by half a step, 2^-8 of its value, as the output itself is.
 //
 // What bounds it: every key and value row is read once, 4 d bytes for 4 G d operations, so HBM
 // does.  The two products go to the tensor cores with the keys as M, so that the G heads cost
@@ -31,6 +31,10 @@
 // workspace and the combine kernel, at most two partial results a CTA.
 //   warps 0, 2 producers (a lane per page);     warps 1, 3  MMA issuers (one thread each);
 //   warps 4-11 softmax, thread = key row.
+// Measured: d = 128, 32 query and 8 key/value heads, 64 sequences of 8192: 309 us, 6.95 TB/s, the
+// rate of a plain copy.  d = 64, 24 and 8 heads, 48 ragged sequences to 5001: 60 us for 37 us of
+// bytes, of which some 12 us do not grow with the lengths; pages of 16 tokens cost 12% more than
+// pages of 256 at d = 64 and 4% at d = 128 (boxes of 2 KB and 4 KB).
 // Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and leaves.
 #include <atomic>
 

@@ -21,8 +21,8 @@
 //           S(n + 1) starts as soon as the softmax warps have read S(n).
 // Of shared memory the owned rows hold 80 KB (dQ: 48, which makes room for a third stage of X);
 // the streamed side X (q or k, 192 columns: scores early, gradient product late) has two or three
-// stages of 48 KB and Y (dO or v, 128) one of 32.  Both lie as [128 rows][64 columns] subtiles that the score products read K-major and the gradient
-// products MN-major.
+// stages of 48 KB and Y (dO or v, 128) one of 32.  Both lie as [128 rows][64 columns] subtiles
+// that the score products read K-major and the gradient products MN-major.
 //   warp 0 producer; warps 1, 3 MMA issuers; warp 2 tensor memory and (dK, dV) the block's lse and
 //   D; warps 4-11 softmax, two threads a row, 64 columns each.
 // Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and exits.

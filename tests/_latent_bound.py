@@ -8,10 +8,11 @@ are off by a relative G of each term:
                      dP, D and P), for the shared k_rope summed over the heads
     |lse - ref|   <= g (1 + |lse_ref|)
 G: a score is a sum of at most 576 fp32 products, so it is off by at most 576 * 2^-24 of the sum
-of their absolute values (below 64 for the standard normal inputs used here, after the scale):
-0.0022 at the worst and in the mean, the errors being of either sign, near sqrt(576) 2^-24 of
-it; G = 2^-10 leaves room for the exponent (2^-22), the sums over up to 1000 keys (1000 * 2^-24)
-and lse's own rounding.  For fp32 the operands are not rounded: u = 2^-24 for the result, g = 2^-13.
+of their absolute values (below 64 for the standard normal inputs used here, after the scale).
+That would be 0.0022 with every error at its largest and of one sign; being of either sign they
+add up to some sqrt(576) 2^-24 of the sum, 0.0001.  G = 2^-10 is ten times that, which leaves
+room for the exponent (2^-22), the sums over up to 1000 keys (1000 * 2^-24) and lse's own
+rounding.  For fp32 the operands are not rounded: u = 2^-24 for the result, g = 2^-13.
 """
 import numpy as np
 
