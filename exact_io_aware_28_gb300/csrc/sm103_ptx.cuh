@@ -127,6 +127,30 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 
 // ------------------------------------------------------------------ fences
 
+// Cluster launch control: asks for a block of this grid that has not started yet; its index (or
+// that there is none left) lands as 16 bytes at dst, which complete as a transaction of bar.  No
+// further request after one that found none.
+__device__ __forceinline__ void next_block_request(void* dst, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+      ::"r"(smem_u32(dst)), "r"(smem_u32(bar))
+      : "memory");
+}
+// The answer: the block's index (x), or -1.
+__device__ __forceinline__ int next_block_answer(const void* src) {
+  int x;
+  asm volatile(
+      "{\n .reg .b128 r;\n .reg .pred p;\n"
+      " ld.shared.b128 r, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+      " mov.b32 %0, -1;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n}"
+      : "=r"(x)
+      : "r"(smem_u32(src))
+      : "memory");
+  return x;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
