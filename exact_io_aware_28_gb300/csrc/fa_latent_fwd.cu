@@ -340,7 +340,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       float l_part[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
       bool any[2] = {false, false};
       for (int j = 0; j < jend && ok; ++j, ++n_v) {
-  #pragma unroll
+#pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || !need(p, u, t, j)) continue;
           ok = mbar_wait_warp(&bars->s_full[t], n_s[t] & 1, abort_flag, p.err, p.wait_ns);
@@ -349,7 +349,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           uint32_t v[64];
           tmem_ld_16x256b_x16_wait(lane_base + t * 128, v);
           float sv[64];
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 64; ++i) sv[i] = __uint_as_float(v[i]);
           const int k0 = j * kBlk;
           const int row0 = u.q0 + t * kBlk;
@@ -358,7 +358,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             const int lim_len = u.L - 1 - k0;
             const int limA = min(p.causal ? row0 + rA - k0 : kBlk - 1, lim_len);
             const int limB = min(p.causal ? row0 + rB - k0 : kBlk - 1, lim_len);
-  #pragma unroll
+#pragma unroll
             for (int cc = 0; cc < 16; ++cc) {
               const int key = 8 * cc + 2 * t4;
               if (key > limA) sv[4 * cc] = -INFINITY;
@@ -369,7 +369,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           }
           float ma0 = fmaxf(sv[0], sv[1]), ma1 = fmaxf(sv[4], sv[5]);
           float mb0 = fmaxf(sv[2], sv[3]), mb1 = fmaxf(sv[6], sv[7]);
-  #pragma unroll
+#pragma unroll
           for (int cc = 2; cc < 16; cc += 2) {
             ma0 = fmax3(ma0, sv[4 * cc], sv[4 * cc + 1]);
             mb0 = fmax3(mb0, sv[4 * cc + 2], sv[4 * cc + 3]);
@@ -394,7 +394,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           const uint64_t nA = f2_pack(-useA, -useA), nB = f2_pack(-useB, -useB);
           uint64_t accA = f2_pack(0.f, 0.f), accB = accA;
           uint32_t pk[32];
-  #pragma unroll
+#pragma unroll
           for (int cc = 0; cc < 16; ++cc) {
             const float2 xa = f2_unpack(ffma2(f2_pack(sv[4 * cc], sv[4 * cc + 1]), c2, nA));
             const float2 xb = f2_unpack(ffma2(f2_pack(sv[4 * cc + 2], sv[4 * cc + 3]), c2, nB));
@@ -415,12 +415,12 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           m_run[t][1] = newB;
           // Rescale the running O (the P V products issued before the S just read are done).
           if (any[t] && __any_sync(0xffffffffu, chA || chB)) {
-  #pragma unroll
+#pragma unroll
             for (int half = 0; half < kVSubs; ++half) {
               uint32_t o[32];
               const uint32_t oaddr = lane_base + 256 + t * 128 + 64 * half;
               tmem_ld_16x256b_x8_wait(oaddr, o);
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 32; ++i)
                 o[i] = __float_as_uint(__uint_as_float(o[i]) * ((i & 2) ? alphaB : alphaA));
               tmem_st_16x256b_x8(oaddr, o);
@@ -434,7 +434,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             const int row = (tid - 128) >> 1;
             if (k0 + row >= u.L) {
               uint4* vr = reinterpret_cast<uint4*>(sV + (tid & 1) * kSub + row * 128);
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 8; ++i) vr[i] = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
@@ -447,7 +447,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         }
       }
       // ------------------------------------------------------------ epilogue
-  #pragma unroll
+#pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (ok && any[t]) {
           ok = mbar_wait_warp(&bars->o_done[t], n_o[t] & 1, abort_flag, p.err, p.wait_ns);
@@ -464,22 +464,22 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         const int rowA = u.q0 + t * kBlk + rA, rowB = rowA + 8;
         // O / l as bf16.  The four threads of a row exchange their column pairs so that each
         // stores 16 bytes, 64 in a row; the fp32 O, where asked for, goes out as it lies.
-  #pragma unroll
+#pragma unroll
         for (int half = 0; half < kVSubs; ++half) {
           uint32_t ov[32];
           if (any[t]) {
             tmem_ld_16x256b_x8_wait(lane_base + 256 + t * 128 + 64 * half, ov);
           } else {
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < 32; ++k) ov[k] = 0u;
           }
-  #pragma unroll
+#pragma unroll
           for (int ab = 0; ab < 2; ++ab) {
             const int row = ab ? rowB : rowA;
             const float inv = ab ? invB : invA;
             const size_t at = (static_cast<size_t>(u.bh) * p.N + row) * FA_LATENT_V + 64 * half;
             uint32_t w[8];
-  #pragma unroll
+#pragma unroll
             for (int cc = 0; cc < 8; ++cc) {
               const float x0 = __uint_as_float(ov[4 * cc + 2 * ab]) * inv;
               const float x1 = __uint_as_float(ov[4 * cc + 2 * ab + 1]) * inv;
@@ -487,7 +487,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
               if (o_acc && row < p.N)
                 *reinterpret_cast<float2*>(o_acc + at + 8 * cc + 2 * t4) = make_float2(x0, x1);
             }
-  #pragma unroll
+#pragma unroll
             for (int c4 = 0; c4 < 2; ++c4) {
               const uint4 x = quad_transpose(w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2],
                                              w[4 * c4 + 3], t4);
