@@ -65,7 +65,6 @@ constexpr int kRestSubs = kRow / 64 - kOwnSubs;   // the other half's, then the 
 constexpr int kQSub = kHeads * 128;           // [128 heads][64 columns], 16 KB
 constexpr int kThreads = 384;
 constexpr uint32_t kTS = kHalf, kTQ = kHalf + kKeys;       // columns of S and of Q's own half
-constexpr int kMaxWorkers = 512;              // the combine kernel's table of parts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units; exact, see fa_fwd_sm103.cu
@@ -477,26 +476,34 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
   }
 }
 
-// One block per (b, h): joins the parts of a sequence that more than one worker had; o = 0,
-// lse = -inf for an empty sequence.  Each half of the columns has statistics of its own (its
-// CTAs add the score products in another order): THREADS / 2 threads form a half's weights, and
-// the rows are added by groups of 128 threads (four columns a thread), each part to one group.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) latent_combine_kernel(LatentArgs a, int workers) {
-  constexpr int GROUPS = THREADS / 128, PER = THREADS / 2;
-  __shared__ float weight[2][kMaxWorkers];
-  __shared__ float red[2][THREADS / 32];
-  __shared__ float4 rows[GROUPS][128];
+// Joins the parts of a sequence that more than one worker had; o = 0, lse = -inf for an empty
+// sequence.  A warp adds a quarter of the columns (four a lane) of HEADS heads.  Each half of the
+// columns has statistics of its own (its CTAs add the score products in another order), which
+// every warp reads for itself, a part in a lane: no barrier.  What it costs is a chain of loads
+// (prefix, statistics, rows), so the rows of the first parts are asked for with the statistics.
+//   GROUPS = 1  block = the four quarters of HEADS heads of a sequence;
+//   GROUPS > 1  block = one quarter of one head, each warp with its share of the parts.
+template <int GROUPS, int HEADS>
+__global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS)
+latent_combine_kernel(LatentArgs a, int workers) {
+  static_assert(GROUPS == 1 || HEADS == 1, "a block's share");
+  constexpr int kAhead = GROUPS == 1 ? 4 : 8;
+  __shared__ float4 rows[GROUPS][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const size_t head = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = GROUPS == 1 ? 0 : warp, quarter = GROUPS == 1 ? warp : blockIdx.x & 3;
+  const int hc = quarter >> 1, col = 32 * quarter + lane;   // columns 4 col ... of half hc
+  const int per = (a.H + HEADS - 1) / HEADS, unit = GROUPS == 1 ? blockIdx.x : blockIdx.x >> 2;
+  const int b = unit / per, h0 = unit % per * HEADS, heads = min(HEADS, a.H - h0);
+  const size_t head0 = static_cast<size_t>(b) * a.H + h0;
   const long long p0 = a.prefix[b], p1 = a.prefix[b + 1], total = a.prefix[a.B];
   if (p0 == p1) {
-    if (tid < kRank / 8)
-      reinterpret_cast<uint4*>(a.o + head * kRank)[tid] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid == 0) a.lse[head] = -INFINITY;
+    for (int k = 0; k < heads; ++k) {
+      if (g == 0)
+        reinterpret_cast<uint2*>(a.o + (head0 + k) * kRank)[col] = make_uint2(0u, 0u);
+      if (g == 0 && col == 0) a.lse[head0 + k] = -INFINITY;
+    }
     return;
   }
   workers = sched::active(total, workers);
@@ -506,60 +513,71 @@ __global__ void __launch_bounds__(THREADS) latent_combine_kernel(LatentArgs a, i
   // Only the first part can sit in the second of its worker's slots.
   const int slot0 = sched::slot(p0, sched::range_start(total, w0, workers), w0);
   auto slot = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
-  const int half = tid / PER, ht = tid - half * PER;
-  auto stat = [&](int i) { return a.stat[(static_cast<size_t>(slot(i)) * 2 + half) * a.H + h]; };
-  float M = -INFINITY;
-  for (int i = ht; i < parts; i += PER) M = fmaxf(M, stat(i).x);
-  M = warp_max(M);
-  if (lane == 0) red[0][warp] = M;
-  __syncthreads();
-  M = -INFINITY;
+  auto row = [&](int i, int k) {
+    return reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(slot(i)) * a.H + h0 + k) *
+                                                        kRank)[col];
+  };
+  auto stat = [&](int i, int k) {
+    return i < parts ? a.stat[(static_cast<size_t>(slot(i)) * 2 + hc) * a.H + h0 + k]
+                     : make_float2(-INFINITY, 0.f);
+  };
+  const int i0 = parts * g / GROUPS, i1 = parts * (g + 1) / GROUPS;
+  float4 first[HEADS][kAhead];
+  float2 own[HEADS];
 #pragma unroll
-  for (int i = 0; i < PER / 32; ++i) M = fmaxf(M, red[0][half * (PER / 32) + i]);
-  if (M == -INFINITY) M = 0.f;
-  float l = 0.f;
-  for (int i = ht; i < parts; i += PER) {
-    const float2 s = stat(i);
-    const float w = ex2(s.x - M);   // a part without a visible key (-inf) weighs 0
-    weight[half][i] = w;
-    l += s.y * w;
+  for (int k = 0; k < HEADS; ++k) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      first[k][i] = k < heads && i0 + i < i1 ? row(i0 + i, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    own[k] = k < heads ? stat(lane, k) : make_float2(-INFINITY, 0.f);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
-  const int g = tid >> 7, col = tid & 127, hc = col >> 6;   // columns 4 col ... of half hc
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = g; i < parts; i += GROUPS) {
-    const float w = weight[hc][i];
-    const float4 v = reinterpret_cast<const float4*>(
-        a.part + (static_cast<size_t>(slot(i)) * a.H + h) * kRank)[col];
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  if constexpr (GROUPS > 1) {
-    rows[g][col] = acc;
-    __syncthreads();
-    if (g > 0) return;
-#pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-      const float4 v = rows[i][col];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+  for (int k = 0; k < HEADS; ++k) {
+    if (k >= heads) break;
+    float M = own[k].x;
+    for (int i = 32; i < parts; i += 32) M = fmaxf(M, stat(i + lane, k).x);
+    M = warp_max(M);
+    if (M == -INFINITY) M = 0.f;
+    float l = own[k].y * ex2(own[k].x - M);   // a part without a visible key (-inf) weighs 0
+    for (int i = 32; i < parts; i += 32) {
+      const float2 s = stat(i + lane, k);
+      l += s.y * ex2(s.x - M);
     }
-  }
-  l = 0.f;
 #pragma unroll
-  for (int i = 0; i < PER / 32; ++i) l += red[1][hc * (PER / 32) + i];
-  const float inv = l == 0.f ? 0.f : 1.f / l;   // a NaN sum stays one
-  reinterpret_cast<uint2*>(a.o + head * kRank)[col] =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (tid == 0) a.lse[head] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;   // of half 0
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float w, const float4& v) {
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    };
+    for (int c = i0; c < i1; c += 32) {   // the weights of 32 parts, one in a lane
+      const float w = ex2(stat(c + lane, k).x - M);
+      const int n = min(32, i1 - c);
+      int i = 0;
+      if (c == i0) {
+#pragma unroll
+        for (; i < kAhead; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          if (i < n) add(wi, first[k][i]);
+        }
+      }
+#pragma unroll 4
+      for (; i < n; ++i) add(__shfl_sync(0xffffffffu, w, i), row(c + i, k));
+    }
+    if constexpr (GROUPS > 1) {
+      rows[g][lane] = acc;
+      __syncthreads();
+      if (g > 0) return;
+#pragma unroll
+      for (int i = 1; i < GROUPS; ++i) add(1.f, rows[i][lane]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;   // a NaN sum stays one
+    reinterpret_cast<uint2*>(a.o + (head0 + k) * kRank)[col] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (col == 0) a.lse[head0 + k] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
+  }
 }
 
 // Up to 16 heads leave the tensor cores idle here (M = 128) and fit one tile of the warp-level MMA:
@@ -568,7 +586,7 @@ __global__ void __launch_bounds__(THREADS) latent_combine_kernel(LatentArgs a, i
 bool few_heads(int H) { return H <= kFewHeads; }
 
 // Workers, and with it two parts' room each: pairs of CTAs, or CTAs.
-int max_workers(int H) { return std::min(few_heads(H) ? sm_count() : sm_count() / 2, kMaxWorkers); }
+int max_workers(int H) { return few_heads(H) ? sm_count() : sm_count() / 2; }
 
 size_t part_bytes(int H) {
   return 2 * static_cast<size_t>(max_workers(H)) * H * kRank * sizeof(float);
@@ -620,12 +638,19 @@ cudaError_t launch_latent_decode(const void* q, const void* cache, long long pag
                          a);
   }
   if (e != cudaSuccess) return e;
-  // Few sequences: many parts each.
-  const dim3 grid(static_cast<unsigned>(B) * H);
-  return workers > 8 * B ? launch_dependent(latent_combine_kernel<512>, grid, dim3(512), 0, s, a,
-                                            workers)
-                         : launch_dependent(latent_combine_kernel<128>, grid, dim3(128), 0, s, a,
-                                            workers);
+  // Warps to a row by the parts of an average sequence: every block costs a chain of loads, so more
+  // of them only pay where a warp's own sum would be longer (1 x 16 heads, 152 parts: 16, 8, 4 warps
+  // 18.9, 21.6, 24.4 us; 1 x 128, 76 parts: 26.4, 23.0, 24.2; 2 x 128, 38 parts: 8, 4 warps 24.6,
+  // 22.2; 4 x 128, 19 parts: 4, 1 warps 30.3, 33.5; 8 x 128, 9 parts, many rows: 41, 37.5).
+  const unsigned rows = static_cast<unsigned>(B) * H;
+  const int parts = workers / B;
+  auto combine = [&](auto kernel, unsigned blocks, unsigned threads) {
+    return launch_dependent(kernel, dim3(blocks), dim3(threads), 0, s, a, workers);
+  };
+  if (parts >= 128) return combine(latent_combine_kernel<16, 1>, 4 * rows, 512);
+  if (parts >= 64) return combine(latent_combine_kernel<8, 1>, 4 * rows, 256);
+  if (parts >= 8 && rows <= 512) return combine(latent_combine_kernel<4, 1>, 4 * rows, 128);
+  return combine(latent_combine_kernel<1, 2>, static_cast<unsigned>(B) * ((H + 1) / 2), 128);
 }
 
 }  // namespace fa
