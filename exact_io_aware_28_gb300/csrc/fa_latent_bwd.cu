@@ -59,6 +59,7 @@ struct Bars {
   uint64_t dp_full;
   uint64_t p_ready;
   uint64_t ds_ready;
+  uint64_t ds_taken;           // the product with dS's first term has completed
   uint64_t do_ready;           // dQ: the owned dO is in tensor memory
   uint64_t acc_full;
   uint64_t drain;
@@ -151,6 +152,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->p_ready, 256);
     mbar_init(&bars->ds_ready, 256);
+    mbar_init(&bars->ds_taken, 1);
     mbar_init(&bars->do_ready, 256);
     mbar_init(&bars->acc_full, 1);
     mbar_init(&bars->drain, DQ ? 2 : 1);
@@ -173,6 +175,15 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
     L = p.kv_len[seq];
     L = L < 0 ? 0 : (L > p.N ? p.N : L);
   }
+  // A rounding of dS averages out over long sums.  The first queries of a causal sequence see few
+  // keys and have the largest dS (a row over n keys some 1 / n of it), so dq of 4 x 2 heads of two
+  // rows was off by 0.0035 of its norm and by 0.0024 at 300 rows, where one rounding of the result
+  // makes 0.0017.  The first query block's dS therefore goes into its product as two bf16 terms, the
+  // second in the first's place when its product is done: the same instructions once more, since
+  // further MMAs in the issuers' loops slow every block.  A training step of 16 heads x 8192 takes
+  // 1207 us with it and 1186 without, 2 x 8 heads x 1000 62.5 and 61.5; the MMAs side by side
+  // 1213 to 1285, a template for the blocks that need it 1200 but 67 (code read for the first time).
+  const bool fine = row0 == 0 && (p.causal || p.N <= kRows);
   // The streamed rows [begin, end) in blocks of 128.
   const int begin = !DQ && p.causal ? row0 : 0;
   const int end = DQ ? (p.causal ? min(L, row0 + kRows) : L) : (row0 < L ? p.N : begin);
@@ -286,15 +297,27 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
         tc_fence_after();
         return true;
       };
+      // dQ += dS K, dK += dS^T Q, in one term or (the first block) in two.
+      int nd = 0;
+      auto dS_product = [&](int st, int n) -> bool {
+        bool more = fine && n == 0;
+#pragma unroll 1
+        for (bool acc = n > 0;; acc = true) {
+          if (!wait(&bars->ds_ready, nd++)) return false;
+          grads(tb + kAccX, tb + kDS, kDSHalf, dXm + ((st * kX) >> 4), idX, acc);
+          if (!more) return true;
+          more = false;
+          mma_commit(&bars->ds_taken);
+        }
+      };
       bool ok = blocks > 0;
       if (DQ && warp == 3) {
         ok = ok && mbar_wait(&bars->do_ready, 0, abort_flag, p.err, p.wait_ns) && start_dp(0);
         for (int n = 0; ok && n < blocks; ++n) {
           const int st = n % kXStages;
           ok = mbar_wait(&bars->x_full[st], (n / kXStages) & 1, abort_flag, p.err, p.wait_ns) &&
-               wait(&bars->ds_ready, n);
+               dS_product(st, n);
           if (!ok) break;
-          grads(tb, tb + kDS, kDSHalf, dXm + ((st * kX) >> 4), idX, n > 0);
           mma_commit(&bars->x_empty[st]);
           if (n + 1 < blocks) ok = start_dp(n + 1);   // over dS, behind the product that reads it
         }
@@ -312,10 +335,8 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
           if (!ok) break;
           grads(tb, tb + kP, 32, dYm, idV, n > 0);
           mma_commit(&bars->y_empty);
-          ok = wait(&bars->ds_ready, n);
+          ok = dS_product(st, n);
           if (!ok) break;
-          grads(tb + kAccX, tb + kDS, kDSHalf, dXm + ((st * kX) >> 4), idX,
-                n > 0);
           mma_commit(&bars->x_empty[st]);
           if (n + 1 < blocks) ok = start_s(n + 1);
         }
@@ -475,6 +496,25 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars->ds_ready);
+      if (fine && n == 0) {   // what the rounding left
+        ok = mbar_wait_warp(&bars->ds_taken, 0, abort_flag, p.err, p.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = P[32 * q + 2 * i], y = P[32 * q + 2 * i + 1];
+            pk[i] = pack_bf16x2(x - __bfloat162float(__float2bfloat16_rn(x)),
+                                y - __bfloat162float(__float2bfloat16_rn(y)));
+          }
+          tmem_st16(lane_base + kDS + kDSHalf * half + 16 * q, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->ds_ready);
+      }
     }
     // ------------------------------------------------------------ epilogue
     if (ok && blocks > 0) {
