@@ -10,9 +10,10 @@
 // What bounds it: 640 operations a (query, key) pair against 832 bytes a key and 128 queries,
 // so the tensor cores, and beside them the softmax.  As in fa_fwd_sm103.cu a CTA owns two tiles
 // of 128 query rows, one MMA-issuing thread each, and all eight softmax warps take the tiles in
-// turn: 545 us for 16 heads x 8192 without a mask (1.26 PFLOP/s), 4.2k cycles a pair of tiles
+// turn: 555 us for 16 heads x 8192 without a mask (1.24 PFLOP/s), 4.2k cycles a pair of tiles
 // and block of which 2.8k are MMAs.  Softmax warps of a tile's own measured slower, both four (a
-// row per thread, 678 us) and eight (scores read twice, 627 us).
+// row per thread, 678 us) and eight (scores read twice, 627 us), and a P V product in two halves of
+// the keys, the first while the second half of P is formed, gains nothing (566 us).
 // A CTA takes further units of the grid with cluster launch control, for a unit's own cost (Q's and
 // the first K's way from HBM, the first scores, O's way out) is that of two blocks: the roles walk
 // the units on their own, so the next unit's loads and scores run while the softmax warps finish
