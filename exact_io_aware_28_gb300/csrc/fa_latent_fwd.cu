@@ -17,12 +17,13 @@
 // A CTA takes further units of the grid with cluster launch control, for a unit's own cost (Q's and
 // the first K's way from HBM, the first scores, O's way out) is that of two blocks: the roles walk
 // the units on their own, so the next unit's loads and scores run while the softmax warps finish
-// this one (16 heads x 8192, causal: 313 -> 263 us; 4 x 16 x 2000: 97 -> 82).  O goes out from the
-// registers, as Q's buffers are by then the next unit's.
+// this one (causal, 4 x 16 heads x 2000: 90 -> 82 us, 16 x 8192: 268 -> 264; a grid that fits the SMs
+// pays 0.2).  O goes out from the registers, as Q's buffers are by then the next unit's.
 // Of the 227 KB of shared memory Q's two tiles hold 96, two K stages 96 and one V stage 32:
 // V(j + 1) is fetched behind P V(j), while the scores of block j + 1 and their
 // softmax run.  Tensor memory: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).
 // Every mbarrier wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and exits.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkn,
                   const __grid_constant__ CUtensorMap mkr, const __grid_constant__ CUtensorMap mv,
                   __nv_bfloat16* __restrict__ o, float* __restrict__ o_acc,
-                  float* __restrict__ lse, LatentProblem p) {
+                  float* __restrict__ lse, LatentProblem p, int G) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -102,27 +103,24 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // Work unit of a block index: equal groups of heads whose K and V (640 N bytes a head) fit 96 MiB
-  // of L2 (all heads at once: 4% slower at 200 MB; 64 MiB, more groups: 3% at 82 MB, as a group
-  // that starts late ends late); in each group heavy (late, causal) query blocks first, the group's
-  // heads fastest.
-  auto unit = [&](int b) {
+  // Work unit of a block index: groups of G heads; in each group heavy (late, causal) query blocks
+  // first, the group's heads fastest.
+  auto place = [&](int b) {
     const int nqb = (p.N + 2 * kBlk - 1) / (2 * kBlk), bhs = p.B * p.H;
-    const int most = static_cast<int>(max(1ll, min(static_cast<long long>(bhs),
-                                                   (96ll << 20) / (640ll * p.N))));
-    const int groups = (bhs + most - 1) / most, G = (bhs + groups - 1) / groups;
     const int g = b / (G * nqb), r = b - g * G * nqb;
     const int Gg = min(G, bhs - g * G);
     Unit u;
     u.bh = g * G + r % Gg;
     u.q0 = (nqb - 1 - r / Gg) * 2 * kBlk;
     u.nb = (p.N + kBlk - 1) / kBlk;
-    int L = p.N;
-    if (p.kv_len) {
-      L = p.kv_len[u.bh / p.H];
-      L = L < 0 ? 0 : (L > p.N ? p.N : L);
-    }
-    u.L = L;
+    u.L = p.N;
+    return u;
+  };
+  const Unit first_unit = place(blockIdx.x);
+  auto unit = [&](int i, int b) {   // the i-th of this CTA
+    Unit u = first_unit;
+    if (i > 0) u = place(b);
+    if (p.kv_len) u.L = max(0, min(p.kv_len[u.bh / p.H], p.N));
     return u;
   };
 
@@ -176,7 +174,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       bool ok = true;
       int n = 0, nu = 0;   // key blocks, units with any
       for (int i = 0, blk = blockIdx.x; ok && blk >= 0; ++i) {
-        const Unit u = unit(blk);
+        const Unit u = unit(i, blk);
         const int jend = key_blocks(p, u), seq = u.bh / p.H;
         // The next unit is asked for two blocks before this one's end: early enough for the answer,
         // and late enough that no block waits here while another CTA runs dry.
@@ -244,7 +242,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       int nk = 0, nv = 0, nu = 0, np = 0;   // K and V blocks, units with any, P V products
       bool ok = true;
       for (int i = 0, blk = blockIdx.x; ok && blk >= 0; ++i) {
-        const Unit u = unit(blk);
+        const Unit u = unit(i, blk);
         const int jend = key_blocks(p, u);
         int last = -1;
         for (int j = jend - 1; j >= 0 && last < 0; --j)
@@ -335,7 +333,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     bool ok = true;
     int n_s[2] = {0, 0}, n_o[2] = {0, 0}, n_v = 0;   // score tiles, outputs, key blocks so far
     for (int i = 0, blk = blockIdx.x; ok && blk >= 0; ++i) {
-      const Unit u = unit(blk);
+      const Unit u = unit(i, blk);
       const int jend = key_blocks(p, u);
       float m_run[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};  // [tile][A/B]
       float l_part[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -550,9 +548,14 @@ cudaError_t launch_latent_fwd_sm103(const LatentProblem& p, const void* q, const
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   const long long nqb = (p.N + 255) / 256;
+  // Equal groups of heads whose K and V (640 N bytes a head) fit 96 MiB of L2 (all heads at once: 4%
+  // slower at 200 MB; 64 MiB, more groups: 3% at 82 MB, as a group that starts late ends late).
+  const int most = static_cast<int>(
+      std::max(1ll, std::min<long long>(BH, (96ll << 20) / (640ll * p.N))));
+  const int groups = (BH + most - 1) / most, G = (BH + groups - 1) / groups;
   return launch_dependent(latent_fwd_kernel, dim3(static_cast<unsigned>(BH * nqb)),
                           dim3(kThreads), kSmem, s, mq, mkn, mkr, mv, static_cast<__nv_bfloat16*>(o),
-                          o_acc, lse, p);
+                          o_acc, lse, p, G);
 }
 
 }  // namespace fa

@@ -83,6 +83,30 @@ def test_long_sequences(dtype):
     _check(1, 2, 900, dtype, False, [801], seed=4)
 
 
+@pytest.mark.parametrize("causal", [False, True])
+def test_more_units_than_multiprocessors(causal):
+    # CTAs take further units as they finish: 480 of them, empty and one-key sequences among them
+    lens = [300, 0, 257, 1, 128, 300, 129, 0, 255, 256, 2, 300, 0, 0, 127]
+    _check(15, 16, 300, "bf16", causal, lens, seed=8, grad=False)
+    _check(13, 4, 700, "bf16", causal, None, seed=9, grad=False)
+
+
+def test_two_streams_at_once():
+    # each grid hands its units to its own CTAs only
+    x = [_inputs(B, H, N, "bf16", 10 + N) for B, H, N in ((20, 16, 260), (9, 16, 515))]
+    want = [fa.latent_forward(*t[:4], True, need_grad=True) for t in x]
+    _ok()
+    streams = [torch.cuda.Stream() for _ in x]
+    got = [[], []]
+    for _ in range(6):
+        for i, (t, s) in enumerate(zip(x, streams)):
+            got[i].append(fa.latent_forward(*t[:4], True, need_grad=True, stream=s))
+    _ok()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, r))
+
+
 def test_peaked_scores():
     # rows whose weight is almost all on one key: D, dP and dS nearly cancel
     _check(1, 2, 260, "bf16", True, seed=5, mult=6.0)
