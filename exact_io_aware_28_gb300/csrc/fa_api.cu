@@ -292,6 +292,34 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
 
 }  // namespace
 
+namespace {
+
+// A call's memory: where some CTAs read what others write, no output shares memory with an input
+// or with another output.
+struct Span {
+  uintptr_t begin, end;
+  Span(const void* p, long long bytes)
+      : begin(reinterpret_cast<uintptr_t>(p)),
+        end(p ? reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(bytes) : 0) {}
+  bool meets(const Span& o) const { return begin < o.end && o.begin < end; }
+};
+template <size_t I, size_t O>
+bool apart(const Span (&ins)[I], const Span (&outs)[O]) {
+  for (size_t j = 0; j < O; ++j) {
+    for (const Span& in : ins)
+      if (outs[j].meets(in)) return false;
+    for (size_t i = 0; i < j; ++i)
+      if (outs[j].meets(outs[i])) return false;
+  }
+  return true;
+}
+// Bytes of a bf16 pool.
+long long pool_bytes(int num_pages, long long page_stride, long long page_elems) {
+  return 2 * ((num_pages - 1) * page_stride + page_elems);
+}
+
+}  // namespace
+
 extern "C" {
 
 fa_status fa_bwd_main(const void* q, const void* k, const void* v, const float* lse,
@@ -442,11 +470,7 @@ fa_status check_table(const int32_t* table, long long table_stride, int max_page
 
 bool bad_row_stride(long long stride, long long row) { return stride < row || stride % 8 != 0; }
 
-// Do two int32 arrays share memory?
-bool overlap(const int32_t* a, long long na, const int32_t* b, long long nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + 4u * static_cast<uintptr_t>(nb) && y < x + 4u * static_cast<uintptr_t>(na);
-}
+constexpr int kLatentQK = FA_LATENT_NOPE + FA_LATENT_ROPE;
 
 bool bad_softmax_scale(float scale) { return !(isfinite(scale) && scale > 0.f); }
 
@@ -468,17 +492,10 @@ fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
       bad4(pages_taken))
     return FA_ERR_INVALID_ARG;
   if ((n_free > 0 && bad4(free_pages)) || (n_slots > 0 && bad4(slots))) return FA_ERR_INVALID_ARG;
-  // Every block reads the inputs while others write the outputs.
-  const int32_t* ins[3] = {cache_len, new_len, free_pages};
-  const long long n_in[3] = {B, B, n_free};
-  const int32_t* outs[5] = {total_len, token_start, slots, pages_taken, block_table};
-  const long long n_out[5] = {B, B + 1ll, n_slots, 1, (B - 1) * table_stride + max_pages};
-  for (int j = 0; j < 5; ++j) {
-    for (int i = 0; i < 3; ++i)
-      if (overlap(ins[i], n_in[i], outs[j], n_out[j])) return FA_ERR_INVALID_ARG;
-    for (int i = 0; i < j; ++i)
-      if (overlap(outs[i], n_out[i], outs[j], n_out[j])) return FA_ERR_INVALID_ARG;
-  }
+  const Span ins[] = {{cache_len, 4ll * B}, {new_len, 4ll * B}, {free_pages, 4ll * n_free}};
+  const Span outs[] = {{total_len, 4ll * B}, {token_start, 4 * (B + 1ll)}, {slots, 4ll * n_slots},
+                       {pages_taken, 4}, {block_table, 4 * ((B - 1) * table_stride + max_pages)}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
   return to_status(launch_paged_tables(cache_len, new_len, free_pages, n_free, block_table,
                                        table_stride, max_pages, total_len, token_start, slots,
                                        n_slots, pages_taken, B, page_shift(page_size), num_pages,
@@ -554,7 +571,14 @@ fa_status fa_decode_paged(const void* q, const void* k, const void* v, long long
   if (bad_ptr(q) || bad_ptr(k) || bad_ptr(v) || bad_ptr(o) || bad_ptr(workspace) || bad4(lse) ||
       bad4(cache_len) || bad_softmax_scale(scale))
     return FA_ERR_INVALID_ARG;
-  if (workspace_bytes < fa_decode_paged_workspace_bytes(B, Hq, Hkv, d)) return FA_ERR_INVALID_ARG;
+  const size_t need = fa_decode_paged_workspace_bytes(B, Hq, Hkv, d);
+  if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
+  const long long rows = (long long)B * Hq;
+  const long long pool = pool_bytes(num_pages, page_stride, (long long)Hkv * page_size * d);
+  const Span ins[] = {{q, rows * d * 2}, {k, pool}, {v, pool}, {cache_len, 4ll * B},
+                      {block_table, 4 * ((B - 1) * table_stride + max_pages)}};
+  const Span outs[] = {{o, rows * d * 2}, {lse, rows * 4}, {workspace, (long long)need}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
   int* err = error_word();
   if (!err) return FA_ERR_CUDA;
   return to_status(launch_decode_paged(q, k, v, page_stride, block_table, table_stride, max_pages,
@@ -581,7 +605,16 @@ fa_status fa_latent_decode(const void* q, const void* cache, long long page_stri
   if (bad_ptr(q) || bad_ptr(cache) || bad_ptr(o) || bad_ptr(workspace) || bad4(lse) ||
       bad4(cache_len) || bad_softmax_scale(scale))
     return FA_ERR_INVALID_ARG;
-  if (workspace_bytes < fa_latent_decode_workspace_bytes(B, H)) return FA_ERR_INVALID_ARG;
+  const size_t need = fa_latent_decode_workspace_bytes(B, H);
+  if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
+  constexpr int kRow = FA_LATENT_RANK + FA_LATENT_ROPE;
+  const long long rows = (long long)B * H;
+  const Span ins[] = {{q, rows * kRow * 2}, {cache_len, 4ll * B},
+                      {cache, pool_bytes(num_pages, page_stride, (long long)page_size * kRow)},
+                      {block_table, 4 * ((B - 1) * table_stride + max_pages)}};
+  const Span outs[] = {{o, rows * FA_LATENT_RANK * 2}, {lse, rows * 4},
+                       {workspace, (long long)need}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
   int* err = error_word();
   if (!err) return FA_ERR_CUDA;
   return to_status(launch_latent_decode(q, cache, page_stride, block_table, table_stride,
@@ -601,6 +634,14 @@ fa_status fa_latent_fwd(const void* q, const void* k_nope, const void* k_rope, c
   if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
   st = check_masks_scale(kv_len, lse, scale);
   if (st != FA_OK) return st;
+  const long long rows = (long long)B * H * N, esz = dtype == FA_BF16 ? 2 : 4;
+  const bool same = o_acc == o && dtype == FA_FP32;   // allowed: the same values
+  const Span ins[] = {{q, rows * kLatentQK * esz}, {k_nope, rows * FA_LATENT_NOPE * esz},
+                      {k_rope, (long long)B * N * FA_LATENT_ROPE * esz}, {v, rows * FA_LATENT_V * esz},
+                      {kv_len, 4ll * B}};
+  const Span outs[] = {{o, rows * FA_LATENT_V * esz}, {same ? nullptr : o_acc, rows * FA_LATENT_V * 4},
+                       {lse, rows * 4}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
   int* err = error_word();
   if (!err) return FA_ERR_CUDA;
   LatentProblem p{B, H, N, FA_LATENT_V, causal ? 1 : 0, nullptr, kv_len, scale, err,
@@ -633,6 +674,15 @@ fa_status fa_latent_bwd(const void* q, const void* k_nope, const void* k_rope, c
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < fa_latent_bwd_workspace_bytes(B, H, N))
     return FA_ERR_INVALID_ARG;
+  const long long rows = (long long)B * H * N, esz = dtype == FA_BF16 ? 2 : 4;
+  const long long rope = (long long)B * N * FA_LATENT_ROPE * esz;
+  const Span ins[] = {{q, rows * kLatentQK * esz}, {k_nope, rows * FA_LATENT_NOPE * esz},
+                      {k_rope, rope}, {v, rows * FA_LATENT_V * esz}, {o_acc, rows * FA_LATENT_V * 4},
+                      {lse, rows * 4}, {dO, rows * FA_LATENT_V * esz}, {kv_len, 4ll * B}};
+  const Span outs[] = {{dq, rows * kLatentQK * esz}, {dk_nope, rows * FA_LATENT_NOPE * esz},
+                       {dk_rope, rope}, {dv, rows * FA_LATENT_V * esz},
+                       {workspace, (long long)fa_latent_bwd_workspace_bytes(B, H, N)}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
   int* err = error_word();
   if (!err) return FA_ERR_CUDA;
   LatentProblem p{B, H, N, FA_LATENT_V, causal ? 1 : 0, nullptr, kv_len, scale, err,

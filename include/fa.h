@@ -333,6 +333,8 @@ fa_status fa_grad_finish(void* out, const float* acc, long long n, fa_dtype dtyp
  *                 pages may be parts of larger blocks (keys and values side by side, say).
  * Lengths are clamped to [0, max_pages * page_size] on the device.  The pages of different
  * sequences may be the same (a shared prefix) for reading.
+ * In the entry points from here to fa_latent_decode, appends excepted, FA_ERR_INVALID_ARG if an
+ * output (the workspace is one) shares memory with an input or with another output.
  */
 
 /*
@@ -349,8 +351,7 @@ fa_status fa_grad_finish(void* out, const float* acc, long long n, fa_dtype dtyp
  *   slots       out: int32 [n_slots], the slot of every packed new token; -1 for a token in a hole
  *                 and for the rows behind the last token.  May be shorter than the tokens are.
  *   pages_taken out: int32 [1], pages the step needs; more than n_free: the list was too short.
- * Requests take pages in order.  FA_ERR_INVALID_ARG if an output shares memory with an input or
- * another output.  FA_ERR_UNSUPPORTED for B > 8192, n_slots > 2^30 or
+ * Requests take pages in order.  FA_ERR_UNSUPPORTED for B > 8192, n_slots > 2^30 or
  * B * max_pages * page_size >= 2^31.
  */
 fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
@@ -367,6 +368,7 @@ fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
  *   k_cache, v_cache out: bf16 pools [num_pages, Hkv, page_size, d], pages page_stride apart.
  *   slots    in : int32 [T]; a slot outside the pool: the token is skipped.  Slots should differ:
  *                 rows that share one are written in no particular order, piece by piece.
+ * k and v may be rows of the pools themselves (a copy of tokens), if no slot names one of them.
  * d = 64 or 128; T = 0 does nothing.
  */
 fa_status fa_paged_append(const void* k, const void* v, long long k_stride, long long v_stride,

@@ -10,6 +10,7 @@ pytestmark = pytest.mark.skipif(not os.path.exists(fa.LIB_PATH),
                                 reason="libfa_gb300.so not built")
 
 A = 0x100000  # a fake, aligned address: never dereferenced on the host
+X = [A + (i << 40) for i in range(16)]   # more of them, far apart
 INV, UNS = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
 
 
@@ -70,8 +71,8 @@ def test_latent_append_rejects(kw, code):
     assert _call("fa_latent_append", LAPPEND, kw) == code
 
 
-DECODE = dict(q=A, k=A, v=A, ps=8 * 16 * 64, table=A, stride=16, M=16, cl=A, o=A, lse=A, B=2,
-              Hq=16, Hkv=8, P=16, page=16, d=64, scale=0.125, ws=A, wsb=1 << 30)
+DECODE = dict(q=X[0], k=X[1], v=X[2], ps=8 * 16 * 64, table=X[3], stride=16, M=16, cl=X[4], o=X[5],
+              lse=X[6], B=2, Hq=16, Hkv=8, P=16, page=16, d=64, scale=0.125, ws=X[7], wsb=1 << 30)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -83,13 +84,16 @@ DECODE = dict(q=A, k=A, v=A, ps=8 * 16 * 64, table=A, stride=16, M=16, cl=A, o=A
     ({"scale": 0.0}, INV), ({"scale": float("nan")}, INV), ({"scale": -1.0}, INV),
     ({"B": 8192, "Hq": 8, "Hkv": 8}, UNS), ({"M": (1 << 26) + 1, "stride": 1 << 27}, UNS),
     ({"ps": 1 << 39}, UNS),
+    # outputs over inputs or one another
+    ({"o": X[0]}, INV), ({"o": X[1] + 64}, INV), ({"o": X[2] + 16 * 8 * 16 * 64 * 2 - 16}, INV),
+    ({"lse": X[4]}, INV), ({"lse": X[5] + 16}, INV), ({"ws": X[3] + 112}, INV), ({"ws": X[6]}, INV),
 ])
 def test_decode_paged_rejects(kw, code):
     assert _call("fa_decode_paged", DECODE, kw) == code
 
 
-LDECODE = dict(q=A, cache=A, ps=16 * 576, table=A, stride=16, M=16, cl=A, o=A, lse=A, B=2, H=16,
-               P=16, page=16, scale=0.07, ws=A, wsb=1 << 30)
+LDECODE = dict(q=X[0], cache=X[1], ps=16 * 576, table=X[2], stride=16, M=16, cl=X[3], o=X[4],
+               lse=X[5], B=2, H=16, P=16, page=16, scale=0.07, ws=X[6], wsb=1 << 30)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -97,13 +101,17 @@ LDECODE = dict(q=A, cache=A, ps=16 * 576, table=A, stride=16, M=16, cl=A, o=A, l
     ({"cl": A + 3}, INV), ({"table": None}, INV), ({"ws": None}, INV), ({"wsb": 1000}, INV),
     ({"B": 0}, INV), ({"H": 0}, INV), ({"H": 129}, UNS), ({"B": 70000}, UNS),
     ({"page": 1}, UNS), ({"ps": 100}, INV), ({"scale": float("inf")}, INV),
+    # outputs over inputs or one another
+    ({"o": X[0]}, INV), ({"o": X[1] + 16 * 16 * 576 * 2 - 16}, INV), ({"lse": X[3] + 4}, INV),
+    ({"ws": X[0] - 16}, INV), ({"lse": X[4] + 2 * 16 * 512 * 2 - 4}, INV),
+    ({"ws": X[2] + 64}, INV),
 ])
 def test_latent_decode_rejects(kw, code):
     assert _call("fa_latent_decode", LDECODE, kw) == code
 
 
-LFWD = dict(q=A, kn=A, kr=A, v=A, o=A, oa=None, lse=A, B=1, H=2, N=100, causal=1, kv=None,
-            scale=0.07, dtype=fa.FA_BF16)
+LFWD = dict(q=X[0], kn=X[1], kr=X[2], v=X[3], o=X[4], oa=None, lse=X[5], B=1, H=2, N=100, causal=1,
+            kv=None, scale=0.07, dtype=fa.FA_BF16)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -111,13 +119,16 @@ LFWD = dict(q=A, kn=A, kr=A, v=A, o=A, oa=None, lse=A, B=1, H=2, N=100, causal=1
     ({"o": None}, INV), ({"oa": A + 4}, INV), ({"lse": A + 1}, INV), ({"kv": A + 2}, INV),
     ({"N": 0}, INV), ({"B": -1}, INV), ({"dtype": 3}, INV), ({"scale": 0.0}, INV),
     ({"B": 256, "H": 256}, UNS), ({"N": 1 << 25}, UNS),
+    ({"o": X[3]}, INV), ({"o": X[0] + 2 * 100 * 192 * 2 - 16}, INV), ({"oa": X[4]}, INV),
+    ({"lse": X[4] + 32}, INV), ({"oa": X[1]}, INV), ({"kv": X[5]}, INV),
 ])
 def test_latent_fwd_rejects(kw, code):
     assert _call("fa_latent_fwd", LFWD, kw) == code
 
 
-LBWD = dict(q=A, kn=A, kr=A, v=A, oa=A, lse=A, do=A, dq=A, dkn=A, dkr=A, dv=A, B=1, H=2, N=100,
-            causal=1, kv=None, scale=0.07, dtype=fa.FA_BF16, ws=A, wsb=1 << 30)
+LBWD = dict(q=X[0], kn=X[1], kr=X[2], v=X[3], oa=X[4], lse=X[5], do=X[6], dq=X[7], dkn=X[8], dkr=X[9],
+            dv=X[10], B=1, H=2, N=100, causal=1, kv=None, scale=0.07, dtype=fa.FA_BF16, ws=X[11],
+            wsb=1 << 30)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -125,6 +136,8 @@ LBWD = dict(q=A, kn=A, kr=A, v=A, oa=A, lse=A, do=A, dq=A, dkn=A, dkr=A, dv=A, B
     ({"dkr": None}, INV), ({"dv": None}, INV), ({"lse": None}, INV), ({"ws": None}, INV),
     ({"ws": A + 128}, INV), ({"wsb": 100 * 2 * 64 * 4}, INV), ({"N": 0}, INV),
     ({"dtype": 2}, INV), ({"scale": float("nan")}, INV), ({"H": 70000}, UNS),
+    ({"dq": X[0]}, INV), ({"dv": X[6]}, INV), ({"dkn": X[1]}, INV), ({"dkr": X[2] + 16}, INV),
+    ({"dv": X[8]}, INV), ({"ws": X[5]}, INV), ({"ws": X[10]}, INV), ({"dq": X[4]}, INV),
 ])
 def test_latent_bwd_rejects(kw, code):
     assert _call("fa_latent_bwd", LBWD, kw) == code
