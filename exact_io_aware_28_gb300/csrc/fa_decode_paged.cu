@@ -331,8 +331,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
         if (!ok) break;
         tc_fence_after();
         uint32_t sv[16];
-        tmem_ld16(lane_base + st * kN, sv);
-        tmem_wait_ld();
+        tmem_ld16_wait(lane_base + st * kN, sv);
         float x[GP];
 #pragma unroll
         for (int h = 0; h < GP; ++h) x[h] = vis ? __uint_as_float(sv[h]) * a.c : -INFINITY;
@@ -383,8 +382,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
           tc_fence_after();
           uint32_t ov[16];
           const uint32_t oaddr = lane_base + kO + ((nu & 1) * 2 + grp) * kN;
-          tmem_ld16(oaddr, ov);
-          tmem_wait_ld();
+          tmem_ld16_wait(oaddr, ov);
 #pragma unroll
           for (int h = 0; h < GP; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * alpha[h]);
           tmem_st16(oaddr, ov);
@@ -415,9 +413,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
         if (!ok) break;
         tc_fence_after();
         uint32_t o0[16], o1[16];
-        tmem_ld16(lane_base + kO + (nu & 1) * 2 * kN, o0);
-        tmem_ld16(lane_base + kO + ((nu & 1) * 2 + 1) * kN, o1);
-        tmem_wait_ld();
+        tmem_ld16_wait(lane_base + kO + (nu & 1) * 2 * kN, o0);
+        tmem_ld16_wait(lane_base + kO + ((nu & 1) * 2 + 1) * kN, o1);
         tc_fence_before();
         const int slot = sched::slot(sg.pair_start, start.first, blockIdx.x);
         float* out = a.part + static_cast<size_t>(slot) * G * kPStride;
