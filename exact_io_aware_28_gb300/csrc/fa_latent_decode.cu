@@ -355,19 +355,26 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
           ma1 = fmax3(ma1, sv[4 * cc + 4], sv[4 * cc + 5]);
           mb1 = fmax3(mb1, sv[4 * cc + 6], sv[4 * cc + 7]);
         }
-        float tA = fmaxf(ma0, ma1), tB = fmaxf(mb0, mb1);
-        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
-        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 1));
-        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2)) * a.c;
-        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2)) * a.c;
-        const float nA = tA > mA + kRescaleThreshold ? tA : mA;
-        const float nB = tB > mB + kRescaleThreshold ? tB : mB;
-        const bool chA = nA != mA, chB = nB != mB;
-        const float alphaA = chA ? ex2(mA - nA) : 1.f;   // m = -inf gives 0
-        const float alphaB = chB ? ex2(mB - nB) : 1.f;
-        mA = nA;
-        mB = nB;
-        const float useA = nA == -INFINITY ? 0.f : nA, useB = nB == -INFINITY ? 0.f : nB;
+        float tA = fmaxf(ma0, ma1) * a.c, tB = fmaxf(mb0, mb1) * a.c;
+        // As in fa_latent_fwd.cu: rows' maxima only where one passes the running reference.
+        float alphaA = 1.f, alphaB = 1.f;
+        const bool grew = __any_sync(0xffffffffu, tA > mA + kRescaleThreshold ||
+                                                      tB > mB + kRescaleThreshold);
+        if (grew) {
+          tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
+          tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 1));
+          tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2));
+          tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2));
+          if (tA > mA + kRescaleThreshold) {
+            alphaA = ex2(mA - tA);   // m = -inf gives 0
+            mA = tA;
+          }
+          if (tB > mB + kRescaleThreshold) {
+            alphaB = ex2(mB - tB);
+            mB = tB;
+          }
+        }
+        const float useA = mA == -INFINITY ? 0.f : mA, useB = mB == -INFINITY ? 0.f : mB;
         const uint64_t negA = f2_pack(-useA, -useA), negB = f2_pack(-useB, -useB);
         uint64_t accA = f2_pack(0.f, 0.f), accB = accA;
         uint32_t pk[32];
@@ -389,7 +396,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
         lB = lB * alphaB + (sb.x + sb.y);
         // Rescale the running O when a maximum moved after the first tile: its products were
         // issued before these scores, so they have completed.
-        if (k0 > sg.k0 && __any_sync(0xffffffffu, chA || chB)) {
+        if (k0 > sg.k0 && grew) {
 #pragma unroll 1
           for (int i = 0; i < kHalf / 64; ++i) {
             uint32_t o[32];

@@ -375,19 +375,27 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             ma1 = fmax3(ma1, sv[4 * cc + 4], sv[4 * cc + 5]);
             mb1 = fmax3(mb1, sv[4 * cc + 6], sv[4 * cc + 7]);
           }
-          float mA = fmaxf(ma0, ma1), mB = fmaxf(mb0, mb1);
-          mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 1));
-          mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 1));
-          mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 2));
-          mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 2));
-          mA *= c;
-          mB *= c;
+          float mA = fmaxf(ma0, ma1) * c, mB = fmaxf(mb0, mb1) * c;
+          // The rows' maxima are only formed where a thread's own part of one passes the running
+          // reference by 2^8, in the first block and rarely after it.
           const float oldA = m_run[t][0], oldB = m_run[t][1];
-          const float newA = mA > oldA + kRescaleThreshold ? mA : oldA;
-          const float newB = mB > oldB + kRescaleThreshold ? mB : oldB;
-          const bool chA = newA != oldA, chB = newB != oldB;
-          const float alphaA = chA ? ex2(oldA - newA) : 1.f;  // old = -inf gives 0
-          const float alphaB = chB ? ex2(oldB - newB) : 1.f;
+          float newA = oldA, newB = oldB, alphaA = 1.f, alphaB = 1.f;
+          const bool grew = __any_sync(0xffffffffu, mA > oldA + kRescaleThreshold ||
+                                                        mB > oldB + kRescaleThreshold);
+          if (grew) {
+            mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 1));
+            mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 1));
+            mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 2));
+            mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 2));
+            if (mA > oldA + kRescaleThreshold) {
+              newA = mA;
+              alphaA = ex2(oldA - newA);   // old = -inf gives 0
+            }
+            if (mB > oldB + kRescaleThreshold) {
+              newB = mB;
+              alphaB = ex2(oldB - newB);
+            }
+          }
           const float useA = newA == -INFINITY ? 0.f : newA;
           const float useB = newB == -INFINITY ? 0.f : newB;
           const uint64_t nA = f2_pack(-useA, -useA), nB = f2_pack(-useB, -useB);
@@ -413,7 +421,7 @@ latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
           m_run[t][0] = newA;
           m_run[t][1] = newB;
           // Rescale the running O (the P V products issued before the S just read are done).
-          if (any[t] && __any_sync(0xffffffffu, chA || chB)) {
+          if (any[t] && grew) {
 #pragma unroll
             for (int half = 0; half < kVSubs; ++half) {
               uint32_t o[32];
