@@ -32,7 +32,7 @@
 // for the 80 KB: a wait and a commit between four MMAs cost as much as the four.
 //   warp 0     producer: Q, then the tiles page by page;  warp 1  MMA issuer (one thread);
 //   warp 2     tensor memory;                             warps 4-11 softmax, a row in 4 threads.
-// Measured: 32 sequences of 4096 to 8192 tokens, 128 heads: 79 us for 35 us of bytes (L2 serves the
+// Measured: 32 sequences of 4096 to 8192 tokens, 128 heads: 78 us for 35 us of bytes (L2 serves the
 // other CTA of the pair).  A tile takes 5k cycles, of which the pipe runs 3.4k: the rest's scores
 // 1445, the own half's 950, the softmax 1070 between them and P V; joining the parts adds 8 us.
 // Work is shared out as fa_paged_sched.cuh says, over pairs of CTAs.  Every wait is bounded; on

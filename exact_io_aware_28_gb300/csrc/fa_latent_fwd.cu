@@ -10,7 +10,7 @@
 // What bounds it: 640 operations a (query, key) pair against 832 bytes a key and 128 queries,
 // so the tensor cores, and beside them the softmax.  As in fa_fwd_sm103.cu a CTA owns two tiles
 // of 128 query rows, one MMA-issuing thread each, and all eight softmax warps take the tiles in
-// turn: 555 us for 16 heads x 8192 without a mask (1.24 PFLOP/s), 4.2k cycles a pair of tiles
+// turn: 540 us for 16 heads x 8192 without a mask (1.27 PFLOP/s), 4.1k cycles a pair of tiles
 // and block of which 2.8k are MMAs.  Softmax warps of a tile's own measured slower, both four (a
 // row per thread, 678 us) and eight (scores read twice, 627 us), and a P V product in two halves of
 // the keys, the first while the second half of P is formed, gains nothing (566 us).
