@@ -58,6 +58,7 @@ struct Bars {
   uint64_t s_read;             // the softmax warps have the scores in registers
   uint64_t dp_full;
   uint64_t p_ready;
+  uint64_t ds_half;            // of each 64 columns the first 32
   uint64_t ds_ready;
   uint64_t ds_taken;           // the product with dS's first term has completed
   uint64_t do_ready;           // dQ: the owned dO is in tensor memory
@@ -151,6 +152,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
     mbar_init(&bars->s_read, 256);
     mbar_init(&bars->dp_full, 1);
     mbar_init(&bars->p_ready, 256);
+    mbar_init(&bars->ds_half, 256);
     mbar_init(&bars->ds_ready, 256);
     mbar_init(&bars->ds_taken, 1);
     mbar_init(&bars->do_ready, 256);
@@ -297,14 +299,27 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
         tc_fence_after();
         return true;
       };
-      // dQ += dS K, dK += dS^T Q, in one term or (the first block) in two.
+      // dQ += dS K, dK += dS^T Q, in one term or (the first block) in two; begun on the first half of
+      // dS while the softmax warps form the second (16 heads x 8192: 1199 -> 1188 us).
       int nd = 0;
       auto dS_product = [&](int st, int n) -> bool {
         bool more = fine && n == 0;
 #pragma unroll 1
         for (bool acc = n > 0;; acc = true) {
-          if (!wait(&bars->ds_ready, nd++)) return false;
-          grads(tb + kAccX, tb + kDS, kDSHalf, dXm + ((st * kX) >> 4), idX, acc);
+          const uint32_t b0 = dXm + ((st * kX) >> 4);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (!wait(q ? &bars->ds_ready : &bars->ds_half, nd)) return false;
+            uint32_t ta[4], db[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {   // 16 rows of the streamed block: half k / 2
+              const int step = 4 * (k >> 1) + 2 * q + (k & 1);
+              ta[k] = tb + kDS + kDSHalf * (k >> 1) + 8 * (2 * q + (k & 1));
+              db[k] = b0 + ((2048 * step) >> 4);
+            }
+            mma_ts_x4_lo(tb + kAccX, ta, db, hi, idX, (acc || q > 0) ? 1u : 0u);
+          }
+          ++nd;
           if (!more) return true;
           more = false;
           mma_commit(&bars->ds_taken);
@@ -455,6 +470,20 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
       ok = mbar_wait_warp(&bars->dp_full, n & 1, abort_flag, p.err, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
+      if (tail) {
+        // Keys past the length: zero their rows before dS K reads them, so that 0 x (anything)
+        // stays 0 (the scores of this block have been formed).
+        const int key = (tid - 128) >> 1;
+        if (begin + n * kRows + key >= L) {
+          uint8_t* kr = sX + st * kX + key * 128 + 64 * (tid & 1);
+#pragma unroll
+          for (int s = 0; s < kXSubs; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<uint4*>(kr + s * kSub)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t dv[32], pk[16];
@@ -478,24 +507,10 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
           pk[i] = pack_bf16x2(P[32 * q + 2 * i], P[32 * q + 2 * i + 1]);
         // In place: columns of this thread's own that it has read.
         tmem_st16(lane_base + kDS + kDSHalf * half + 16 * q, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(q ? &bars->ds_ready : &bars->ds_half);
       }
-      if (tail) {
-        // Keys past the length: zero their rows before dS K reads them, so that 0 x (anything)
-        // stays 0 (the scores of this block have been formed).
-        const int key = (tid - 128) >> 1;
-        if (begin + n * kRows + key >= L) {
-          uint8_t* kr = sX + st * kX + key * 128 + 64 * (tid & 1);
-#pragma unroll
-          for (int s = 0; s < kXSubs; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<uint4*>(kr + s * kSub)[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars->ds_ready);
       if (fine && n == 0) {   // what the rounding left
         ok = mbar_wait_warp(&bars->ds_taken, 0, abort_flag, p.err, p.wait_ns);
         if (!ok) break;
@@ -510,10 +525,10 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
                                 y - __bfloat162float(__float2bfloat16_rn(y)));
           }
           tmem_st16(lane_base + kDS + kDSHalf * half + 16 * q, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(q ? &bars->ds_ready : &bars->ds_half);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->ds_ready);
       }
     }
     // ------------------------------------------------------------ epilogue
