@@ -78,7 +78,7 @@ struct Bars {
   uint64_t q_own;       // Q's own half is in tensor memory
   uint64_t q_empty;     // every score product of the segment has completed
   uint64_t s_full;
-  uint64_t p_full;
+  uint64_t p_full[2];   // of each half of the tile's keys
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t seen[2];  // bit i: rows 16 i ... 16 i + 15 of the tile are in the pool
@@ -124,7 +124,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
     mbar_init(&bars->q_own, 256);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->s_full, 1);
-    mbar_init(&bars->p_full, 256);
+    mbar_init(&bars->p_full[0], 256);
+    mbar_init(&bars->p_full[1], 256);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     bars->never = 0;
@@ -249,11 +250,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
           }
           mma_commit(&bars->s_full);
           if (k0 + kKeys >= sg.k1) mma_commit(&bars->q_empty);
-          ok = mbar_wait(&bars->p_full, n & 1, abort_flag, a.err, a.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
+            ok = ok && mbar_wait(&bars->p_full[g], n & 1, abort_flag, a.err, a.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
             uint32_t ta[4];
             uint64_t db[4];
 #pragma unroll
@@ -263,6 +264,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
             }
             mma_ts_x4(tb, ta, db, idO, (k0 > sg.k0 || g > 0) ? 1u : 0u);
           }
+          if (!ok) break;
           mma_commit(&bars->own_empty);
         }
         ++nu;
@@ -376,24 +378,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
         }
         const float useA = mA == -INFINITY ? 0.f : mA, useB = mB == -INFINITY ? 0.f : mB;
         const uint64_t negA = f2_pack(-useA, -useA), negB = f2_pack(-useB, -useB);
-        uint64_t accA = f2_pack(0.f, 0.f), accB = accA;
-        uint32_t pk[32];
-#pragma unroll
-        for (int cc = 0; cc < 16; ++cc) {
-          const float2 xa = f2_unpack(ffma2(f2_pack(sv[4 * cc], sv[4 * cc + 1]), c2, negA));
-          const float2 xb = f2_unpack(ffma2(f2_pack(sv[4 * cc + 2], sv[4 * cc + 3]), c2, negB));
-          const float pa0 = ex2(xa.x), pa1 = ex2(xa.y);
-          const float pb0 = ex2(xb.x), pb1 = ex2(xb.y);
-          accA = fadd2(accA, f2_pack(pa0, pa1));
-          accB = fadd2(accB, f2_pack(pb0, pb1));
-          pk[2 * cc] = pack_bf16x2(pa0, pa1);
-          pk[2 * cc + 1] = pack_bf16x2(pb0, pb1);
-        }
-        // P over the first 64 columns of S in this warp's 16 lanes, which no other warp reads.
-        tmem_st_16x128b_x16(lane_base + kTS, pk);
-        const float2 sa = f2_unpack(accA), sb = f2_unpack(accB);
-        lA = lA * alphaA + (sa.x + sa.y);
-        lB = lB * alphaB + (sb.x + sb.y);
         // Rescale the running O when a maximum moved after the first tile: its products were
         // issued before these scores, so they have completed.
         if (k0 > sg.k0 && grew) {
@@ -407,9 +391,32 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mc, const __grid_consta
             tmem_st_16x256b_x8(lane_base + 64 * i, o);
           }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->p_full);
+        // P over the first 64 columns of S in this warp's 16 lanes, which no other warp reads; the
+        // product starts on each half of the keys as it comes.
+        uint64_t accA = f2_pack(0.f, 0.f), accB = accA;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* x = sv + 4 * (8 * g + i);
+            const float2 xa = f2_unpack(ffma2(f2_pack(x[0], x[1]), c2, negA));
+            const float2 xb = f2_unpack(ffma2(f2_pack(x[2], x[3]), c2, negB));
+            const float pa0 = ex2(xa.x), pa1 = ex2(xa.y);
+            const float pb0 = ex2(xb.x), pb1 = ex2(xb.y);
+            accA = fadd2(accA, f2_pack(pa0, pa1));
+            accB = fadd2(accB, f2_pack(pb0, pb1));
+            pk[2 * i] = pack_bf16x2(pa0, pa1);
+            pk[2 * i + 1] = pack_bf16x2(pb0, pb1);
+          }
+          tmem_st_16x128b_x8(lane_base + kTS + 32 * g, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[g]);
+        }
+        const float2 sa = f2_unpack(accA), sb = f2_unpack(accB);
+        lA = lA * alphaA + (sa.x + sa.y);
+        lB = lB * alphaB + (sb.x + sb.y);
       }
       if (!ok) break;
       // The next segment's queries first: the issuer's next scores wait for them.
