@@ -57,6 +57,7 @@ struct Bars {
   uint64_t s_full;
   uint64_t s_read;             // the softmax warps have the scores in registers
   uint64_t dp_full;
+  uint64_t p_half;             // of each 64 columns the first 32
   uint64_t p_ready;
   uint64_t ds_half;            // of each 64 columns the first 32
   uint64_t ds_ready;
@@ -151,6 +152,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
     mbar_init(&bars->s_full, 1);
     mbar_init(&bars->s_read, 256);
     mbar_init(&bars->dp_full, 1);
+    mbar_init(&bars->p_half, 256);
     mbar_init(&bars->p_ready, 256);
     mbar_init(&bars->ds_half, 256);
     mbar_init(&bars->ds_ready, 256);
@@ -250,19 +252,17 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
           mma_ss_x4_lo(d, da, hi, db, hi, idS, g > 0 ? 1u : 0u);
         }
       };
-      // Gradient product: A from the bf16 pairs at `t` (64 rows of the block each `half` columns),
-      // B the stage's subtiles along the rows.
-      auto grads = [&](uint32_t d, uint32_t t, uint32_t half, uint32_t b0, uint32_t id, bool acc) {
+      // Half of a gradient product: A from the bf16 pairs at `t` (64 rows of the block each `half`
+      // columns), of each 64 rows the first or the last 32, B the stage's subtiles along the rows.
+      auto halves = [&](uint32_t d, uint32_t t, uint32_t half, uint32_t b0, uint32_t id, int q,
+                        bool acc) {
+        uint32_t ta[4], db[4];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t ta[4], db[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ta[k] = t + g * half + 8 * k;
-            db[k] = b0 + ((2048 * (4 * g + k)) >> 4);
-          }
-          mma_ts_x4_lo(d, ta, db, hi, id, (acc || g > 0) ? 1u : 0u);
+        for (int k = 0; k < 4; ++k) {
+          ta[k] = t + (k >> 1) * half + 8 * (2 * q + (k & 1));
+          db[k] = b0 + ((2048 * (4 * (k >> 1) + 2 * q + (k & 1))) >> 4);
         }
+        mma_ts_x4_lo(d, ta, db, hi, id, acc ? 1u : 0u);
       };
       auto start_s = [&](int n) -> bool {
         const int st = n % kXStages;
@@ -300,7 +300,8 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
         return true;
       };
       // dQ += dS K, dK += dS^T Q, in one term or (the first block) in two; begun on the first half of
-      // dS while the softmax warps form the second (16 heads x 8192: 1199 -> 1188 us).
+      // dS while the softmax warps form the second, as dV += P^T dO is (16 heads x 8192: 1199 -> 1169
+      // us, 2 x 8 x 1000: 62.5 -> 63.5).
       int nd = 0;
       auto dS_product = [&](int st, int n) -> bool {
         bool more = fine && n == 0;
@@ -310,14 +311,7 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             if (!wait(q ? &bars->ds_ready : &bars->ds_half, nd)) return false;
-            uint32_t ta[4], db[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {   // 16 rows of the streamed block: half k / 2
-              const int step = 4 * (k >> 1) + 2 * q + (k & 1);
-              ta[k] = tb + kDS + kDSHalf * (k >> 1) + 8 * (2 * q + (k & 1));
-              db[k] = b0 + ((2048 * step) >> 4);
-            }
-            mma_ts_x4_lo(tb + kAccX, ta, db, hi, idX, (acc || q > 0) ? 1u : 0u);
+            halves(tb + kAccX, tb + kDS, kDSHalf, b0, idX, q, acc || q > 0);
           }
           ++nd;
           if (!more) return true;
@@ -346,9 +340,15 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
         ok = ok && mbar_wait(&bars->fixed_full, 0, abort_flag, p.err, p.wait_ns) && start_s(0);
         for (int n = 0; ok && n < blocks; ++n) {
           const int st = n % kXStages;
-          ok = wait(&bars->s_read, n) && start_dp(n) && wait(&bars->p_ready, n);
+          ok = wait(&bars->s_read, n) && start_dp(n);
           if (!ok) break;
-          grads(tb, tb + kP, 32, dYm, idV, n > 0);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            ok = ok && wait(q ? &bars->p_ready : &bars->p_half, n);
+            if (!ok) break;
+            halves(tb, tb + kP, 32, dYm, idV, q, n > 0 || q > 0);
+          }
+          if (!ok) break;
           mma_commit(&bars->y_empty);
           ok = dS_product(st, n);
           if (!ok) break;
@@ -445,27 +445,30 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
       const bool edge = lo > 0 || hi < 64;
       float P[64];
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        float4 l2 = make_float4(row_l2, row_l2, row_l2, row_l2);
-        if (!DQ) l2 = *reinterpret_cast<const float4*>(&stats[st].lse2[64 * half + i]);
-        P[i] = ex2(fmaf(__uint_as_float(sv[i]), c, -l2.x));
-        P[i + 1] = ex2(fmaf(__uint_as_float(sv[i + 1]), c, -l2.y));
-        P[i + 2] = ex2(fmaf(__uint_as_float(sv[i + 2]), c, -l2.z));
-        P[i + 3] = ex2(fmaf(__uint_as_float(sv[i + 3]), c, -l2.w));
-      }
-      if (edge) {
+      for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (i < lo || i >= hi) P[i] = 0.f;
-      }
-      if (!DQ) {
-        uint32_t pk[32];
+        for (int i = 32 * q; i < 32 * q + 32; i += 4) {
+          float4 l2 = make_float4(row_l2, row_l2, row_l2, row_l2);
+          if (!DQ) l2 = *reinterpret_cast<const float4*>(&stats[st].lse2[64 * half + i]);
+          P[i] = ex2(fmaf(__uint_as_float(sv[i]), c, -l2.x));
+          P[i + 1] = ex2(fmaf(__uint_as_float(sv[i + 1]), c, -l2.y));
+          P[i + 2] = ex2(fmaf(__uint_as_float(sv[i + 2]), c, -l2.z));
+          P[i + 3] = ex2(fmaf(__uint_as_float(sv[i + 3]), c, -l2.w));
+        }
+        if (edge) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(P[2 * i], P[2 * i + 1]);
-        tmem_st32(lane_base + kP + 32 * half, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->p_ready);
+          for (int i = 32 * q; i < 32 * q + 32; ++i)
+            if (i < lo || i >= hi) P[i] = 0.f;
+        }
+        if (!DQ) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(P[32 * q + 2 * i], P[32 * q + 2 * i + 1]);
+          tmem_st16(lane_base + kP + 32 * half + 16 * q, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(q ? &bars->p_ready : &bars->p_half);
+        }
       }
       ok = mbar_wait_warp(&bars->dp_full, n & 1, abort_flag, p.err, p.wait_ns);
       if (!ok) break;
