@@ -399,19 +399,24 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
       row_D = a.D[static_cast<size_t>(bh) * p.N + row];
     }
     if (DQ && blocks > 0) {
-      // The owned dO, this thread's 64 columns of its row, as the A operand of dP.
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.dO + (static_cast<size_t>(bh) * p.N + (row < p.N ? row : 0)) * kV + 64 * half);
+      // The owned dO as the A operand of dP: 16 rows a warp, four threads to 32 bytes of a row.
+      const int rA = row0 + 32 * w4 + 16 * half + (lane >> 2), rB = rA + 8;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(a.dO) +
+                            static_cast<size_t>(bh) * p.N * (kV / 2) + 2 * (lane & 3);
       uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 x = row < p.N ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        w[4 * i] = x.x;
-        w[4 * i + 1] = x.y;
-        w[4 * i + 2] = x.z;
-        w[4 * i + 3] = x.w;
+      for (int cc = 0; cc < 8; ++cc) {
+        uint2 x = make_uint2(0u, 0u), y = x;
+        if (rA < p.N)
+          x = *reinterpret_cast<const uint2*>(src + static_cast<size_t>(rA) * (kV / 2) + 8 * cc);
+        if (rB < p.N)
+          y = *reinterpret_cast<const uint2*>(src + static_cast<size_t>(rB) * (kV / 2) + 8 * cc);
+        w[4 * cc] = x.x;
+        w[4 * cc + 1] = x.y;
+        w[4 * cc + 2] = y.x;
+        w[4 * cc + 3] = y.y;
       }
-      tmem_st32(lane_base + kDO + 32 * half, w);
+      tmem_st_16x256b_x8(lane_base + (static_cast<uint32_t>(16 * half) << 16) + kDO, w);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars->do_ready);
