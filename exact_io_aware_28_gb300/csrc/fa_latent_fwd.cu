@@ -72,22 +72,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-// Four threads hold words 0..3 of a chunk each, thread i of the quad its i-th pair of columns:
-// thread i gets chunk i whole.
-__device__ __forceinline__ uint4 quad_transpose(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3,
-                                                int i) {
-  const bool odd = i & 1, high = i & 2;
-  // Against the neighbour: (w0, w1) and (w2, w3), the even thread keeps the first of each.
-  uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 1);
-  uint32_t b = __shfl_xor_sync(0xffffffffu, odd ? w2 : w3, 1);
-  const uint32_t x0 = odd ? a : w0, x1 = odd ? w1 : a;   // chunk (i & 1): columns 0-3 of the pair
-  const uint32_t y0 = odd ? b : w2, y1 = odd ? w3 : b;   // chunk 2 + (i & 1)
-  // Against the thread two on.
-  a = __shfl_xor_sync(0xffffffffu, high ? x0 : y0, 2);
-  b = __shfl_xor_sync(0xffffffffu, high ? x1 : y1, 2);
-  return high ? make_uint4(a, b, y0, y1) : make_uint4(x0, x1, a, b);
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
 latent_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkn,
                   const __grid_constant__ CUtensorMap mkr, const __grid_constant__ CUtensorMap mv,
