@@ -614,8 +614,8 @@ def _table(t, B):
 
 
 def _on_stream(stream, fn, *args, **kw):
-    """An allocating helper on a stream that was named: its outputs and scratch memory belong to
-    that stream, and inputs made on another are kept until its work is done."""
+    """A helper on a stream that was named: what it allocates belongs to that stream, and tensors made
+    on another are kept until its work is done."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     if stream != torch.cuda.current_stream():
@@ -692,7 +692,12 @@ def fa_paged_append(k, v, k_cache, v_cache, slots, stream=None) -> None:
         raise FaError(st, "fa_paged_append")
 
 
-paged_append = fa_paged_append   # it allocates nothing
+def paged_append(k, v, k_cache, v_cache, slots, stream=None) -> None:
+    """fa_paged_append; on a ``stream`` that is named, the tensors' memory is kept until its work is
+    done."""
+    if stream is not None:
+        return _on_stream(stream, paged_append, k, v, k_cache, v_cache, slots)
+    fa_paged_append(k, v, k_cache, v_cache, slots)
 
 
 def fa_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
@@ -874,7 +879,12 @@ def fa_latent_append(c, k_rope, cache, slots, stream=None) -> None:
         raise FaError(st, "fa_latent_append")
 
 
-latent_append = fa_latent_append   # it allocates nothing
+def latent_append(c, k_rope, cache, slots, stream=None) -> None:
+    """fa_latent_append; on a ``stream`` that is named, the tensors' memory is kept until its work is
+    done."""
+    if stream is not None:
+        return _on_stream(stream, latent_append, c, k_rope, cache, slots)
+    fa_latent_append(c, k_rope, cache, slots)
 
 
 def fa_latent_decode_workspace_bytes(B: int, H: int) -> int:

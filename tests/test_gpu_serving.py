@@ -243,3 +243,42 @@ def test_gradients_against_differences():
         along = (grads[i].double() * t.double())
         assert abs((f[1] - f[0]) / (2 * e) - along.sum().item()) <= 0.01 * along.abs().sum().item()
     _ok()
+
+
+@pytest.mark.parametrize("latent_rows", [False, True])
+def test_appends_on_a_named_stream_keep_their_inputs(latent_rows):
+    # The named stream is held up, so the rows are read after the caller has dropped them and filled
+    # new tensors of their sizes.
+    T, Hkv, d, page, P = 300, 4, 64, 32, 12
+    g = _gen(10)
+    if latent_rows:
+        rows, pools = [(T, 512), (T, 64)], [torch.zeros(P, page, 576, dtype=BF, device="cuda")]
+    else:
+        rows = [(T, Hkv, d)] * 2
+        pools = [torch.zeros(P, Hkv, page, d, dtype=BF, device="cuda") for _ in rows]
+    append = fa.latent_append if latent_rows else fa.paged_append
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        host = [torch.randn(*s, generator=g).bfloat16() for s in rows]
+        slots = torch.randperm(P * page, generator=g)[:T].int()
+        before = [_np(p) for p in pools]
+        x = [r.cuda() for r in host]
+        at = slots.cuda()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        append(*x, *pools, at, stream=side)
+        del x, at
+        junk = [torch.full(s, 7.0, dtype=BF, device="cuda") for s in rows]
+        junk.append(torch.full((T,), -1, dtype=I32, device="cuda"))
+        torch.cuda.current_stream().wait_stream(side)
+        _ok()
+        if latent_rows:
+            host = [torch.cat(host, 1)]
+        for p, b, r in zip(pools, before, host):
+            assert np.array_equal(_np(p), paged.append(b, _np(r), slots.tolist()))
+        # a handle will do, and no stream is the current one
+        append(*(r.cuda() for r in (host if not latent_rows else host[0].split((512, 64), 1))),
+               *pools, slots.cuda(), stream=side.cuda_stream)
+        side.synchronize()
+        _ok()
