@@ -179,19 +179,22 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
     L = p.kv_len[seq];
     L = L < 0 ? 0 : (L > p.N ? p.N : L);
   }
-  // A rounding of dS averages out over long sums.  The first queries of a causal sequence see few
-  // keys and have the largest dS (a row over n keys some 1 / n of it), so dq of 4 x 2 heads of two
-  // rows was off by 0.0035 of its norm and by 0.0024 at 300 rows, where one rounding of the result
-  // makes 0.0017.  The first query block's dS therefore goes into its product as two bf16 terms, the
-  // second in the first's place when its product is done: the same instructions once more, since
-  // further MMAs in the issuers' loops slow every block.  A training step of 16 heads x 8192 takes
-  // 1207 us with it and 1186 without, 2 x 8 heads x 1000 62.5 and 61.5; the MMAs side by side
-  // 1213 to 1285, a template for the blocks that need it 1200 but 67 (code read for the first time).
-  const bool fine = row0 == 0 && (p.causal || p.N <= kRows);
   // The streamed rows [begin, end) in blocks of 128.
   const int begin = !DQ && p.causal ? row0 : 0;
   const int end = DQ ? (p.causal ? min(L, row0 + kRows) : L) : (row0 < L ? p.N : begin);
   const int blocks = end > begin ? (end - begin + kRows - 1) / kRows : 0;
+  // One rounding of dS leaves dq 0.0024 of its norm off at any length, where the result's own leaves
+  // 0.0017.  But the fewer keys a query sees, the fewer roundings its row of dq holds and the farther
+  // off a single row can be: 0.0045 of it over 2 keys, 0.0035 over 300 (the result's rounding alone:
+  // 0.0021; the largest of 2400 rows, D taken as given).  An accuracy choice for such rows: queries
+  // that see at most 128 keys, whose row of dS is one block, have it in the products as two bf16
+  // terms, the second in the first's place when its product is done: the same instructions once
+  // more, since further MMAs in the issuers' loops slow every block (side by side, 6% and more).
+  // `fine`: the CTA's first blocks that hold such queries.  A training step of 16 heads x 8192,
+  // causal, takes 1137 us with it and 1113 without, 4 x 64 heads x 100 61.5 and 57.3, 2 x 8 x 1000
+  // 56.4 both; 4 x 8 x 1000 with 2 visible keys each 62 and 55.
+  const int fine = DQ ? (end <= kRows ? blocks : 0)
+                      : row0 > 0 ? 0 : L <= kRows ? blocks : p.causal ? 1 : 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -299,12 +302,12 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
         tc_fence_after();
         return true;
       };
-      // dQ += dS K, dK += dS^T Q, in one term or (the first block) in two; begun on the first half of
-      // dS while the softmax warps form the second, as dV += P^T dO is (16 heads x 8192: 1199 -> 1169
-      // us, 2 x 8 x 1000: 62.5 -> 63.5).
+      // dQ += dS K, dK += dS^T Q, in one term or (the first `fine` blocks) in two; begun on the first
+      // half of dS while the softmax warps form the second, as dV += P^T dO is (16 heads x 8192: 1199
+      // -> 1169 us, 2 x 8 x 1000: 62.5 -> 63.5).
       int nd = 0;
       auto dS_product = [&](int st, int n) -> bool {
-        bool more = fine && n == 0;
+        bool more = n < fine;
 #pragma unroll 1
         for (bool acc = n > 0;; acc = true) {
           const uint32_t b0 = dXm + ((st * kX) >> 4);
@@ -519,8 +522,8 @@ __device__ __forceinline__ void bwd_cta(const CUtensorMap& mq, const CUtensorMap
         tc_fence_before();
         mbar_arrive(q ? &bars->ds_ready : &bars->ds_half);
       }
-      if (fine && n == 0) {   // what the rounding left
-        ok = mbar_wait_warp(&bars->ds_taken, 0, abort_flag, p.err, p.wait_ns);
+      if (n < fine) {   // what the rounding left
+        ok = mbar_wait_warp(&bars->ds_taken, n & 1, abort_flag, p.err, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll

@@ -431,7 +431,9 @@ fa_status fa_latent_fwd(const void* q, const void* k_nope, const void* k_rope, c
  * the heads' gradients of the shared part.  o_acc and lse as fa_latent_fwd wrote them (same masks,
  * same scale).  workspace: at least fa_latent_bwd_workspace_bytes(B, H, N) bytes, 256-byte
  * aligned: the fp32 row sums of dO o O, then the heads' fp32 shares of dk_rope.  Gradients of keys
- * past kv_len[b] are 0.  No atomics: the same call gives the same bits.
+ * past kv_len[b] are 0.  No atomics: the same call gives the same bits.  bf16 tensors: P and dS are
+ * rounded to bf16 as operands; dS of queries that see at most 128 keys (by the causal mask or
+ * kv_len) is held to twice the bits, as two bf16 terms.
  */
 size_t fa_latent_bwd_workspace_bytes(int B, int H, int N);
 fa_status fa_latent_bwd(const void* q, const void* k_nope, const void* k_rope, const void* v,
