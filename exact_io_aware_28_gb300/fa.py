@@ -579,6 +579,12 @@ def _shaped(name, t, shape, dtype):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _scratch(t):
+    """The workspace's bytes are all its own (an expanded tensor counts some that it does not have)."""
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _rows(name, t, shape, dtype=torch.bfloat16):
     """Elements between the first index's entries of ``t``, whose other dimensions are dense (a
     slice of a larger tensor along them is taken as it is)."""
@@ -729,6 +735,7 @@ def fa_decode_paged(q, k, v, block_table, cache_len, o, lse, workspace, scale=No
     _shaped("cache_len", cache_len, (B,), torch.int32)
     _shaped("o", o, heads, torch.bfloat16)
     _shaped("lse", lse, (B, Hq), torch.float32)
+    _scratch(workspace)
     handle = _same_gpu(stream, q, k, v, block_table, cache_len, o, lse, workspace)
     st = load().fa_decode_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), kp,
                                 block_table.data_ptr(), stride, block_table.shape[1],
@@ -832,6 +839,7 @@ def fa_latent_bwd(q, k_nope, k_rope, v, o_acc, lse, do, dq, dk_nope, dk_rope, dv
     for name, t, like in (("do", do, v), ("dq", dq, q), ("dk_nope", dk_nope, k_nope),
                           ("dk_rope", dk_rope, k_rope), ("dv", dv, v)):
         _shaped(name, t, like.shape, q.dtype)
+    _scratch(workspace)
     handle = _same_gpu(stream, *_given(q, k_nope, k_rope, v, o_acc, lse, do, dq, dk_nope, dk_rope,
                                        dv, workspace, kv_len))
     st = load().fa_latent_bwd(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
@@ -911,6 +919,7 @@ def fa_latent_decode(q, cache, block_table, cache_len, o, lse, workspace, scale=
     _shaped("cache_len", cache_len, (B,), torch.int32)
     _shaped("o", o, (B, H, LATENT_RANK), torch.bfloat16)
     _shaped("lse", lse, (B, H), torch.float32)
+    _scratch(workspace)
     handle = _same_gpu(stream, q, cache, block_table, cache_len, o, lse, workspace)
     st = load().fa_latent_decode(q.data_ptr(), cache.data_ptr(), ps, block_table.data_ptr(), stride,
                                  block_table.shape[1], cache_len.data_ptr(), o.data_ptr(),

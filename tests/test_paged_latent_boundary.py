@@ -212,3 +212,19 @@ def test_binding_refuses_host_tensors_and_wrong_latents():
     with pytest.raises(ValueError):
         fa.fa_latent_decode(_z(2, 4, 512), cache, _z(2, 3, dtype=I32), _z(2, dtype=I32),
                             _z(2, 4, 512), _z(2, 4, dtype=torch.float32), _z(8))
+
+
+def test_binding_refuses_workspaces_that_repeat_their_bytes():
+    # an expanded tensor counts bytes that it does not have
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 24)
+    table, lens = _z(2, 3, dtype=I32), _z(2, dtype=I32)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        fa.fa_decode_paged(_z(2, 4, 64), _z(5, 2, 16, 64), _z(5, 2, 16, 64), table, lens,
+                           _z(2, 4, 64), _z(2, 4, dtype=torch.float32), ws)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        fa.fa_latent_decode(_z(2, 4, 576), _z(4, 16, 576), table, lens, _z(2, 4, 512),
+                            _z(2, 4, dtype=torch.float32), ws)
+    x = _z(1, 2, 8, 192), _z(1, 2, 8, 128), _z(1, 8, 64), _z(1, 2, 8, 128)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        fa.fa_latent_bwd(*x, _z(1, 2, 8, 128, dtype=torch.float32),
+                         _z(1, 2, 8, dtype=torch.float32), x[3], *x, ws)
