@@ -468,6 +468,17 @@ fa_status check_table(const int32_t* table, long long table_stride, int max_page
   return FA_OK;
 }
 
+// Two pools of pages of E elements, S apart, have no element in common: pages i and j lie
+// delta + (j - i) S apart, and the two distances nearest to 0 are delta mod S and that less S.
+bool pools_apart(const void* a, const void* b, long long S, long long E, int num_pages) {
+  S *= 2, E *= 2;   // bytes
+  const long long delta = static_cast<long long>(reinterpret_cast<intptr_t>(b) -
+                                                 reinterpret_cast<intptr_t>(a));
+  const long long r = ((delta % S) + S) % S, i = (delta - r) / S;
+  return !(r < E && i > -num_pages && i < num_pages) &&
+         !(S - r < E && i + 1 > -num_pages && i + 1 < num_pages);
+}
+
 bool bad_row_stride(long long stride, long long row) { return stride < row || stride % 8 != 0; }
 
 constexpr int kLatentQK = FA_LATENT_NOPE + FA_LATENT_ROPE;
@@ -514,6 +525,8 @@ fa_status fa_paged_append(const void* k, const void* v, long long k_stride, long
   if (bad_ptr(k) || bad_ptr(v) || bad_ptr(k_cache) || bad_ptr(v_cache) || bad4(slots))
     return FA_ERR_INVALID_ARG;
   if (bad_row_stride(k_stride, (long long)Hkv * d) || bad_row_stride(v_stride, (long long)Hkv * d))
+    return FA_ERR_INVALID_ARG;
+  if (!pools_apart(k_cache, v_cache, page_stride, (long long)Hkv * page_size * d, num_pages))
     return FA_ERR_INVALID_ARG;
   return to_status(launch_paged_append(k, v, k_stride, v_stride, k_cache, v_cache, page_stride,
                                        slots, T, num_pages, Hkv, page_shift(page_size), d,

@@ -291,3 +291,26 @@ def test_a_long_cache_passes_32_bit_offsets():
     ro, rlse, spread = paged.decode(_np(q), _np(kk), _np(vv), np.array([[0]]), [T], d ** -0.5)
     check_o(_np(o), ro, spread)
     check_lse(_np(lse), rlse)
+
+
+@pytest.mark.parametrize("layout", ["behind", "before", "beside", "beside_before", "one_page",
+                                    "gaps"])
+def test_append_takes_pools_in_one_allocation(layout):
+    # keys' and values' pages next to one another in either order, in one block of memory
+    T, Hkv, d, page = 9, 2, 64, 16
+    P = 1 if layout == "one_page" else 4
+    g = _gen(14)
+    k, v = (torch.randn(T, Hkv, d, generator=g).bfloat16() for _ in range(2))
+    slots = torch.randperm(P * page, generator=g)[:T].int()
+    beside = layout in ("beside", "beside_before", "gaps")
+    both = torch.zeros(*((P, 3 if layout == "gaps" else 2) if beside else (2, P)), Hkv, page, d,
+                       dtype=torch.bfloat16, device="cuda")
+    pools = both.unbind(1 if beside else 0)
+    kc, vc = (pools[0], pools[-1]) if "before" not in layout else (pools[1], pools[0])
+    fa.paged_append(k.cuda(), v.cuda(), kc, vc, slots.cuda())
+    _ok()
+    zero = np.zeros((P, Hkv, page, d))
+    for c, x in ((kc, k), (vc, v)):
+        assert np.array_equal(_np(c), paged.append(zero, _np(x), slots.tolist()))
+    if layout == "gaps":
+        assert (pools[1] == 0).all()

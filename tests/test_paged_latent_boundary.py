@@ -228,3 +228,25 @@ def test_binding_refuses_workspaces_that_repeat_their_bytes():
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         fa.fa_latent_bwd(*x, _z(1, 2, 8, 128, dtype=torch.float32),
                          _z(1, 2, 8, dtype=torch.float32), x[3], *x, ws)
+
+
+PAGE = 8 * 16 * 64                          # elements of a page of APPEND's pools
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"vc": X[0]}, INV),                                          # one pool for both
+    ({"vc": X[0] + 2 * (PAGE - 8)}, INV),                         # the last piece of a page
+    ({"vc": X[0] + 2 * PAGE}, INV),                               # the pool a page on
+    ({"kc": X[0] + 2 * 5 * PAGE, "vc": X[0]}, INV),
+    ({"vc": X[0] + 2 * (15 * PAGE + 8)}, INV),                    # its last page
+    ({"ps": 2 * PAGE, "vc": X[0] + 2 * (PAGE - 8)}, INV),         # side by side, but too close
+    ({"ps": 2 * PAGE, "vc": X[0] + 2 * (31 * PAGE - 8)}, INV),
+    ({"ps": 2 * PAGE, "kc": X[0] + 2 * (PAGE + 8), "vc": X[0]}, INV),   # over the next page
+    ({"T": 0, "vc": X[0]}, fa.FA_OK),                             # no rows, nothing to disturb
+    # and the other refusals with pools apart
+    ({"k": None}, INV), ({"v": X[2] + 8}, INV), ({"kc": X[0] + 4}, INV), ({"vc": None}, INV),
+    ({"slots": X[4] + 2}, INV), ({"ks": 504}, INV), ({"vs": 516}, INV), ({"ps": PAGE + 4}, INV),
+])
+def test_append_refuses_pools_that_share_memory(kw, code):
+    base = dict(APPEND, k=X[1], v=X[2], kc=X[0], vc=X[3], slots=X[4])
+    assert _call("fa_paged_append", base, kw) == code
