@@ -46,7 +46,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kPStride = 2 * kFewKeys + 16;   // bytes of a row of P: 16 past a multiple of 128
 constexpr int kQPart = 3 * 64;                // columns of q that pass through shared memory at once
 constexpr int kQStride = 2 * kQPart + 16;     // bytes of a row of them: 16 past a multiple of 128
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units; exact, see fa_fwd_sm103.cu
 static_assert(kRank == 64 * kWarps && kFewKeys == 8 * kWarps, "a warp's share");

@@ -125,7 +125,7 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// ------------------------------------------------------------------ fences
+// ------------------------------------------------------------------ cluster launch control
 
 // Cluster launch control: asks for a block of this grid that has not started yet; its index (or
 // that there is none left) lands as 16 bytes at dst, which complete as a transaction of bar.  No
@@ -150,6 +150,8 @@ __device__ __forceinline__ int next_block_answer(const void* src) {
       : "memory");
   return x;
 }
+
+// ------------------------------------------------------------------ fences
 
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
