@@ -16,8 +16,9 @@
 // warp is done with tile n - 1, and each warp asks for one subtile of tile n + 2 in its stage (all
 // nine by one warp took 1.4k cycles, which the others waited out at the second barrier), the page
 // numbers looked up a tile ago.
-// Measured: 32 sequences of 4096 to 8192 tokens, 16 heads: 57 us for 34 us of bytes (4.4 TB/s);
-// 2 sequences of 901 tokens 12.4 us.
+// All 255 registers are taken, and 72 bytes of a thread's values spill.
+// Measured: 32 sequences of 4096 to 8192 tokens, 16 heads: 58 us for 34 us of bytes (3.9 TB/s), the
+// join in it; 2 sequences of 901 tokens 11.4 us.
 // Work is shared out as fa_paged_sched.cuh says.  Waits are bounded: after an expiry the block
 // runs on without waiting, in step with its barriers, and records FA_ERR_TIMEOUT.
 #include <atomic>

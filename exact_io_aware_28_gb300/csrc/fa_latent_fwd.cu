@@ -7,8 +7,8 @@
 // rescaled only past a 2^8 growth of the maximum).  The shared part is never copied per head: a
 // key tile is two subtiles of the head's own tensor and one of the shared one.
 //
-// What bounds it: 640 operations a (query, key) pair against 832 bytes a key and 128 queries,
-// so the tensor cores, and beside them the softmax.  As in fa_fwd_sm103.cu a CTA owns two tiles
+// What bounds it: 640 operations a (query, key) pair against 640 bytes a key, read once for 256
+// queries, so the tensor cores, and beside them the softmax.  As in fa_fwd_sm103.cu a CTA owns two tiles
 // of 128 query rows, one MMA-issuing thread each, and all eight softmax warps take the tiles in
 // turn: 540 us for 16 heads x 8192 without a mask (1.27 PFLOP/s), 4.1k cycles a pair of tiles
 // and block of which 2.8k are MMAs.  Softmax warps of a tile's own measured slower, both four (a

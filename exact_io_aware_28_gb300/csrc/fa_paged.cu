@@ -7,10 +7,10 @@
 //    list, off being the exclusive sums of the pages lacking.  Token t of the packed new tokens
 //    sits in the request whose range of the exclusive sums of n holds t.  Every block forms
 //    both sums itself (8 B bytes from L2), which costs less than a second launch, and then
-//    takes its share of the list entries and of the tokens.  Latency bounds it: 2.3 us for a step
-//    of 64 requests, 6.6 us for 1024 requests and tables of 512 pages (2.3 MB).
-//  * append: a copy of rows, 16 bytes a thread and access, bound by HBM: 1.7 us for 64 rows,
-//    21.8 us for 16384 rows of 8 x 128 keys and values (134 MB, 6.2 TB/s).
+//    takes its share of the list entries and of the tokens.  Latency bounds it: 2.4 us for a step
+//    of 64 requests, 6.5 us for 1024 requests and tables of 512 pages (2.3 MB).
+//  * append: a copy of rows, 16 bytes a thread and access, bound by HBM: 1.5 us for 64 rows,
+//    21.7 us for 16384 rows of 8 x 128 keys and values (134 MB, 6.2 TB/s).
 //
 // Both launch as dependent kernels (they wait for the previous kernel in the stream before
 // touching global memory).
