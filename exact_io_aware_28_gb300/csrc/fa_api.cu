@@ -526,7 +526,8 @@ fa_status fa_paged_append(const void* k, const void* v, long long k_stride, long
     return FA_ERR_INVALID_ARG;
   if (bad_row_stride(k_stride, (long long)Hkv * d) || bad_row_stride(v_stride, (long long)Hkv * d))
     return FA_ERR_INVALID_ARG;
-  if (!pools_apart(k_cache, v_cache, page_stride, (long long)Hkv * page_size * d, num_pages))
+  const bool same = k == v && k_stride == v_stride && k_cache == v_cache;   // the same bytes twice
+  if (!same && !pools_apart(k_cache, v_cache, page_stride, (long long)Hkv * page_size * d, num_pages))
     return FA_ERR_INVALID_ARG;
   return to_status(launch_paged_append(k, v, k_stride, v_stride, k_cache, v_cache, page_stride,
                                        slots, T, num_pages, Hkv, page_shift(page_size), d,

@@ -580,9 +580,10 @@ def _shaped(name, t, shape, dtype):
 
 
 def _scratch(t):
-    """The workspace's bytes are all its own (an expanded tensor counts some that it does not have)."""
-    if not t.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    """The workspace has the bytes that it counts (an expanded tensor counts some more often)."""
+    if not t.is_contiguous() and t.numel() > 1 + sum((n - 1) * st for n, st in zip(t.shape,
+                                                                                t.stride())):
+        raise ValueError("workspace must be contiguous: it counts bytes that it does not have")
 
 
 def _rows(name, t, shape, dtype=torch.bfloat16):

@@ -366,7 +366,8 @@ fa_status fa_paged_tables(const int32_t* cache_len, const int32_t* new_len,
  *   k, v     in : bf16, token t's rows [Hkv, d] at k + t * k_stride, v + t * v_stride (elements,
  *                 multiples of 8, >= Hkv * d: a slice of a fused projection is taken as it is).
  *   k_cache, v_cache out: bf16 pools [num_pages, Hkv, page_size, d], pages page_stride apart; no
- *                 page of one shares memory with one of the other (FA_ERR_INVALID_ARG).
+ *                 page of one shares memory with one of the other (FA_ERR_INVALID_ARG), unless both
+ *                 are one pool and k and v the same rows.
  *   slots    in : int32 [T]; a slot outside the pool: the token is skipped.  Slots should differ:
  *                 rows that share one are written in no particular order, piece by piece.
  * k and v may be rows of the pools themselves (a copy of tokens), if no slot names one of them.

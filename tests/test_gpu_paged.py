@@ -314,3 +314,17 @@ def test_append_takes_pools_in_one_allocation(layout):
         assert np.array_equal(_np(c), paged.append(zero, _np(x), slots.tolist()))
     if layout == "gaps":
         assert (pools[1] == 0).all()
+
+
+def test_append_of_the_same_rows_to_one_pool():
+    # keys that are the values as well: one pool, the same bytes from both
+    g = _gen(15)
+    x = torch.randn(9, 2, 64, generator=g).bfloat16()
+    slots = torch.randperm(64, generator=g)[:9].int()
+    pool = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    rows = x.cuda()
+    fa.paged_append(rows, rows, pool, pool, slots.cuda())
+    _ok()
+    assert np.array_equal(_np(pool), paged.append(np.zeros((4, 2, 16, 64)), _np(x), slots.tolist()))
+    with pytest.raises(fa.FaError):
+        fa.paged_append(rows, rows.clone(), pool, pool, slots.cuda())

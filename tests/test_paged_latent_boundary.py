@@ -228,6 +228,12 @@ def test_binding_refuses_workspaces_that_repeat_their_bytes():
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         fa.fa_latent_bwd(*x, _z(1, 2, 8, 128, dtype=torch.float32),
                          _z(1, 2, 8, dtype=torch.float32), x[3], *x, ws)
+    # strides that leave room, or another order of the dimensions, do no harm
+    for ws in (torch.zeros(1 << 14, dtype=torch.uint8)[::2], _z(64, 8).t(), _z(4, 8)[:, :0],
+               torch.zeros(200, dtype=torch.uint8).as_strided((2, 4), (100, 0))):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            fa.fa_latent_bwd(*x, _z(1, 2, 8, 128, dtype=torch.float32),
+                             _z(1, 2, 8, dtype=torch.float32), x[3], *x, ws)
 
 
 PAGE = 8 * 16 * 64                          # elements of a page of APPEND's pools
