@@ -601,6 +601,284 @@ fa_status fa_decode_paged(const void* q, const void* k, const void* v, long long
                                        static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+bool bad8(const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 7u) != 0; }
+
+// Rotary positions' plan: axes, turns of the rot / 2 pairs and the axis of each.
+fa_status check_rope(const int32_t* pos, int axes, const int64_t* turns, const int32_t* axis, int d,
+                     int rot) {
+  if (d < 16 || d % 8 != 0 || d > 1024 || rot < 16 || rot % 16 != 0 || rot > d)
+    return FA_ERR_UNSUPPORTED;
+  if (axes < 1 || bad4(pos) || bad8(turns) || bad4(axis)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+// A [B, H, N, d] tensor by its strides (elements): bytes from its first to its last element.
+struct Strided {
+  long long n[3], st[3];
+  int d, esz;
+  Strided(int B, int H, int N, int d_, long long sb, long long sh, long long sn, int esz_)
+      : n{B, H, N}, st{sb, sh, sn}, d(d_), esz(esz_) {}
+  bool fits() const {              // pieces of 16 bytes
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && (st[i] < 0 || st[i] * esz % 16 != 0 || st[i] > (1ll << 40))) return false;
+    return true;
+  }
+  long long bytes() const {
+    long long e = d;
+    for (int i = 0; i < 3; ++i) e += (n[i] - 1) * st[i];
+    return e * esz;
+  }
+  // Every element has a place of its own: each stride passes all that the smaller ones reach.
+  bool distinct() const {
+    bool used[3] = {n[0] == 1, n[1] == 1, n[2] == 1};
+    long long reach = d;
+    for (int k = 0; k < 3; ++k) {
+      int least = -1;
+      for (int i = 0; i < 3; ++i)
+        if (!used[i] && (least < 0 || st[i] < st[least])) least = i;
+      if (least < 0) break;
+      if (st[least] < reach) return false;
+      reach += (n[least] - 1) * st[least];
+      used[least] = true;
+    }
+    return true;
+  }
+  bool same(const Strided& o) const {
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && st[i] != o.st[i]) return false;
+    return true;
+  }
+};
+
+// T rows of ea elements at a, sa apart, and of eb at b, sb apart (bf16), have no element in common.
+// Rows of one buffer (equal strides) may lie between one another.
+bool rows_apart(const void* a, long long sa, long long ea, const void* b, long long sb, long long eb,
+                int T) {
+  const Span x(a, 2 * ((T - 1) * sa + ea)), y(b, 2 * ((T - 1) * sb + eb));
+  if (!x.meets(y)) return true;
+  if (sa != sb || T == 1) return false;
+  const long long S = 2 * sa;
+  const long long r = ((static_cast<long long>(y.begin - x.begin) % S) + S) % S;
+  return r >= 2 * ea && S - r >= 2 * eb;
+}
+
+}  // namespace
+
+fa_status fa_rope(const void* x, void* y, long long x_batch, long long x_head, long long x_token,
+                  long long y_batch, long long y_head, long long y_token, const int32_t* pos,
+                  long long pos_axis, long long pos_batch, int axes, const int64_t* turns,
+                  const int32_t* axis, int B, int H, int N, int d, int rot, int interleaved,
+                  int inverse, fa_dtype dtype, void* stream) {
+  if (B < 1 || H < 1 || N < 1) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
+  fa_status st = check_rope(pos, axes, turns, axis, d, rot);
+  if (st != FA_OK) return st;
+  if (B > 65535 || H > 65535 || N > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  const int esz = dtype == FA_BF16 ? 2 : 4;
+  const Strided xs(B, H, N, d, x_batch, x_head, x_token, esz);
+  const Strided ys(B, H, N, d, y_batch, y_head, y_token, esz);
+  if (bad_ptr(x) || bad_ptr(y) || !xs.fits() || !ys.fits() || !ys.distinct())
+    return FA_ERR_INVALID_ARG;
+  if ((axes > 1 && pos_axis < 0) || (B > 1 && pos_batch < 0)) return FA_ERR_INVALID_ARG;
+  const long long places = (axes - 1) * pos_axis + (B - 1) * pos_batch + N;
+  const bool in_place = x == y && xs.same(ys);
+  const Span ins[] = {{in_place ? nullptr : x, xs.bytes()}, {pos, 4 * places}, {turns, 4ll * rot},
+                      {axis, 2ll * rot}};
+  const Span outs[] = {{y, ys.bytes()}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
+  return to_status(launch_rope(x, y, {x_batch, x_head, x_token}, {y_batch, y_head, y_token}, pos,
+                               pos_axis, pos_batch, axes, reinterpret_cast<const long long*>(turns),
+                               axis, B, H, N, d, rot, interleaved ? 1 : 0, inverse ? 1 : 0, dtype,
+                               static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_rope_append(const void* q, const void* k, const void* v, long long q_stride,
+                         long long k_stride, long long v_stride, void* q_out, long long qo_stride,
+                         void* k_cache, void* v_cache, long long page_stride, const int32_t* slots,
+                         const int32_t* pos, long long pos_axis, int axes, const int64_t* turns,
+                         const int32_t* axis, int T, int Hq, int Hkv, int num_pages, int page_size,
+                         int d, int rot, int interleaved, void* stream) {
+  if (T < 0 || Hq < 1 || Hkv < 1) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || Hq > 65535 || Hkv > 65535 || T > (1 << 26)) return FA_ERR_UNSUPPORTED;
+  const long long page = (long long)Hkv * page_size * d;
+  fa_status st = check_pool(num_pages, page_size, page_stride, page);
+  if (st != FA_OK) return st;
+  if (T == 0) return FA_OK;
+  st = check_rope(pos, axes, turns, axis, d, rot);
+  if (st != FA_OK) return st;
+  if (bad_ptr(q) || bad_ptr(k) || bad_ptr(v) || bad_ptr(q_out) || bad_ptr(k_cache) ||
+      bad_ptr(v_cache) || bad4(slots) || (axes > 1 && pos_axis < 0))
+    return FA_ERR_INVALID_ARG;
+  const long long qe = (long long)Hq * d, ke = (long long)Hkv * d;
+  if (bad_row_stride(q_stride, qe) || bad_row_stride(qo_stride, qe) ||
+      bad_row_stride(k_stride, ke) || bad_row_stride(v_stride, ke))
+    return FA_ERR_INVALID_ARG;
+  const bool in_place = q == q_out && (T == 1 || q_stride == qo_stride);
+  if ((!in_place && !rows_apart(q_out, qo_stride, qe, q, q_stride, qe, T)) ||
+      !rows_apart(q_out, qo_stride, qe, k, k_stride, ke, T) ||
+      !rows_apart(q_out, qo_stride, qe, v, v_stride, ke, T) ||
+      !pools_apart(k_cache, v_cache, page_stride, page, num_pages))
+    return FA_ERR_INVALID_ARG;
+  const Span small[] = {{slots, 4ll * T}, {pos, 4 * ((axes - 1) * pos_axis + T)}, {turns, 4ll * rot},
+                        {axis, 2ll * rot}};
+  const Span rows[] = {{q, 2 * ((T - 1) * q_stride + qe)}, {k, 2 * ((T - 1) * k_stride + ke)},
+                       {v, 2 * ((T - 1) * v_stride + ke)}};
+  const long long pool = pool_bytes(num_pages, page_stride, page);
+  const Span out(q_out, 2 * ((T - 1) * qo_stride + qe)), kc(k_cache, pool), vc(v_cache, pool);
+  if (kc.meets(out) || vc.meets(out)) return FA_ERR_INVALID_ARG;
+  for (const Span& s : small)
+    if (s.meets(out) || s.meets(kc) || s.meets(vc)) return FA_ERR_INVALID_ARG;
+  for (const Span& s : rows)
+    if (s.meets(kc) || s.meets(vc)) return FA_ERR_INVALID_ARG;
+  return to_status(launch_rope_append(q, k, v, q_stride, k_stride, v_stride, q_out, qo_stride,
+                                      k_cache, v_cache, page_stride, slots, pos, pos_axis, axes,
+                                      reinterpret_cast<const long long*>(turns), axis, T, Hq, Hkv,
+                                      num_pages, page_shift(page_size), d, rot, interleaved ? 1 : 0,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// What the operators on a cache's tables have in common.
+fa_status check_pages(const int32_t* cache_len, const int32_t* table, long long table_stride,
+                      int max_pages, int B, int page_size, int num_pages) {
+  if (B < 1) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pool(num_pages, page_size, 8, 8);
+  if (st == FA_OK) st = check_table(table, table_stride, max_pages, page_size);
+  if (st != FA_OK) return st;
+  if (B > 8192 || (long long)B * max_pages * page_size >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  return bad4(cache_len) ? FA_ERR_INVALID_ARG : FA_OK;
+}
+
+}  // namespace
+
+fa_status fa_paged_fork(int32_t* cache_len, int32_t* block_table, long long table_stride,
+                        int max_pages, const int32_t* free_pages, int n_free, const int32_t* src,
+                        const int32_t* dst, int n, int32_t* copy_src, int32_t* copy_dst,
+                        int32_t* copy_rows, int32_t* pages_taken, int B, int page_size,
+                        int num_pages, void* stream) {
+  if (n < 0 || n_free < 0) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pages(cache_len, block_table, table_stride, max_pages, B, page_size,
+                             num_pages);
+  if (st != FA_OK) return st;
+  if (n > 8192) return FA_ERR_UNSUPPORTED;
+  if (bad4(pages_taken) || (n_free > 0 && bad4(free_pages))) return FA_ERR_INVALID_ARG;
+  if (n > 0 && (bad4(src) || bad4(dst) || bad4(copy_src) || bad4(copy_dst) || bad4(copy_rows)))
+    return FA_ERR_INVALID_ARG;
+  const Span ins[] = {{n ? src : nullptr, 4ll * n}, {n ? dst : nullptr, 4ll * n},
+                      {n_free ? free_pages : nullptr, 4ll * n_free}};
+  const Span outs[] = {{cache_len, 4ll * B}, {block_table, 4 * ((B - 1) * table_stride + max_pages)},
+                       {n ? copy_src : nullptr, 4ll * n}, {n ? copy_dst : nullptr, 4ll * n},
+                       {n ? copy_rows : nullptr, 4ll * n}, {pages_taken, 4}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
+  return to_status(launch_paged_fork(cache_len, block_table, table_stride, max_pages, free_pages,
+                                     n_free, src, dst, n, copy_src, copy_dst, copy_rows,
+                                     pages_taken, B, page_shift(page_size), num_pages,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged_free(int32_t* cache_len, int32_t* block_table, long long table_stride,
+                        int max_pages, const int32_t* rows, int n, int32_t* refs,
+                        int32_t* free_pages, int32_t* n_free, int B, int page_size, int num_pages,
+                        void* stream) {
+  if (n < 0) return FA_ERR_INVALID_ARG;
+  fa_status st = check_pages(cache_len, block_table, table_stride, max_pages, B, page_size,
+                             num_pages);
+  if (st != FA_OK) return st;
+  if ((n > 0 && bad4(rows)) || bad4(refs) || bad4(free_pages) || bad4(n_free))
+    return FA_ERR_INVALID_ARG;
+  const Span ins[] = {{n ? rows : nullptr, 4ll * n}};
+  const Span outs[] = {{cache_len, 4ll * B}, {block_table, 4 * ((B - 1) * table_stride + max_pages)},
+                       {refs, 4ll * num_pages}, {free_pages, 4ll * num_pages}, {n_free, 4}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
+  return to_status(launch_paged_free(cache_len, block_table, table_stride, max_pages, rows, n, refs,
+                                     free_pages, n_free, B, page_shift(page_size), num_pages,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged_compact(const int32_t* cache_len, int32_t* block_table, long long table_stride,
+                           int max_pages, int32_t* moved, int32_t* copy_src, int32_t* copy_dst,
+                           int n_copies, int32_t* n_used, int B, int page_size, int num_pages,
+                           void* stream) {
+  fa_status st = check_pages(cache_len, block_table, table_stride, max_pages, B, page_size,
+                             num_pages);
+  if (st != FA_OK) return st;
+  if (n_copies < num_pages / 2 || bad4(moved) || bad4(n_used)) return FA_ERR_INVALID_ARG;
+  if (n_copies > 0 && (bad4(copy_src) || bad4(copy_dst))) return FA_ERR_INVALID_ARG;
+  const Span ins[] = {{cache_len, 4ll * B}};
+  const Span outs[] = {{block_table, 4 * ((B - 1) * table_stride + max_pages)},
+                       {moved, 4ll * num_pages}, {n_copies ? copy_src : nullptr, 4ll * n_copies},
+                       {n_copies ? copy_dst : nullptr, 4ll * n_copies}, {n_used, 4}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
+  return to_status(launch_paged_compact(cache_len, block_table, table_stride, max_pages, moved,
+                                        copy_src, copy_dst, n_copies, n_used, B,
+                                        page_shift(page_size), num_pages,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_paged_copy(void* k_cache, void* v_cache, long long page_stride,
+                        const int32_t* copy_src, const int32_t* copy_dst, const int32_t* copy_rows,
+                        int n, int num_pages, int Hkv, int page_size, int d, void* stream) {
+  if (n < 0 || Hkv < 1) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128 && d != FA_LATENT_RANK + FA_LATENT_ROPE) || Hkv > 65535)
+    return FA_ERR_UNSUPPORTED;
+  const long long page = (long long)Hkv * page_size * d;
+  fa_status st = check_pool(num_pages, page_size, page_stride, page);
+  if (st != FA_OK) return st;
+  if (page / 8 >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (n == 0) return FA_OK;
+  if (bad_ptr(k_cache) || !aligned16(v_cache) || bad4(copy_src) || bad4(copy_dst) ||
+      (copy_rows && bad4(copy_rows)))
+    return FA_ERR_INVALID_ARG;
+  if (v_cache && !pools_apart(k_cache, v_cache, page_stride, page, num_pages))
+    return FA_ERR_INVALID_ARG;
+  const long long pool = pool_bytes(num_pages, page_stride, page);
+  const Span ins[] = {{copy_src, 4ll * n}, {copy_dst, 4ll * n}, {copy_rows, 4ll * n}};
+  for (const Span& s : ins)
+    if (s.meets(Span(k_cache, pool)) || s.meets(Span(v_cache, pool))) return FA_ERR_INVALID_ARG;
+  return to_status(launch_paged_copy(k_cache, v_cache, page_stride, copy_src, copy_dst, copy_rows,
+                                     n, num_pages, Hkv, page_shift(page_size), d,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d) {
+  return check_decode_paged(B, Hq, Hkv, d) == FA_OK ? decode_shared_bytes(B, Hq, Hkv, d) : 0;
+}
+
+fa_status fa_decode_shared(const void* q, const void* k, const void* v, long long page_stride,
+                           const int32_t* block_table, long long table_stride, int max_pages,
+                           const int32_t* cache_len, const int32_t* group_start,
+                           const int32_t* shared_len, int groups, void* o, float* lse, int B,
+                           int Hq, int Hkv, int num_pages, int page_size, int d, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status st = check_decode_paged(B, Hq, Hkv, d);
+  if (st == FA_OK)
+    st = check_pool(num_pages, page_size, page_stride, (long long)Hkv * page_size * d);
+  if (st == FA_OK) st = check_table(block_table, table_stride, max_pages, page_size);
+  if (st != FA_OK) return st;
+  if (bad_ptr(q) || bad_ptr(k) || bad_ptr(v) || bad_ptr(o) || bad_ptr(workspace) || bad4(lse) ||
+      bad4(cache_len) || bad4(group_start) || bad4(shared_len) || groups < 1 || groups > B ||
+      bad_softmax_scale(scale))
+    return FA_ERR_INVALID_ARG;
+  const size_t need = fa_decode_shared_workspace_bytes(B, Hq, Hkv, d);
+  if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
+  const long long rows = (long long)B * Hq;
+  const long long pool = pool_bytes(num_pages, page_stride, (long long)Hkv * page_size * d);
+  const Span ins[] = {{q, rows * d * 2}, {k, pool}, {v, pool}, {cache_len, 4ll * B},
+                      {block_table, 4 * ((B - 1) * table_stride + max_pages)},
+                      {group_start, 4 * (groups + 1ll)}, {shared_len, 4ll * groups}};
+  const Span outs[] = {{o, rows * d * 2}, {lse, rows * 4}, {workspace, (long long)need}};
+  if (!apart(ins, outs)) return FA_ERR_INVALID_ARG;
+  int* err = error_word();
+  if (!err) return FA_ERR_CUDA;
+  return to_status(launch_decode_shared(q, k, v, page_stride, block_table, table_stride, max_pages,
+                                        page_shift(page_size), num_pages, cache_len, group_start,
+                                        shared_len, groups, o, lse, B, Hq, Hkv, d, scale, workspace,
+                                        err, wait_limit_ns(), static_cast<cudaStream_t>(stream)));
+}
+
 size_t fa_latent_decode_workspace_bytes(int B, int H) {
   return check_latent_decode(B, H) == FA_OK ? latent_decode_bytes(B, H) : 0;
 }

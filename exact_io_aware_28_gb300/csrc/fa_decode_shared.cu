@@ -1,0 +1,889 @@
+// Decode attention over a paged cache for groups of sequences that share a prefix: one new query
+// token per sequence, the keys and values of a group's shared tokens read once for all of it.
+//
+// Mathematics.  A sequence's keys are its group's shared ones, j < S, and its own, S <= j < L:
+//   o = (sum over the parts i of 2^(m_i - M) o_i) / (sum of 2^(m_i - M) l_i),
+// with each part's maximum m_i, sum l_i and unnormalised o_i in fp32 (log2 domain, c = scale
+// log2 e).  Over the shared keys the group's queries of one key/value head are the rows of one
+// matrix product, as in a prompt, up to 256 rows a CTA; over its own keys a sequence is what it is
+// in fa_decode_paged.cu.  P is rounded once to bf16 as an operand of P V in both.
+//
+// What bounds it: the bytes of the prefixes, once, and of the continuations; with many sequences a
+// group also the products over the prefix, 4 S d operations a row, on the tensor cores.
+//
+// Work.  All tiles of 128 keys lie on one line: first the prefixes' (group by group, head by head,
+// 256 rows by 256 rows), then the continuations' (sequence by sequence, head by head).  A tile of
+// either kind costs about the same: 64 KB at d = 128 from HBM take an SM some 2.8k cycles when all
+// read, and 256 rows of a prefix tile some 2.6k of products and exponentials.  Worker w of W takes
+// the tiles [total w / W, total (w + 1) / W), so every SM has the same share of the whole, and the
+// one launch has no seam between prefixes and continuations.  Every segment of a pair in a worker's
+// range leaves a partial result in a place of its own: (pair) + (worker) grows along the line, so
+// no two meet.  A combine kernel joins them.  The cut depends on lengths, groups and W alone: the
+// same call gives the same bits.
+//
+// A prefix segment (one CTA, two tiles of up to 128 query rows; a tile holds 128 / G sequences of
+// G heads, in whole sequences):
+//   warps 0, 2 producers of keys and values (a lane per page); warps 1, 3 MMA issuers, one a tile;
+//   warps 4-11 softmax, all of them on each tile in turn: S = Q K^T in tensor memory, P over it as
+//   bf16, O += P V.  A group with rows for one tile only has its queries in both, and the two take
+//   the key tiles in turn.
+// A sequence shorter than its group's shared tokens takes no part in them: it reads its own keys
+// from the first on, and the products it is in are never joined.  Pages outside the pool are holes,
+// as in fa_decode_paged.cu: not loaded, their scores replaced, their V rows zeroed.
+// Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and leaves.
+#include <atomic>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "fa_decode_units.cuh"
+#include "fa_internal.cuh"
+#include "fa_paged_sched.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace {
+
+using namespace decode;
+
+constexpr int kRows = 128;                       // query rows of a tile
+
+template <int D>
+struct PC {
+  static constexpr int NSUB = D / 64;
+  static constexpr int TILE = NSUB * kSub;
+  static constexpr int NST = D == 128 ? 2 : 4;   // stages of a K and a V tile each
+  static constexpr int SMEM = 2 * TILE + 2 * NST * TILE;
+  // The decode's barriers and statistics lie behind what the prefix phase uses.
+  static_assert(SMEM <= TC<D>::STAGES * TC<D>::STAGE, "shared memory");
+};
+constexpr int kSeen = 8;                         // row masks of the last key tiles
+
+struct PBars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
+  uint64_t drain;
+  uint32_t seen[kSeen];
+  uint32_t tmem_base;
+  int abort;
+  int never;
+};
+
+struct SharedArgs {
+  PagedArgs a;                 // of the continuations; a.part their partial results
+  const int32_t* start;        // [groups + 1]
+  const int32_t* len;          // [groups]
+  int groups;
+  int seqs;                    // sequences of a tile: 128 / G
+  float* part;                 // of the prefixes
+  long long entries;           // places in it
+  long long *tiles_g, *tiles_b;  // exclusive sums over groups and sequences, for the combine kernel
+  int32_t* group_of;
+};
+
+__device__ __forceinline__ int cap_of(const PagedArgs& a) { return a.max_pages << a.page_shift; }
+
+struct Group {
+  int s0, s1;                  // its sequences
+  int len;                     // shared tokens; shorter sequences take no part
+  int keys;                    // of them, those read once: whole boxes
+  int supers;                  // pieces of up to 2 x seqs sequences
+  int tiles;
+  __device__ __forceinline__ Group(const SharedArgs& g, int p) {
+    s0 = min(max(g.start[p], 0), g.a.B);
+    s1 = max(s0, min(max(g.start[p + 1], 0), g.a.B));
+    const int box = min(kKeys, 1 << g.a.page_shift);
+    // one sequence alone shares with nobody
+    len = s1 - s0 > 1 ? sched::clamp_len(g.len, p, cap_of(g.a)) : 0;
+    keys = len & ~(box - 1);
+    supers = (s1 - s0 + 2 * g.seqs - 1) / (2 * g.seqs);
+    tiles = sched::granules<kKeys>(keys);
+  }
+  __device__ __forceinline__ long long all(const SharedArgs& g) const {
+    return static_cast<long long>(tiles) * g.a.Hkv * supers;
+  }
+};
+
+// The group of sequence b: the last whose first sequence is not behind it.
+__device__ __forceinline__ int group_at(const SharedArgs& g, int b) {
+  int lo = 0, hi = g.groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (g.start[mid] <= b) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Tokens of sequence b (length L) that it takes from its group.
+__device__ __forceinline__ int shared_of(const SharedArgs& g, const Group& p, int b, int L) {
+  return b >= p.s0 && b < p.s1 && L >= p.len ? p.keys : 0;
+}
+
+struct SharedStart {
+  long long first, last;       // the worker's range of the line
+  long long total_g;           // tiles of the prefixes
+  int p, b, pb;                // group of the first prefix tile; sequence of the first own tile, its group
+  long long before_p, before_b;
+};
+
+// As sched::find_start, for both parts of the line.
+__device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch)[2],
+                                           const SharedArgs& g, int w, int workers, bool write) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = g.a.B, cap = cap_of(g.a);
+  const int per_p = (g.groups + kThreads - 1) / kThreads, per_b = (B + kThreads - 1) / kThreads;
+  const int p0 = min(tid * per_p, g.groups), p1 = min(p0 + per_p, g.groups);
+  const int b0 = min(tid * per_b, B), b1 = min(b0 + per_b, B);
+  const int at0 = b0 < b1 ? group_at(g, b0) : 0;
+  auto own_tiles = [&](int b, int* p) {
+    while (*p + 1 < g.groups && g.start[*p + 1] <= b) ++*p;
+    const int L = sched::clamp_len(g.a.cache_len, b, cap);
+    const Group gr(g, *p);
+    return static_cast<long long>(sched::granules<kKeys>(L - shared_of(g, gr, b, L))) * g.a.Hkv;
+  };
+  long long sum[2] = {0, 0};
+  for (int p = p0; p < p1; ++p) sum[0] += Group(g, p).all(g);
+  {
+    int p = at0;
+    for (int b = b0; b < b1; ++b) sum[1] += own_tiles(b, &p);
+  }
+  long long incl[2] = {sum[0], sum[1]};
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl[i], off);
+      if (lane >= off) incl[i] += up;
+    }
+  if (lane == 31) scratch[warp][0] = incl[0], scratch[warp][1] = incl[1];
+  __syncthreads();
+  long long before[2] = {incl[0] - sum[0], incl[1] - sum[1]}, total[2] = {0, 0};
+  for (int i = 0; i < kThreads / 32; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const long long v = scratch[i][j];
+      if (i < warp) before[j] += v;
+      total[j] += v;
+    }
+  const long long all = total[0] + total[1];
+  const int W = sched::active(all, workers);
+  const long long first = w < W ? sched::range_start(all, w, W) : all;
+  if (tid == 0) {
+    out->first = first;
+    out->last = w < W ? sched::range_start(all, w + 1, W) : all;
+    out->total_g = total[0];
+    out->p = g.groups, out->b = B, out->pb = 0;
+    out->before_p = out->before_b = 0;
+  }
+  __syncthreads();
+  long long at = before[0];
+  if (write || (first >= at && first < at + sum[0]))
+    for (int p = p0; p < p1; ++p) {
+      const long long n = Group(g, p).all(g);
+      if (write) g.tiles_g[p] = at;
+      if (first >= at && first < at + n) out->p = p, out->before_p = at;
+      at += n;
+    }
+  at = before[1];
+  const long long own = first > total[0] ? first - total[0] : 0;
+  if (write || (own >= at && own < at + sum[1])) {
+    int p = at0;
+    for (int b = b0; b < b1; ++b) {
+      const long long n = own_tiles(b, &p);
+      if (write) g.tiles_b[b] = at, g.group_of[b] = p;
+      if (own >= at && own < at + n) out->b = b, out->pb = p, out->before_b = at;
+      at += n;
+    }
+  }
+  if (write && tid == 0) g.tiles_g[g.groups] = total[0], g.tiles_b[B] = total[1];
+  __syncthreads();
+}
+
+// One prefix segment: keys [k0, k1) of (group, head, piece).
+struct PSegment {
+  int p, head, k0, k1;
+  int s0, n;                   // the piece's sequences
+  bool both;                   // it has rows for both tiles
+  long long entry;             // place of its first partial result
+  __device__ __forceinline__ int blocks() const { return (k1 - k0 + kKeys - 1) / kKeys; }
+  // Does tile t take the segment's key tile j?
+  __device__ __forceinline__ bool need(int t, int j) const { return both || (j & 1) == t; }
+  // The number of key tiles that tile t takes.
+  __device__ __forceinline__ int count(int t) const {
+    return both ? blocks() : (blocks() + 1 - t) >> 1;
+  }
+};
+
+// Places of a piece's rows before those of its pair's segments of other workers.
+__device__ __forceinline__ long long first_entry(const SharedArgs& g, const Group& p, int head,
+                                                 int piece) {
+  const int G = g.a.Hq / g.a.Hkv;
+  return 2ll * p.s0 * g.a.Hq + 2ll * head * (p.s1 - p.s0) * G + 2ll * piece * g.seqs * G;
+}
+
+struct PrefixWalk {
+  const SharedArgs& g;
+  int p, w;
+  long long at, last, before;
+  __device__ __forceinline__ PrefixWalk(const SharedArgs& g_, const SharedStart& s, int w_)
+      : g(g_), p(s.p), w(w_), at(s.first), last(min(s.last, s.total_g)), before(s.before_p) {}
+  __device__ __forceinline__ bool next(PSegment& sg) {
+    if (at >= last) return false;
+    for (; p < g.groups; ++p) {
+      const Group gr(g, p);
+      const long long all = gr.all(g);
+      if (at < before + all) {
+        const int pair = static_cast<int>((at - before) / gr.tiles);
+        const long long pair_start = before + static_cast<long long>(pair) * gr.tiles;
+        const int piece = pair % gr.supers;
+        sg.p = p;
+        sg.head = pair / gr.supers;
+        sg.k0 = static_cast<int>(at - pair_start) * kKeys;
+        const int g1 = static_cast<int>(min(static_cast<long long>(gr.tiles), last - pair_start));
+        sg.k1 = min(g1 * kKeys, gr.keys);
+        sg.s0 = gr.s0 + piece * 2 * g.seqs;
+        sg.n = min(2 * g.seqs, gr.s1 - sg.s0);
+        sg.both = sg.n > g.seqs;
+        sg.entry = first_entry(g, gr, sg.head, piece) + 2ll * w * g.seqs * (g.a.Hq / g.a.Hkv);
+        at = pair_start + g1;
+        return true;
+      }
+      before += all;
+    }
+    return false;
+  }
+};
+
+struct OwnWalk {
+  const SharedArgs& g;
+  int b, p, w;
+  long long at, last, before;
+  __device__ __forceinline__ OwnWalk(const SharedArgs& g_, const SharedStart& s, int w_)
+      : g(g_), b(s.b), p(s.pb), w(w_), at(max(s.first - s.total_g, 0ll)), last(s.last - s.total_g),
+        before(s.before_b) {}
+  __device__ __forceinline__ bool next(Segment& sg) {
+    if (at >= last) return false;
+    for (; b < g.a.B; ++b) {
+      while (p + 1 < g.groups && g.start[p + 1] <= b) ++p;
+      const int L = sched::clamp_len(g.a.cache_len, b, cap_of(g.a));
+      const Group gr(g, p);
+      const int from = shared_of(g, gr, b, L);
+      const int n = sched::granules<kKeys>(L - from);
+      const long long all = static_cast<long long>(n) * g.a.Hkv;
+      if (at < before + all) {
+        sg.b = b;
+        sg.head = static_cast<int>((at - before) / n);
+        sg.len = L;
+        sg.pair_start = before + static_cast<long long>(sg.head) * n;
+        const int g0 = static_cast<int>(at - sg.pair_start);
+        const int g1 = static_cast<int>(min(static_cast<long long>(n), last - sg.pair_start));
+        sg.k0 = from + g0 * kKeys;
+        sg.k1 = min(from + g1 * kKeys, L);
+        sg.whole = from == 0 && g0 == 0 && g1 == n;
+        sg.slot = b * g.a.Hkv + sg.head + w;
+        at = sg.pair_start + g1;
+        return true;
+      }
+      before += all;
+    }
+    return false;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUtensorMap& mv,
+                                                const CUtensorMap& mr, const SharedArgs& g,
+                                                uint8_t* base, PBars* bars, uint32_t tb,
+                                                PrefixWalk walk) {
+  using C = PC<D>;
+  const PagedArgs& a = g.a;
+  uint8_t* sQ = base;                            // [2][TILE]
+  uint8_t* sK = sQ + 2 * C::TILE;                // [NST][TILE]
+  uint8_t* sV = sK + C::NST * C::TILE;           // [NST][TILE]
+  volatile int* abort_flag = &bars->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+  PSegment sg;
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA producers
+    const bool keys = warp == 0;
+    const CUtensorMap* map = keys ? &mk : &mv;
+    uint64_t* full = keys ? bars->k_full : bars->v_full;
+    uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
+    const int shift = a.page_shift;
+    const int rows = min(kKeys, 1 << shift), boxes = kKeys / rows;
+    const uint32_t bits = (1u << (rows / 16)) - 1u;
+    bool ok = true;
+    int n = 0, ns = 0;
+    while (ok && walk.next(sg)) {
+      if (keys) {
+        if (ns > 0) {
+          ok = mbar_wait_warp(&bars->q_empty, (ns - 1) & 1, abort_flag, a.err, a.wait_ns);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          const uint32_t box = static_cast<uint32_t>(g.seqs) * G * 128;
+          mbar_arrive_expect_tx(&bars->q_full, 2 * C::NSUB * box);
+          for (int t = 0; t < 2; ++t)
+            for (int s = 0; s < C::NSUB; ++s)
+              tma_load_4d(sQ + t * C::TILE + s * kSub, &mr, &bars->q_full, 64 * s, 0, sg.head,
+                          sg.s0 + (sg.both ? t * g.seqs : 0));
+        }
+      }
+      // The table row of the group's first sequence that has all of the shared tokens.
+      const Group gr(g, sg.p);
+      int rep = -1;
+      for (int b = gr.s0; rep < 0 && b < gr.s1; b += 32) {
+        const bool has = b + lane < gr.s1 &&
+                         sched::clamp_len(a.cache_len, b + lane, cap_of(a)) >= gr.len;
+        const uint32_t hit = __ballot_sync(0xffffffffu, has);
+        if (hit) rep = b + __ffs(hit) - 1;
+      }
+      const int32_t* row = a.table + max(rep, 0) * a.table_stride;
+      for (int k0 = sg.k0; k0 < sg.k1; k0 += kKeys, ++n) {
+        const int st = n % C::NST;
+        const int x = k0 + lane * rows;
+        int p = -1;
+        if (lane < boxes && x < sg.k1 && rep >= 0) p = row[x >> shift];
+        const bool in = p >= 0 && p < a.num_pages;
+        const uint32_t pages = __ballot_sync(0xffffffffu, in);
+        if (n >= C::NST) {
+          ok = mbar_wait_warp(&empty[st], ((n / C::NST) - 1) & 1, abort_flag, a.err, a.wait_ns);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          if (keys) {
+            uint32_t seen = 0;
+            for (int i = 0; i < boxes; ++i)
+              if (pages >> i & 1u) seen |= bits << (i * (rows / 16));
+            bars->seen[n % kSeen] = seen;
+          }
+          mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(pages)) * rows * D * 2);
+        }
+        __syncwarp();
+        if (in) {
+          uint8_t* dst = (keys ? sK : sV) + st * C::TILE + lane * rows * 128;
+          const int y = x & ((1 << shift) - 1);
+#pragma unroll
+          for (int s = 0; s < C::NSUB; ++s)
+            tma_load_4d(dst + s * kSub, map, &full[st], 64 * s, y, sg.head, p);
+        }
+      }
+      ++ns;
+    }
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ MMA issuers, one a tile
+    // Both walk every stage (a stage is free when both have released it).  In the order of one
+    // thread's MMAs the scores of the tile's next key tile follow the product that reads its P.
+    if (lane == 0) {
+      const int t = warp == 1 ? 0 : 1;
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+      const uint64_t dQ = sw128_desc(smem_u32(sQ + t * C::TILE), 16, 1024);
+      const uint64_t dK0 = sw128_desc(smem_u32(sK), 16, 1024);
+      const uint64_t dV0 = sw128_desc(smem_u32(sV), kSub, 1024);
+      constexpr uint64_t kTileD = C::TILE >> 4;
+      const uint32_t tS = tb + t * 128, tO = tb + 256 + t * 128;
+      bool ok = true;
+      int n = 0, ns = 0, npv = 0, nout = 0;
+      auto scores = [&](int m) {         // of the m-th key tile
+        const uint64_t dK = dK0 + static_cast<uint64_t>(m % C::NST) * kTileD;
+#pragma unroll
+        for (int q = 0; q < C::NSUB; ++q) {
+          uint64_t da[4], db[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t off = static_cast<uint64_t>((q * kSub + k * 32) >> 4);
+            da[k] = dQ + off;
+            db[k] = dK + off;
+          }
+          mma_ss_x4(tS, da, db, idS, q > 0 ? 1u : 0u);
+        }
+        mma_commit(&bars->s_full[t]);
+      };
+      auto wait_full = [&](uint64_t* full, int m) {
+        ok = mbar_wait(&full[m % C::NST], (m / C::NST) & 1, abort_flag, a.err, a.wait_ns);
+        return ok;
+      };
+      while (ok && walk.next(sg)) {
+        const int blocks = sg.blocks(), mine = sg.count(t);
+        ok = mbar_wait(&bars->q_full, ns & 1, abort_flag, a.err, a.wait_ns);
+        if (!ok || !wait_full(bars->k_full, n)) break;
+        tc_fence_after();
+        if (sg.need(t, 0)) scores(n);
+        mma_commit(&bars->k_empty[n % C::NST]);
+        if (blocks == 1) mma_commit(&bars->q_empty);
+        int done = 0;
+        for (int j = 0; j < blocks; ++j, ++n) {
+          if (!wait_full(bars->v_full, n)) break;
+          if (j + 1 < blocks && !wait_full(bars->k_full, n + 1)) break;
+          tc_fence_after();
+          if (sg.need(t, j)) {
+            ok = mbar_wait(&bars->p_full[t], npv & 1, abort_flag, a.err, a.wait_ns);
+            // the previous segment's O has been read
+            if (ok && done == 0 && nout > 0)
+              ok = mbar_wait(&bars->o_empty[t], (nout - 1) & 1, abort_flag, a.err, a.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dV = dV0 + static_cast<uint64_t>(n % C::NST) * kTileD;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t ta[4];
+              uint64_t db[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                ta[k] = tS + 8 * (4 * q + k);
+                db[k] = dV + static_cast<uint64_t>((2048 * (4 * q + k)) >> 4);
+              }
+              mma_ts_x4(tO, ta, db, idO, (done > 0 || q > 0) ? 1u : 0u);
+            }
+            ++npv;
+            if (++done == mine) mma_commit(&bars->o_done[t]);
+          }
+          mma_commit(&bars->v_empty[n % C::NST]);
+          if (j + 1 < blocks) {
+            if (sg.need(t, j + 1)) scores(n + 1);
+            mma_commit(&bars->k_empty[(n + 1) % C::NST]);
+            if (j + 2 == blocks) mma_commit(&bars->q_empty);
+          }
+        }
+        if (mine > 0) ++nout;
+        ++ns;
+      }
+      // Every MMA issued by either thread has completed before tensor memory is used again.
+      mma_commit(&bars->drain);
+      mbar_wait(&bars->drain, 0, &bars->never, nullptr, a.wait_ns);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax warps
+    // Warp 4 + q + 4 h owns rows 32 q + 16 h + [0, 16) of both tiles: thread t has rows
+    // A = 32 q + 16 h + t / 4 and B = A + 8, keys 8 c + 2 (t % 4) + {0, 1}.
+    const int q4 = warp & 3, hh = (warp - 4) >> 2, t4 = lane & 3;
+    const int rA = 32 * q4 + 16 * hh + (lane >> 2), rB = rA + 8;
+    const uint32_t lane_base = tb + (static_cast<uint32_t>(32 * q4 + 16 * hh) << 16);
+    const uint64_t c2 = f2_pack(a.c, a.c);
+    int n = 0, n_s[2] = {0, 0}, n_out[2] = {0, 0};
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int blocks = sg.blocks();
+      float m_run[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+      float l_part[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      for (int j = 0; j < blocks && ok; ++j, ++n) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || !sg.need(t, j)) continue;
+          ok = mbar_wait_warp(&bars->s_full[t], n_s[t] & 1, abort_flag, a.err, a.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t v[64];
+          tmem_ld_16x256b_x16_wait(lane_base + t * 128, v);
+          float sv[64];
+#pragma unroll
+          for (int i = 0; i < 64; ++i) sv[i] = __uint_as_float(v[i]);
+          const uint32_t seen = bars->seen[n % kSeen];
+          const int lim = min(sg.k1 - (sg.k0 + j * kKeys), kKeys);
+          const bool edge = lim < kKeys || seen != 0xffu;
+          if (edge) {
+#pragma unroll
+            for (int cc = 0; cc < 16; ++cc) {
+              // the limit is a multiple of 16, as the pages are
+              if (16 * (cc >> 1) >= lim || !((seen >> (cc >> 1)) & 1u))
+                sv[4 * cc] = sv[4 * cc + 1] = sv[4 * cc + 2] = sv[4 * cc + 3] = -INFINITY;
+            }
+          }
+          float ma0 = fmaxf(sv[0], sv[1]), ma1 = fmaxf(sv[4], sv[5]);
+          float mb0 = fmaxf(sv[2], sv[3]), mb1 = fmaxf(sv[6], sv[7]);
+#pragma unroll
+          for (int cc = 2; cc < 16; cc += 2) {
+            ma0 = fmax3(ma0, sv[4 * cc], sv[4 * cc + 1]);
+            mb0 = fmax3(mb0, sv[4 * cc + 2], sv[4 * cc + 3]);
+            ma1 = fmax3(ma1, sv[4 * cc + 4], sv[4 * cc + 5]);
+            mb1 = fmax3(mb1, sv[4 * cc + 6], sv[4 * cc + 7]);
+          }
+          float mA = fmaxf(ma0, ma1), mB = fmaxf(mb0, mb1);
+          mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 1));
+          mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 1));
+          mA = fmaxf(mA, __shfl_xor_sync(0xffffffffu, mA, 2));
+          mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 2));
+          mA *= a.c;
+          mB *= a.c;
+          const float oldA = m_run[t][0], oldB = m_run[t][1];
+          const float newA = mA > oldA + kRescaleThreshold ? mA : oldA;
+          const float newB = mB > oldB + kRescaleThreshold ? mB : oldB;
+          const bool chA = newA != oldA, chB = newB != oldB;
+          const float alphaA = chA ? ex2(oldA - newA) : 1.f;   // old = -inf gives 0
+          const float alphaB = chB ? ex2(oldB - newB) : 1.f;
+          const float useA = newA == -INFINITY ? 0.f : newA;
+          const float useB = newB == -INFINITY ? 0.f : newB;
+          const uint64_t nA = f2_pack(-useA, -useA), nB = f2_pack(-useB, -useB);
+          uint64_t accA = f2_pack(0.f, 0.f), accB = accA;
+          uint32_t pk[32];
+#pragma unroll
+          for (int cc = 0; cc < 16; ++cc) {
+            const float2 xa = f2_unpack(ffma2(f2_pack(sv[4 * cc], sv[4 * cc + 1]), c2, nA));
+            const float2 xb = f2_unpack(ffma2(f2_pack(sv[4 * cc + 2], sv[4 * cc + 3]), c2, nB));
+            const float pa0 = ex2(xa.x), pa1 = ex2(xa.y);
+            const float pb0 = ex2(xb.x), pb1 = ex2(xb.y);
+            accA = fadd2(accA, f2_pack(pa0, pa1));
+            accB = fadd2(accB, f2_pack(pb0, pb1));
+            pk[2 * cc] = pack_bf16x2(pa0, pa1);
+            pk[2 * cc + 1] = pack_bf16x2(pb0, pb1);
+          }
+          tmem_st_16x128b_x16(lane_base + t * 128, pk);
+          const float2 sa = f2_unpack(accA), sb = f2_unpack(accB);
+          l_part[t][0] = l_part[t][0] * alphaA + (sa.x + sa.y);
+          l_part[t][1] = l_part[t][1] * alphaB + (sb.x + sb.y);
+          m_run[t][0] = newA;
+          m_run[t][1] = newB;
+          // Rescale the running O; the products issued before the scores just read are done.
+          if (j > (sg.both ? 0 : t) && __any_sync(0xffffffffu, chA || chB)) {
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+              uint32_t o[32];
+              const uint32_t oaddr = lane_base + 256 + t * 128 + 64 * half;
+              tmem_ld_16x256b_x8_wait(oaddr, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * ((i & 2) ? alphaB : alphaA));
+              tmem_st_16x256b_x8(oaddr, o);
+            }
+          }
+          if (edge && (t == 0 || !sg.both)) {
+            // Hidden rows of V: zero, so that 0 x (anything) stays 0.  The stage is this tile's once
+            // its load has completed.
+            ok = mbar_wait_warp(&bars->v_full[n % C::NST], (n / C::NST) & 1, abort_flag, a.err,
+                                a.wait_ns);
+            if (!ok) break;
+            const int i = tid - 128, r = i & 127;
+            if (r >= lim || !((seen >> (r >> 4)) & 1u)) {
+              uint8_t* vt = sV + (n % C::NST) * C::TILE + r * 128;
+#pragma unroll
+              for (int ch = 0; ch < 4 * C::NSUB; ++ch) {
+                const int at = (i >> 7) * 4 * C::NSUB + ch;      // 16-byte piece of the row
+                *reinterpret_cast<uint4*>(vt + (at >> 3) * kSub + (at & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[t]);
+          ++n_s[t];
+        }
+      }
+      if (!ok) break;
+      // ---- the segment's partial results
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const bool any = sg.count(t) > 0;
+        if (any) {
+          ok = mbar_wait_warp(&bars->o_done[t], n_out[t] & 1, abort_flag, a.err, a.wait_ns);
+          if (!ok) break;
+          ++n_out[t];
+          tc_fence_after();
+        }
+        float lA = l_part[t][0], lB = l_part[t][1];
+        lA += __shfl_xor_sync(0xffffffffu, lA, 1);
+        lB += __shfl_xor_sync(0xffffffffu, lB, 1);
+        lA += __shfl_xor_sync(0xffffffffu, lA, 2);
+        lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+        // Rows of the tile, and the place of its first; group starts that are not ascending may
+        // lead past the end, where nothing is written.
+        const int rows = (sg.both ? (t == 0 ? g.seqs : sg.n - g.seqs) : sg.n) * G;
+        const long long e0 = sg.entry + (t == 0 ? 0 : (sg.both ? g.seqs : sg.n) * G);
+        const bool wA = rA < rows && e0 + rA < g.entries, wB = rB < rows && e0 + rB < g.entries;
+        float* outA = g.part + (e0 + rA) * TC<D>::PSTRIDE;
+        float* outB = g.part + (e0 + rB) * TC<D>::PSTRIDE;
+        if (any) {
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half) {
+            uint32_t ov[32];
+            tmem_ld_16x256b_x8_wait(lane_base + 256 + t * 128 + 64 * half, ov);
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc) {
+              const int col = 64 * half + 8 * cc + 2 * t4;
+              if (wA)
+                *reinterpret_cast<float2*>(outA + col) =
+                    make_float2(__uint_as_float(ov[4 * cc]), __uint_as_float(ov[4 * cc + 1]));
+              if (wB)
+                *reinterpret_cast<float2*>(outB + col) =
+                    make_float2(__uint_as_float(ov[4 * cc + 2]), __uint_as_float(ov[4 * cc + 3]));
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&bars->o_empty[t]);
+        }
+        if (t4 == 0) {
+          if (wA) *reinterpret_cast<float2*>(outA + D) = make_float2(m_run[t][0], lA);
+          if (wB) *reinterpret_cast<float2*>(outB + D) = make_float2(m_run[t][1], lB);
+        }
+      }
+    }
+  }
+}
+
+template <int D, int GP>
+__global__ void __launch_bounds__(kThreads, 1)
+decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                     const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mr,
+                     const __grid_constant__ SharedArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const Smem<D> sh(base);
+  __shared__ PBars pb;
+  __shared__ SharedStart start;
+  __shared__ long long scan[kThreads / 32][2];
+  const int tid = threadIdx.x, warp = tid >> 5;
+
+  if (tid == 0) {
+    mbar_init(&pb.q_full, 1);
+    mbar_init(&pb.q_empty, 2);
+    for (int s = 0; s < PC<D>::NST; ++s) {
+      mbar_init(&pb.k_full[s], 1);
+      mbar_init(&pb.k_empty[s], 2);
+      mbar_init(&pb.v_full[s], 1);
+      mbar_init(&pb.v_empty[s], 2);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&pb.s_full[t], 1);
+      mbar_init(&pb.p_full[t], 256);
+      mbar_init(&pb.o_done[t], 1);
+      mbar_init(&pb.o_empty[t], 256);
+    }
+    mbar_init(&pb.drain, 2);
+    pb.abort = 0;
+    pb.never = 0;
+    init_bars<D>(sh.bars);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mr);
+  }
+  if (warp == 2) {
+    tmem_alloc(&pb.tmem_base, 512);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  find_start(&start, scan, g, blockIdx.x, gridDim.x, blockIdx.x == 0);
+  const uint32_t tb = pb.tmem_base;
+  if (start.first < min(start.last, start.total_g)) {
+    prefix_segments<D>(mk, mv, mr, g, base, &pb, tb, PrefixWalk(g, start, blockIdx.x));
+    // The tiles' memory, shared and tensor, goes over to the continuations.
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  if (!pb.abort && start.last > max(start.first, start.total_g))
+    segments<D, GP>(mk, mv, mq, g.a, sh, tb, OwnWalk(g, start, blockIdx.x));
+
+  tc_fence_before();
+  __syncthreads();
+  if ((pb.abort || sh.bars->abort) && tid == 0) {
+    // Let any copy still in flight land before the CTA's shared memory is released.
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {
+    }
+  }
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+}
+
+// Joins a row's partial results; o = 0, lse = -inf for an empty sequence.  A warp per (sequence,
+// query head).
+template <int D>
+__global__ void __launch_bounds__(256) decode_shared_combine_kernel(
+    const __grid_constant__ SharedArgs g, int workers) {
+  constexpr int PS = TC<D>::PSTRIDE, PER = D / 32;
+  griddep_wait();
+  griddep_launch_dependents();
+  const PagedArgs& a = g.a;
+  const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+  const long long row = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(a.B) * a.Hq) return;
+  const int b = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
+  const int head = hq / G, h = hq % G, p = g.group_of[b];
+  const long long total_g = g.tiles_g[g.groups], total = total_g + g.tiles_b[a.B];
+  const long long t0 = g.tiles_b[b], n = (g.tiles_b[b + 1] - t0) / a.Hkv;
+  const Group gr(g, p);
+  const int shared = shared_of(g, gr, b, sched::clamp_len(a.cache_len, b, cap_of(a)));
+  workers = sched::active(total, workers);
+  int w0 = 0, own = 0;                           // the continuation's parts
+  if (n > 0) {
+    const long long first = total_g + t0 + head * n;
+    w0 = sched::owner(first, total, workers);
+    own = sched::owner(first + n - 1, total, workers) - w0 + 1;
+    if (shared == 0 && own == 1) return;         // finished by its CTA
+  }
+  int v0 = 0, pre = 0, step = 0;                 // the prefix's
+  long long e0 = 0, e1 = 0;
+  if (shared > 0) {
+    const int piece = (b - gr.s0) / (2 * g.seqs), s = (b - gr.s0) % (2 * g.seqs);
+    const int seqs = min(2 * g.seqs, gr.s1 - gr.s0 - piece * 2 * g.seqs);
+    const long long first =
+        g.tiles_g[p] + (static_cast<long long>(head) * gr.supers + piece) * gr.tiles;
+    v0 = sched::owner(first, total, workers);
+    pre = sched::owner(first + gr.tiles - 1, total, workers) - v0 + 1;
+    e0 = first_entry(g, gr, head, piece) + s * G + h;
+    step = 2 * g.seqs * G;
+    // Rows of one tile only: two results a worker, of the even and the odd key tiles.
+    if (seqs <= g.seqs) e1 = seqs * G;
+  }
+  const int twice = e1 > 0 ? 1 : 0, parts = (pre << twice) + own;
+  auto at = [&](int i) -> const float* {
+    if (i < pre << twice) {
+      const long long e =
+          e0 + static_cast<long long>(v0 + (i >> twice)) * step + (i & twice) * e1;
+      return g.part + min(e, g.entries - 1) * PS;
+    }
+    return a.part + ((static_cast<long long>(b) * a.Hkv + head + w0 + i - (pre << twice)) * G + h) * PS;
+  };
+  float acc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  float M = -INFINITY, lsum = 0.f;
+  for (int base = 0; base < parts; base += 32) {
+    const int mine = base + lane;
+    const float* q = at(mine < parts ? mine : base);
+    const float m = mine < parts ? q[D] : -INFINITY, l = mine < parts ? q[D + 1] : 0.f;
+    const float mb = fmaxf(M, warp_max(m));
+    const float use = mb == -INFINITY ? 0.f : mb;
+    const float keep = ex2(M - use);             // M = -inf gives 0
+    const float wt = ex2(m - use);
+    M = mb;
+    lsum = lsum * keep + l * wt;                 // without a key l is 0, of a NaN query NaN
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] *= keep;
+    const uint32_t has = __ballot_sync(0xffffffffu, m != -INFINITY);   // a part without a key has no o
+    const int cnt = min(32, parts - base);
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      if (!(has >> j & 1u)) continue;
+      const float wj = __shfl_sync(0xffffffffu, wt, j);
+      const float* pj = at(base + j) + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(pj);
+        acc[0] = fmaf(wj, v.x, acc[0]);
+        acc[1] = fmaf(wj, v.y, acc[1]);
+        acc[2] = fmaf(wj, v.z, acc[2]);
+        acc[3] = fmaf(wj, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(pj);
+        acc[0] = fmaf(wj, v.x, acc[0]);
+        acc[1] = fmaf(wj, v.y, acc[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;   // a NaN sum stays one
+  __nv_bfloat16* orow = a.o + static_cast<size_t>(row) * D + lane * PER;
+#pragma unroll
+  for (int i = 0; i < PER; i += 2)
+    *reinterpret_cast<uint32_t*>(orow + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0) a.lse[row] = lsum == 0.f ? -INFINITY : (M + __log2f(lsum)) * kLn2;
+}
+
+template <int D, int GP>
+cudaError_t launch_g(const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
+                     const CUtensorMap& mr, const SharedArgs& g, int workers, cudaStream_t s) {
+  static std::atomic<bool> attr_set[64];  // per device; a race repeats the same call
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
+    cudaError_t e = cudaFuncSetAttribute(decode_shared_kernel<D, GP>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev].store(true);
+  }
+  cudaError_t e = launch_dependent(decode_shared_kernel<D, GP>, dim3(workers), dim3(kThreads),
+                                   TC<D>::SMEM, s, mk, mv, mq, mr, g);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(g.a.B) * g.a.Hq;
+  return launch_dependent(decode_shared_combine_kernel<D>,
+                          dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, g, workers);
+}
+
+template <int D>
+cudaError_t launch_d(const void* q, const void* k, const void* v, long long page_stride,
+                     const SharedArgs& g, int workers, cudaStream_t s) {
+  CUtensorMap mk, mv, mq, mr;
+  const PagedArgs& a = g.a;
+  const int page = 1 << a.page_shift, rows = page < kKeys ? page : kKeys, G = a.Hq / a.Hkv;
+  // The rows of a prefix tile: G heads of `seqs` sequences, from [B, Hkv, G, d].
+  if (!make_page_map(&mk, k, a.num_pages, a.Hkv, page, D, page_stride, rows) ||
+      !make_page_map(&mv, v, a.num_pages, a.Hkv, page, D, page_stride, rows) ||
+      !make_head_map_rows(&mq, q, 1, a.B * a.Hq, D, kN) ||
+      !make_query_map(&mr, q, a.B, a.Hkv, G, D, g.seqs))
+    return cudaErrorInvalidValue;
+  if (G > 8) return launch_g<D, 16>(mk, mv, mq, mr, g, workers, s);
+  if (G > 4) return launch_g<D, 8>(mk, mv, mq, mr, g, workers, s);
+  if (G > 2) return launch_g<D, 4>(mk, mv, mq, mr, g, workers, s);
+  if (G > 1) return launch_g<D, 2>(mk, mv, mq, mr, g, workers, s);
+  return launch_g<D, 1>(mk, mv, mq, mr, g, workers, s);
+}
+
+// Places for the prefixes' partial results: two a row (the even and the odd key tiles), and a
+// piece's rows for every worker that begins inside a pair.
+long long prefix_entries(int B, int Hq, int G) {
+  return 2ll * B * Hq + 2ll * sm_count() * (kRows / G) * G;
+}
+long long own_entries(int B, int Hkv, int G) {
+  return (static_cast<long long>(B) * Hkv + sm_count()) * G;
+}
+
+}  // namespace
+
+size_t decode_shared_bytes(int B, int Hq, int Hkv, int d) {
+  const int G = Hq / Hkv;
+  const size_t entry = (d + 4) * sizeof(float);
+  return round_up(prefix_entries(B, Hq, G) * entry, 256) +
+         round_up(own_entries(B, Hkv, G) * entry, 256) +
+         2 * (static_cast<size_t>(B) + 1) * sizeof(long long) + B * sizeof(int32_t);
+}
+
+cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
+                                 long long page_stride, const int32_t* table,
+                                 long long table_stride, int max_pages, int page_shift,
+                                 int num_pages, const int32_t* cache_len, const int32_t* start,
+                                 const int32_t* shared_len, int groups, void* o, float* lse, int B,
+                                 int Hq, int Hkv, int d, float scale, void* workspace, int* err,
+                                 unsigned long long wait_ns, cudaStream_t s) {
+  const int G = Hq / Hkv;
+  const size_t entry = (d + 4) * sizeof(float);
+  char* at = static_cast<char*>(workspace);
+  SharedArgs g{};
+  g.entries = prefix_entries(B, Hq, G);
+  g.part = reinterpret_cast<float*>(at);
+  at += round_up(g.entries * entry, 256);
+  g.a = PagedArgs{table, table_stride, max_pages, page_shift, num_pages, cache_len, B, Hq, Hkv,
+                  scale * kLog2e, static_cast<__nv_bfloat16*>(o), lse,
+                  reinterpret_cast<float*>(at), nullptr, err, wait_ns};
+  at += round_up(own_entries(B, Hkv, G) * entry, 256);
+  g.tiles_g = reinterpret_cast<long long*>(at);
+  g.tiles_b = g.tiles_g + B + 1;
+  g.group_of = reinterpret_cast<int32_t*>(g.tiles_b + B + 1);
+  g.start = start;
+  g.len = shared_len;
+  g.groups = groups;
+  g.seqs = kRows / G;
+  // No more CTAs than there can be tiles: a sequence's own, and with two of them a prefix's.
+  const long long most = (static_cast<long long>(max_pages) << page_shift) + kKeys - 1;
+  const long long tiles = 2ll * B * Hkv * (most / kKeys);
+  const int workers = tiles < sm_count() ? static_cast<int>(tiles) : sm_count();
+  return d == 64 ? launch_d<64>(q, k, v, page_stride, g, workers, s)
+                 : launch_d<128>(q, k, v, page_stride, g, workers, s);
+}
+
+}  // namespace fa

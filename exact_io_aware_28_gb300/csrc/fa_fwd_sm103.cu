@@ -557,6 +557,23 @@ bool make_page_map(CUtensorMap* map, const void* ptr, int P, int heads, int page
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Decode queries [B, heads, group, d] bf16; 64-column boxes of one head's `group` rows of `seqs`
+// sequences, 128B swizzle, sequences beyond B read as zero.
+bool make_query_map(CUtensorMap* map, const void* ptr, int B, int heads, int group, int d,
+                    int seqs) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(group),
+                        static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(group) * d * 2,
+                           static_cast<cuuint64_t>(heads) * group * d * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), 1, static_cast<cuuint32_t>(seqs)};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [B*H, N, d] fp32 accumulator as a 3-D tensor with 32 x 32 boxes (128-byte rows, 128-byte
 // swizzle); rows beyond N are outside the map, so a box that overhangs the sequence end is
 // clipped.

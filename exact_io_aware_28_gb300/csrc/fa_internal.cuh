@@ -150,6 +150,50 @@ cudaError_t launch_latent_decode(const void* q, const void* cache, long long pag
                                  float* lse, int B, int H, float scale, void* workspace, int* err,
                                  unsigned long long wait_ns, cudaStream_t s);
 
+// Decode for groups of sequences with a prefix in common (fa_decode_shared.cu).
+size_t decode_shared_bytes(int B, int Hq, int Hkv, int d);
+cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
+                                 long long page_stride, const int32_t* table,
+                                 long long table_stride, int max_pages, int page_shift,
+                                 int num_pages, const int32_t* cache_len, const int32_t* start,
+                                 const int32_t* shared_len, int groups, void* o, float* lse, int B,
+                                 int Hq, int Hkv, int d, float scale, void* workspace, int* err,
+                                 unsigned long long wait_ns, cudaStream_t s);
+// Tensor map of decode queries [B, heads, group, d] with boxes of `seqs` sequences of one head.
+bool make_query_map(CUtensorMap* map, const void* ptr, int B, int heads, int group, int d,
+                    int seqs);
+
+// Rotary positions (fa_rope.cu); strides of batch, head and token in elements.
+cudaError_t launch_rope(const void* x, void* y, const long long (&xs)[3], const long long (&ys)[3],
+                        const int32_t* pos, long long pos_axis, long long pos_batch, int axes,
+                        const long long* turns, const int32_t* axis, int B, int H, int N, int d,
+                        int rot, int interleaved, int inverse, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_rope_append(const void* q, const void* k, const void* v, long long q_stride,
+                               long long k_stride, long long v_stride, void* q_out,
+                               long long qo_stride, void* k_cache, void* v_cache,
+                               long long page_stride, const int32_t* slots, const int32_t* pos,
+                               long long pos_axis, int axes, const long long* turns,
+                               const int32_t* axis, int T, int Hq, int Hkv, int num_pages,
+                               int page_shift, int d, int rot, int interleaved, cudaStream_t s);
+
+// The pages of a paged cache (fa_pages.cu).
+cudaError_t launch_paged_fork(int32_t* cache_len, int32_t* table, long long table_stride,
+                              int max_pages, const int32_t* free_pages, int n_free,
+                              const int32_t* src, const int32_t* dst, int n, int32_t* copy_src,
+                              int32_t* copy_dst, int32_t* copy_rows, int32_t* pages_taken, int B,
+                              int page_shift, int num_pages, cudaStream_t s);
+cudaError_t launch_paged_free(int32_t* cache_len, int32_t* table, long long table_stride,
+                              int max_pages, const int32_t* rows, int n, int32_t* refs,
+                              int32_t* free_pages, int32_t* n_free, int B, int page_shift,
+                              int num_pages, cudaStream_t s);
+cudaError_t launch_paged_compact(const int32_t* cache_len, int32_t* table, long long table_stride,
+                                 int max_pages, int32_t* moved, int32_t* copy_src,
+                                 int32_t* copy_dst, int n_copies, int32_t* n_used, int B,
+                                 int page_shift, int num_pages, cudaStream_t s);
+cudaError_t launch_paged_copy(void* k_cache, void* v_cache, long long page_stride,
+                              const int32_t* src, const int32_t* dst, const int32_t* rows, int n,
+                              int num_pages, int heads, int page_shift, int d, cudaStream_t s);
+
 // Expanded latent attention: fp32 tensors on the CUDA cores (fa_latent_simt.cu), bf16 on the
 // tensor cores (fa_latent_fwd.cu, fa_latent_bwd.cu).  Problem::d and the block mask are unused.
 using LatentProblem = Problem;

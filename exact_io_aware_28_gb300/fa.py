@@ -7,6 +7,7 @@ has not been built, every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -27,7 +28,9 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bwd_preprocess", "f
            "fa_attn_merge", "fa_grad_accumulate", "fa_grad_finish",
            "fa_paged_tables", "fa_paged_append", "fa_decode_paged_workspace_bytes",
            "fa_decode_paged", "fa_latent_fwd", "fa_latent_bwd_workspace_bytes", "fa_latent_bwd",
-           "fa_latent_append", "fa_latent_decode_workspace_bytes", "fa_latent_decode")
+           "fa_latent_append", "fa_latent_decode_workspace_bytes", "fa_latent_decode",
+           "fa_decode_shared_workspace_bytes", "fa_decode_shared", "fa_paged_fork",
+           "fa_paged_free", "fa_paged_compact", "fa_paged_copy", "fa_rope", "fa_rope_append")
 
 # Columns of latent attention: the latent vector, the keys' rotated part, a head's own key part
 # and its values.
@@ -130,6 +133,24 @@ def load() -> ctypes.CDLL:
     lib.fa_latent_decode_workspace_bytes.restype = S
     lib.fa_latent_decode.argtypes = [P, P, L, P, L, I, P, P, P, I, I, I, I, F, P, S, P]
     lib.fa_latent_decode.restype = I
+    lib.fa_decode_shared_workspace_bytes.argtypes = [I, I, I, I]
+    lib.fa_decode_shared_workspace_bytes.restype = S
+    lib.fa_decode_shared.argtypes = [P, P, P, L, P, L, I, P, P, P, I, P, P, I, I, I, I, I, I, F, P,
+                                     S, P]
+    lib.fa_decode_shared.restype = I
+    lib.fa_paged_fork.argtypes = [P, P, L, I, P, I, P, P, I, P, P, P, P, I, I, I, P]
+    lib.fa_paged_fork.restype = I
+    lib.fa_paged_free.argtypes = [P, P, L, I, P, I, P, P, P, I, I, I, P]
+    lib.fa_paged_free.restype = I
+    lib.fa_paged_compact.argtypes = [P, P, L, I, P, P, P, I, P, I, I, I, P]
+    lib.fa_paged_compact.restype = I
+    lib.fa_paged_copy.argtypes = [P, P, L, P, P, P, I, I, I, I, I, P]
+    lib.fa_paged_copy.restype = I
+    lib.fa_rope.argtypes = [P, P, L, L, L, L, L, L, P, L, L, I, P, P, I, I, I, I, I, I, I, I, P]
+    lib.fa_rope.restype = I
+    lib.fa_rope_append.argtypes = [P, P, P, L, L, L, P, L, P, P, L, P, P, L, I, P, P, I, I, I, I, I,
+                                   I, I, I, P]
+    lib.fa_rope_append.restype = I
     _lib = lib
     return lib
 
@@ -626,9 +647,10 @@ def _on_stream(stream, fn, *args, **kw):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     if stream != torch.cuda.current_stream():
-        for t in (*args, *kw.values()):
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
+        for x in (*args, *kw.values()):
+            for t in x if isinstance(x, tuple) else (x,):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
     with torch.cuda.stream(stream):
         return fn(*args, **kw)
 
@@ -757,6 +779,339 @@ def decode_paged(q, k, v, block_table, cache_len, scale=None, workspace=None, st
         workspace = alloc_decode_paged_workspace(*q.shape[:2], k.shape[1], q.shape[2], q.device)
     fa_decode_paged(q, k, v, block_table, cache_len, o, lse, workspace, scale)
     return o, lse
+
+
+# ----------------------------------------------------------- shared prefixes
+
+def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load().fa_decode_shared_workspace_bytes(B, Hq, Hkv, d))
+
+
+def alloc_decode_shared_workspace(B: int, Hq: int, Hkv: int, d: int, device="cuda"):
+    n = fa_decode_shared_workspace_bytes(B, Hq, Hkv, d)
+    if n == 0:
+        raise FaError(FA_ERR_INVALID_ARG, "fa_decode_shared_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fa_decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, o, lse, workspace,
+                     scale=None, stream=None) -> None:
+    """fa_decode_paged for groups of sequences with a prefix in common: group p are the sequences
+    group_start[p] .. group_start[p + 1] - 1 (int32 [groups + 1]), whose first shared_len[p] tokens
+    (int32 [groups]) are in the same pages."""
+    heads, pool = q.shape, k.shape
+    if len(heads) != 3 or len(pool) != 4 or pool[3] != heads[2]:
+        raise ValueError("q must be [B, Hq, d] and k [num_pages, Hkv, page_size, d]; got "
+                         f"{list(heads)} and {list(pool)}")
+    B, Hq, d = heads
+    P, Hkv, page, _ = pool
+    groups = shared_len.numel()
+    _shaped("q", q, heads, torch.bfloat16)
+    kp = _rows("k", k, pool)
+    if kp != _rows("v", v, pool):
+        raise ValueError("k and v must have the same stride between pages")
+    stride = _table(block_table, B)
+    _shaped("cache_len", cache_len, (B,), torch.int32)
+    _shaped("shared_len", shared_len, (groups,), torch.int32)
+    _shaped("group_start", group_start, (groups + 1,), torch.int32)
+    _shaped("o", o, heads, torch.bfloat16)
+    _shaped("lse", lse, (B, Hq), torch.float32)
+    _scratch(workspace)
+    handle = _same_gpu(stream, q, k, v, block_table, cache_len, group_start, shared_len, o, lse,
+                       workspace)
+    st = load().fa_decode_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), kp,
+                                 block_table.data_ptr(), stride, block_table.shape[1],
+                                 cache_len.data_ptr(), group_start.data_ptr(),
+                                 shared_len.data_ptr(), groups, o.data_ptr(), lse.data_ptr(), B,
+                                 Hq, Hkv, P, page, d, 1.0 / d ** 0.5 if scale is None else scale,
+                                 workspace.data_ptr(), workspace.nbytes, handle)
+    if st != FA_OK:
+        raise FaError(st, "fa_decode_shared")
+
+
+def decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, scale=None,
+                  workspace=None, stream=None):
+    """Allocate o, lse (and the workspace unless given) and run fa_decode_shared."""
+    if stream is not None:
+        return _on_stream(stream, decode_shared, q, k, v, block_table, cache_len, group_start,
+                          shared_len, scale, workspace)
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = alloc_decode_shared_workspace(*q.shape[:2], k.shape[1], q.shape[2], q.device)
+    fa_decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, o, lse, workspace,
+                     scale)
+    return o, lse
+
+
+# ----------------------------------------------------------- pages
+
+def fa_paged_fork(cache_len, block_table, free_pages, src, dst, copy_src, copy_dst, copy_rows,
+                  pages_taken, page_size: int, num_pages: int, stream=None) -> None:
+    """Requests dst[i] become copies of src[i] (int32 tensors throughout): cache_len [B] and
+    block_table [B, max_pages] in and out, free_pages [F] in; out: what fa_paged_copy is to copy,
+    copy_src, copy_dst, copy_rows [n], and pages_taken [1]."""
+    B, i32 = cache_len.numel(), torch.int32
+    F, n = free_pages.numel(), src.numel()
+    _shaped("cache_len", cache_len, (B,), i32)
+    _shaped("free_pages", free_pages, (F,), i32)
+    for name, t in (("src", src), ("dst", dst), ("copy_src", copy_src), ("copy_dst", copy_dst),
+                    ("copy_rows", copy_rows)):
+        _shaped(name, t, (n,), i32)
+    _shaped("pages_taken", pages_taken, (1,), i32)
+    stride = _table(block_table, B)
+    handle = _same_gpu(stream, cache_len, block_table, free_pages, src, dst, copy_src, copy_dst,
+                       copy_rows, pages_taken)
+    st = load().fa_paged_fork(cache_len.data_ptr(), block_table.data_ptr(), stride,
+                              block_table.shape[1], free_pages.data_ptr(), F, src.data_ptr(),
+                              dst.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
+                              copy_rows.data_ptr(), pages_taken.data_ptr(), B, page_size,
+                              num_pages, handle)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_fork")
+
+
+def paged_fork(cache_len, block_table, free_pages, src, dst, page_size: int, num_pages: int,
+               stream=None):
+    """Allocate the lists and run fa_paged_fork; cache_len and block_table are updated in place.
+    Returns (copy_src, copy_dst, copy_rows, pages_taken)."""
+    if stream is not None:
+        return _on_stream(stream, paged_fork, cache_len, block_table, free_pages, src, dst,
+                          page_size, num_pages)
+    n = src.numel()
+    buf = torch.empty(3 * n + 1, dtype=torch.int32, device=cache_len.device)
+    frm, to, rows, taken = buf.split((n, n, n, 1))
+    fa_paged_fork(cache_len, block_table, free_pages, src, dst, frm, to, rows, taken, page_size,
+                  num_pages)
+    return frm, to, rows, taken
+
+
+def fa_paged_free(cache_len, block_table, rows, refs, free_pages, n_free, page_size: int,
+                  num_pages: int, stream=None) -> None:
+    """Requests rows [n] end (int32 tensors throughout): cache_len [B] and block_table
+    [B, max_pages] in and out; out: refs and free_pages [num_pages], n_free [1]."""
+    B, n, i32 = cache_len.numel(), rows.numel(), torch.int32
+    _shaped("cache_len", cache_len, (B,), i32)
+    _shaped("rows", rows, (n,), i32)
+    _shaped("refs", refs, (num_pages,), i32)
+    _shaped("free_pages", free_pages, (num_pages,), i32)
+    _shaped("n_free", n_free, (1,), i32)
+    stride = _table(block_table, B)
+    handle = _same_gpu(stream, cache_len, block_table, rows, refs, free_pages, n_free)
+    st = load().fa_paged_free(cache_len.data_ptr(), block_table.data_ptr(), stride,
+                              block_table.shape[1], rows.data_ptr(), n, refs.data_ptr(),
+                              free_pages.data_ptr(), n_free.data_ptr(), B, page_size, num_pages,
+                              handle)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_free")
+
+
+def paged_free(cache_len, block_table, rows, page_size: int, num_pages: int, stream=None):
+    """Allocate the outputs and run fa_paged_free; cache_len and block_table are updated in place.
+    Returns (refs, free_pages, n_free)."""
+    if stream is not None:
+        return _on_stream(stream, paged_free, cache_len, block_table, rows, page_size, num_pages)
+    buf = torch.empty(2 * num_pages + 1, dtype=torch.int32, device=cache_len.device)
+    refs, free, count = buf.split((num_pages, num_pages, 1))
+    fa_paged_free(cache_len, block_table, rows, refs, free, count, page_size, num_pages)
+    return refs, free, count
+
+
+def fa_paged_compact(cache_len, block_table, moved, copy_src, copy_dst, n_used, page_size: int,
+                     num_pages: int, stream=None) -> None:
+    """The pages in use move to the front of the pool (int32 tensors throughout): cache_len [B] in,
+    block_table [B, max_pages] in and out; out: moved [num_pages], copy_src and copy_dst (at least
+    num_pages / 2 each), n_used [1]."""
+    B, n, i32 = cache_len.numel(), copy_src.numel(), torch.int32
+    _shaped("cache_len", cache_len, (B,), i32)
+    _shaped("moved", moved, (num_pages,), i32)
+    _shaped("copy_src", copy_src, (n,), i32)
+    _shaped("copy_dst", copy_dst, (n,), i32)
+    _shaped("n_used", n_used, (1,), i32)
+    stride = _table(block_table, B)
+    handle = _same_gpu(stream, cache_len, block_table, moved, copy_src, copy_dst, n_used)
+    st = load().fa_paged_compact(cache_len.data_ptr(), block_table.data_ptr(), stride,
+                                 block_table.shape[1], moved.data_ptr(), copy_src.data_ptr(),
+                                 copy_dst.data_ptr(), n, n_used.data_ptr(), B, page_size,
+                                 num_pages, handle)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_compact")
+
+
+def paged_compact(cache_len, block_table, page_size: int, num_pages: int, stream=None):
+    """Allocate the outputs and run fa_paged_compact; block_table is updated in place.
+    Returns (moved, copy_src, copy_dst, n_used), the copies for paged_copy."""
+    if stream is not None:
+        return _on_stream(stream, paged_compact, cache_len, block_table, page_size, num_pages)
+    n = max(1, num_pages // 2)
+    buf = torch.empty(num_pages + 2 * n + 1, dtype=torch.int32, device=cache_len.device)
+    moved, frm, to, used = buf.split((num_pages, n, n, 1))
+    fa_paged_compact(cache_len, block_table, moved, frm, to, used, page_size, num_pages)
+    return moved, frm, to, used
+
+
+def fa_paged_copy(k_cache, v_cache, copy_src, copy_dst, copy_rows=None, stream=None) -> None:
+    """Pages copy_src[i] to copy_dst[i] (int32 [n]), or their first copy_rows[i] rows, in the bf16
+    pools k_cache, v_cache [num_pages, Hkv, page_size, d] (v_cache may be None) or in a latent one
+    [num_pages, page_size, 576]."""
+    pool, n = k_cache.shape, copy_src.numel()
+    if len(pool) == 3:
+        stride, heads = _latent_pool(k_cache), 1
+    elif len(pool) == 4:
+        stride, heads = _rows("k_cache", k_cache, pool), pool[1]
+    else:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] or a latent cache, not "
+                         f"{list(pool)}")
+    if v_cache is not None and _rows("v_cache", v_cache, pool) != stride:
+        raise ValueError("k_cache and v_cache must have the same stride between pages")
+    _shaped("copy_src", copy_src, (n,), torch.int32)
+    _shaped("copy_dst", copy_dst, (n,), torch.int32)
+    if copy_rows is not None:
+        _shaped("copy_rows", copy_rows, (n,), torch.int32)
+    handle = _same_gpu(stream, *_given(k_cache, v_cache, copy_src, copy_dst, copy_rows))
+    st = load().fa_paged_copy(k_cache.data_ptr(), _at(v_cache), stride, copy_src.data_ptr(),
+                              copy_dst.data_ptr(), _at(copy_rows), n, pool[0], heads, pool[-2],
+                              pool[-1], handle)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_copy")
+
+
+def paged_copy(k_cache, v_cache, copy_src, copy_dst, copy_rows=None, stream=None) -> None:
+    """fa_paged_copy; on a ``stream`` that is named, the tensors' memory is kept until its work is
+    done."""
+    if stream is not None:
+        return _on_stream(stream, paged_copy, k_cache, v_cache, copy_src, copy_dst, copy_rows)
+    fa_paged_copy(k_cache, v_cache, copy_src, copy_dst, copy_rows)
+
+
+# ----------------------------------------------------------- rotary positions
+
+def rope_table(rot: int, base: float = 10000.0, sections=None, frequencies=None, device="cuda"):
+    """The plan of a rotation of ``rot`` channels: (turns int64 [rot / 2], axis int32 [rot / 2]).
+
+    Pair i turns by base ** (-2 i / rot) radians a position, or by ``frequencies[i]``, on the axis
+    whose part of ``sections`` (pairs of each axis, in order; default: one axis) it lies in.
+    """
+    pairs = rot // 2
+    if frequencies is None:
+        frequencies = [float(base) ** (-2.0 * i / rot) for i in range(pairs)]
+    else:
+        frequencies = [float(f) for f in frequencies]
+    sections = [pairs] if sections is None else [int(n) for n in sections]
+    if rot % 2 or len(frequencies) != pairs or sum(sections) != pairs or min(sections) < 0:
+        raise ValueError(f"{pairs} pairs: as many frequencies, and sections that add up to them")
+    turns = []
+    for f in frequencies:
+        t = f / (2.0 * math.pi)
+        if not math.isfinite(t):
+            raise ValueError("frequencies must be finite")
+        u = round((t - math.floor(t)) * 2.0 ** 64) % 2 ** 64       # modulo a full turn
+        turns.append(u - 2 ** 64 if u >= 2 ** 63 else u)
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    return (torch.tensor(turns, dtype=torch.int64, device=device),
+            torch.tensor(axis, dtype=torch.int32, device=device))
+
+
+def _plan(table):
+    turns, axis = table
+    pairs = turns.numel()
+    _shaped("turns", turns, (pairs,), torch.int64)
+    _shaped("axis", axis, (pairs,), torch.int32)
+    return turns, axis, 2 * pairs
+
+
+def fa_rope(x, y, pos, table, interleaved: bool = False, inverse: bool = False,
+            stream=None) -> None:
+    """Rows of x [B, H, N, d] (bf16 or fp32; any strides, rows dense) turned into y by their
+    positions pos int32 [axes, B, N]; ``table`` as of rope_table.  y may be x."""
+    shape = x.shape
+    if len(shape) != 4:
+        raise ValueError(f"x must be [B, H, N, d], not {list(shape)}")
+    B, H, N, d = shape
+    code = _dtype_code(x)
+    if y.shape != shape or y.dtype != x.dtype:
+        raise ValueError(f"y must be {list(shape)} of {x.dtype}, as x is")
+    xs, ys, ps = x.stride(), y.stride(), pos.stride()
+    if d > 1 and (xs[3] != 1 or ys[3] != 1):
+        raise ValueError("rows of x and y must be dense")
+    if pos.dtype is not torch.int32:
+        raise TypeError("pos must be torch.int32")
+    if pos.dim() != 3 or pos.shape[1:] != (B, N) or (N > 1 and ps[2] != 1):
+        raise ValueError(f"pos must be [axes, {B}, {N}], dense along the last, not "
+                         f"{list(pos.shape)}")
+    turns, axis, rot = _plan(table)
+    handle = _same_gpu(stream, x, y, pos, turns, axis)
+    st = load().fa_rope(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2],
+                        pos.data_ptr(), ps[0], ps[1], pos.shape[0], turns.data_ptr(),
+                        axis.data_ptr(), B, H, N, d, rot, int(interleaved), int(inverse), code,
+                        handle)
+    if st != FA_OK:
+        raise FaError(st, "fa_rope")
+
+
+def rope(x, pos, table, interleaved: bool = False, out=None, stream=None):
+    """Rotary positions: x [B, H, N, d] turned, into ``out`` (which may be x) or a new tensor."""
+    if stream is not None:
+        return _on_stream(stream, rope, x, pos, table, interleaved, out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    fa_rope(x, out, pos, table, interleaved)
+    return out
+
+
+def rope_backward(dy, pos, table, interleaved: bool = False, out=None, stream=None):
+    """The gradient of rope: dy turned back, into ``out`` (which may be dy) or a new tensor."""
+    if stream is not None:
+        return _on_stream(stream, rope_backward, dy, pos, table, interleaved, out)
+    if out is None:
+        out = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    fa_rope(dy, out, pos, table, interleaved, True)
+    return out
+
+
+def fa_rope_append(q, k, v, pos, table, q_out, k_cache, v_cache, slots, interleaved: bool = False,
+                   stream=None) -> None:
+    """The rows of T new tokens: q [T, Hq, d] turned into q_out (which may be q), k [T, Hkv, d] turned
+    and v as it is into slots [T] (int32) of the pools k_cache, v_cache [num_pages, Hkv, page_size,
+    d]; bf16, any stride between tokens; positions pos int32 [axes, T], ``table`` as of
+    rope_table."""
+    rows, heads, pool = k.shape, q.shape, k_cache.shape
+    if (len(rows) != 3 or len(heads) != 3 or len(pool) != 4 or pool[1] != rows[1]
+            or pool[3] != rows[2] or heads[0] != rows[0] or heads[2] != rows[2]):
+        raise ValueError("q must be [T, Hq, d], k [T, Hkv, d] and k_cache [num_pages, Hkv, "
+                         f"page_size, d]; got {list(heads)}, {list(rows)} and {list(pool)}")
+    T, Hkv, d = rows
+    qs, ks, vs = _rows("q", q, heads), _rows("k", k, rows), _rows("v", v, rows)
+    qo, kp = _rows("q_out", q_out, heads), _rows("k_cache", k_cache, pool)
+    if kp != _rows("v_cache", v_cache, pool):
+        raise ValueError("k_cache and v_cache must have the same stride between pages")
+    _shaped("slots", slots, (T,), torch.int32)
+    if pos.dtype is not torch.int32:
+        raise TypeError("pos must be torch.int32")
+    if pos.dim() != 2 or pos.shape[1] != T or (T > 1 and pos.stride(1) != 1):
+        raise ValueError(f"pos must be [axes, {T}], dense along the last, not {list(pos.shape)}")
+    turns, axis, rot = _plan(table)
+    handle = _same_gpu(stream, q, k, v, pos, turns, axis, q_out, k_cache, v_cache, slots)
+    st = load().fa_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                               q_out.data_ptr(), qo, k_cache.data_ptr(), v_cache.data_ptr(), kp,
+                               slots.data_ptr(), pos.data_ptr(), pos.stride(0), pos.shape[0],
+                               turns.data_ptr(), axis.data_ptr(), T, heads[1], Hkv, pool[0],
+                               pool[2], d, rot, int(interleaved), handle)
+    if st != FA_OK:
+        raise FaError(st, "fa_rope_append")
+
+
+def rope_append(q, k, v, pos, table, k_cache, v_cache, slots, interleaved: bool = False, out=None,
+                stream=None):
+    """Run fa_rope_append; returns the turned queries, in ``out`` (which may be q) or a new
+    tensor."""
+    if stream is not None:
+        return _on_stream(stream, rope_append, q, k, v, pos, table, k_cache, v_cache, slots,
+                          interleaved, out)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fa_rope_append(q, k, v, pos, table, out, k_cache, v_cache, slots, interleaved)
+    return out
 
 
 # ----------------------------------------------------------- latent attention

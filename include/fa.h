@@ -334,7 +334,8 @@ fa_status fa_grad_finish(void* out, const float* acc, long long n, fa_dtype dtyp
  * Lengths are clamped to [0, max_pages * page_size] on the device.  The pages of different
  * sequences may be the same (a shared prefix) for reading.
  * In the entry points from here to fa_latent_decode, appends excepted, FA_ERR_INVALID_ARG if an
- * output (the workspace is one) shares memory with an input or with another output.
+ * output (the workspace is one) shares memory with an input or with another output (what an entry
+ * point says of tensors that may share memory goes before this).
  */
 
 /*
@@ -397,6 +398,131 @@ fa_status fa_decode_paged(const void* q, const void* k, const void* v, long long
                           const int32_t* cache_len, void* o, float* lse, int B, int Hq, int Hkv,
                           int num_pages, int page_size, int d, float scale, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention for groups of sequences that share a prefix: fa_decode_paged with the shared
+ * keys and values read once a group.
+ *   q, k, v, block_table, cache_len, o, lse, workspace: as fa_decode_paged; cache_len counts all of
+ *                 a sequence's tokens, the shared ones too, and the table names all their pages.
+ *                 workspace: fa_decode_shared_workspace_bytes(B, Hq, Hkv, d) bytes.
+ *   group_start in: int32 [groups + 1], ascending from 0 to B: group p are the sequences
+ *                 group_start[p] .. group_start[p + 1] - 1.  Sequences in no group share nothing.
+ *   shared_len  in: int32 [groups], tokens at the beginning that all sequences of the group have in
+ *                 the same pages (fa_paged_fork makes such tables); any length, clamped to what a
+ *                 table row holds, 0 for none.  The tables of the group's sequences must name the
+ *                 same pages up to there; they are read from the first one that is long enough.
+ * A sequence shorter than its group's shared tokens (an empty one that pads the batch, say) is
+ * computed from its own length and table.  groups is 1 .. B (FA_ERR_INVALID_ARG otherwise); starts
+ * that are not ascending give no defined result, and touch no other memory.  The result is that of
+ * fa_decode_paged but for the order of sums.  Two kernels run on `stream`; no atomics: the same call
+ * gives the same bits.
+ */
+size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d);
+fa_status fa_decode_shared(const void* q, const void* k, const void* v, long long page_stride,
+                           const int32_t* block_table, long long table_stride, int max_pages,
+                           const int32_t* cache_len, const int32_t* group_start,
+                           const int32_t* shared_len, int groups, void* o, float* lse, int B,
+                           int Hq, int Hkv, int num_pages, int page_size, int d, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The pages of a paged cache.  Nothing is kept beside the block tables and lengths: which pages are
+ * in use, and how often, is counted from them at every call (a request's live entries are the first
+ * ceil(cache_len / page_size) of its row; entries outside the pool are holes and stay what they
+ * are).  The tables may serve any number of pools (one a layer): what is to be copied in each comes
+ * out as a list for fa_paged_copy.  B <= 8192 and B * max_pages * page_size < 2^31
+ * (FA_ERR_UNSUPPORTED otherwise).
+ *
+ * fa_paged_fork: row dst[i] becomes a request with the tokens of row src[i], for i < n <= 8192.
+ *   cache_len   in/out: int32 [B];  block_table in/out: the full pages' entries are taken over, so
+ *                 that both requests use the page; the entry of a page that is filled in part is a
+ *                 page off the free list, -1 when that has run out; those behind stay as they are.
+ *   free_pages  in : int32 [n_free], taken from the front in the order of the pairs.
+ *   src, dst    in : int32 [n].  A pair with an index outside [0, B), whose dst an earlier pair
+ *                 names, or whose src is some pair's dst, is skipped (so -1 pads).  What a dst row
+ *                 held is not freed; its entries are overwritten.
+ *   copy_src, copy_dst, copy_rows out: int32 [n]: the part-filled page of pair i, the page for its
+ *                 copy and the rows in it; -1, -1, 0 where nothing is to be copied.
+ *   pages_taken out: int32 [1], pages the call needs; more than n_free: the list was too short.
+ *
+ * fa_paged_free: the requests rows[0 .. n) end: their lengths become 0 and all entries of their rows
+ *   -1.  n = 0 only counts.  rows outside [0, B) are skipped; a row may be named twice.
+ *   refs        out: int32 [num_pages], how many live entries name each page.
+ *   free_pages  out: int32 [num_pages], the pages with none, ascending, then -1;  n_free out: int32
+ *                 [1], how many they are.
+ *
+ * fa_paged_compact: with U pages in use, those numbered U or more move to the free ones below U, both
+ *   taken in ascending order, and the live entries follow; pages below U stay.
+ *   moved       out: int32 [num_pages], the new number of each page in use, -1 of the others.
+ *   copy_src, copy_dst out: int32 [n_copies], n_copies >= num_pages / 2: the moves, then -1.  No page
+ *                 is in both.
+ *   n_used      out: int32 [1], U.
+ *
+ * fa_paged_copy: page copy_dst[i] of the pools becomes page copy_src[i], for i < n; of every head the
+ *   first copy_rows[i] rows, clamped to [0, page_size] (NULL: all).  Pairs with a page outside the
+ *   pool, or both the same, are skipped.  No page may be a destination twice, or a source and a
+ *   destination: pieces are copied in no particular order.  k_cache, v_cache: bf16 pools
+ *   [num_pages, Hkv, page_size, d] as in fa_paged_append, v_cache may be NULL; d = 64, 128, or 576
+ *   for a latent cache (Hkv = 1).  n = 0 does nothing.
+ */
+fa_status fa_paged_fork(int32_t* cache_len, int32_t* block_table, long long table_stride,
+                        int max_pages, const int32_t* free_pages, int n_free, const int32_t* src,
+                        const int32_t* dst, int n, int32_t* copy_src, int32_t* copy_dst,
+                        int32_t* copy_rows, int32_t* pages_taken, int B, int page_size,
+                        int num_pages, void* stream);
+fa_status fa_paged_free(int32_t* cache_len, int32_t* block_table, long long table_stride,
+                        int max_pages, const int32_t* rows, int n, int32_t* refs,
+                        int32_t* free_pages, int32_t* n_free, int B, int page_size, int num_pages,
+                        void* stream);
+fa_status fa_paged_compact(const int32_t* cache_len, int32_t* block_table, long long table_stride,
+                           int max_pages, int32_t* moved, int32_t* copy_src, int32_t* copy_dst,
+                           int n_copies, int32_t* n_used, int B, int page_size, int num_pages,
+                           void* stream);
+fa_status fa_paged_copy(void* k_cache, void* v_cache, long long page_stride,
+                        const int32_t* copy_src, const int32_t* copy_dst, const int32_t* copy_rows,
+                        int n, int num_pages, int Hkv, int page_size, int d, void* stream);
+
+/*
+ * Rotary positions.  The first `rot` of a row's d channels are rot / 2 pairs; pair i is turned by
+ * the angle n w_i, n being the token's position on axis axis[i] (text has one axis; images and video
+ * have time, height and width):
+ *   y_1 = x_1 cos - x_2 sin,  y_2 = x_2 cos + x_1 sin.
+ * Channels behind `rot` are copied.  The gradient of the turn is the turn back.
+ *   x, y        [B, H, N, d] of `dtype`, rows of d dense, batches, heads and tokens any strides apart
+ *               (elements; multiples of 16 bytes).  y may be x, with the same strides; otherwise they
+ *               share no memory.  In y every element has a place of its own, and each stride is at
+ *               least what the smaller ones reach.
+ *   pos         in : int32, position of token (b, n) on axis a at a * pos_axis + b * pos_batch + n;
+ *                 any value, negative ones too.
+ *   turns       in : int64 [rot / 2], w_i / (2 pi), turns a position, in units of 2^-64 (modulo one
+ *                 turn).  The angle is exact in them, however far the position is.
+ *   axis        in : int32 [rot / 2], clamped to [0, axes).
+ *   interleaved : 0: pair i is channels i and i + rot / 2;  nonzero: channels 2 i and 2 i + 1.
+ *   inverse     : nonzero: the angles' signs change (the gradient).
+ * d a multiple of 8 up to 1024, rot a multiple of 16 in 16 .. d (FA_ERR_UNSUPPORTED otherwise).
+ *
+ * fa_rope_append: the rows of T new tokens, in one pass: queries turned into q_out, keys turned into
+ *   their slots of the cache, values into theirs.
+ *   q, q_out    [T, Hq, d], k, v [T, Hkv, d], bf16, tokens any strides apart (multiples of 8, at
+ *               least a row): slices of one projection are taken as they are.  q_out may be q.  Beyond
+ *               that q_out shares no memory with q, k and v (rows of one buffer may lie between one
+ *               another), and the caches share none with anything.
+ *   pos         in : int32, position of token t on axis a at a * pos_axis + t.
+ *   k_cache, v_cache, page_stride, slots: as fa_paged_append.  Queries of tokens without a slot are
+ *               turned all the same.
+ * d = 64 or 128; T = 0 does nothing.
+ */
+fa_status fa_rope(const void* x, void* y, long long x_batch, long long x_head, long long x_token,
+                  long long y_batch, long long y_head, long long y_token, const int32_t* pos,
+                  long long pos_axis, long long pos_batch, int axes, const int64_t* turns,
+                  const int32_t* axis, int B, int H, int N, int d, int rot, int interleaved,
+                  int inverse, fa_dtype dtype, void* stream);
+fa_status fa_rope_append(const void* q, const void* k, const void* v, long long q_stride,
+                         long long k_stride, long long v_stride, void* q_out, long long qo_stride,
+                         void* k_cache, void* v_cache, long long page_stride, const int32_t* slots,
+                         const int32_t* pos, long long pos_axis, int axes, const int64_t* turns,
+                         const int32_t* axis, int T, int Hq, int Hkv, int num_pages, int page_size,
+                         int d, int rot, int interleaved, void* stream);
 
 /*
  * Latent attention: keys and values of all heads come from one latent vector a token (512 columns,
