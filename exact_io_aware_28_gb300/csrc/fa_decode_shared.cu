@@ -79,8 +79,10 @@ struct SharedArgs {
   int seqs;                    // sequences of a tile: 128 / G
   float* part;                 // of the prefixes
   long long entries;           // places in it
-  long long *tiles_g, *tiles_b;  // exclusive sums over groups and sequences, for the combine kernel
-  int32_t* group_of;
+  // For the combine kernel: exclusive sums over groups and sequences, the sequences' groups, the
+  // workers that have a range.
+  long long *tiles_g, *tiles_b;
+  int32_t *group_of, *workers;
 };
 
 __device__ __forceinline__ int cap_of(const PagedArgs& a) { return a.max_pages << a.page_shift; }
@@ -91,6 +93,7 @@ struct Group {
   int keys;                    // of them, those read once: whole boxes
   int supers;                  // pieces of up to 2 x seqs sequences
   int tiles;
+  int cost;                    // of a tile: 2 where pieces have rows for both tiles
   __device__ __forceinline__ Group(const SharedArgs& g, int p) {
     s0 = min(max(g.start[p], 0), g.a.B);
     s1 = max(s0, min(max(g.start[p + 1], 0), g.a.B));
@@ -100,10 +103,13 @@ struct Group {
     keys = len & ~(box - 1);
     supers = (s1 - s0 + 2 * g.seqs - 1) / (2 * g.seqs);
     tiles = sched::granules<kKeys>(keys);
+    cost = s1 - s0 > g.seqs ? 2 : 1;
   }
+  // Its tiles of all heads and pieces, and what they cost.
   __device__ __forceinline__ long long all(const SharedArgs& g) const {
     return static_cast<long long>(tiles) * g.a.Hkv * supers;
   }
+  __device__ __forceinline__ long long costs(const SharedArgs& g) const { return all(g) * cost; }
 };
 
 // The group of sequence b: the last whose first sequence is not behind it.
@@ -123,10 +129,16 @@ __device__ __forceinline__ int shared_of(const SharedArgs& g, const Group& p, in
 
 struct SharedStart {
   long long first, last;       // the worker's range of the line
-  long long total_g;           // tiles of the prefixes
+  long long total_g;           // cost of the prefixes' tiles
   int p, b, pb;                // group of the first prefix tile; sequence of the first own tile, its group
   long long before_p, before_b;
 };
+
+// Workers that have a range.  Every range holds the beginning of a tile: with tiles of cost 2 it is
+// two long at least.
+__device__ __forceinline__ int active_workers(long long total, bool heavy, int workers) {
+  return sched::active(heavy ? (total + 1) >> 1 : total, workers);
+}
 
 // As sched::find_start, for both parts of the line.
 __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch)[2],
@@ -143,7 +155,12 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
     return static_cast<long long>(sched::granules<kKeys>(L - shared_of(g, gr, b, L))) * g.a.Hkv;
   };
   long long sum[2] = {0, 0};
-  for (int p = p0; p < p1; ++p) sum[0] += Group(g, p).all(g);
+  bool heavy = false;
+  for (int p = p0; p < p1; ++p) {
+    const Group gr(g, p);
+    sum[0] += gr.costs(g);
+    heavy |= gr.tiles > 0 && gr.cost > 1;
+  }
   {
     int p = at0;
     for (int b = b0; b < b1; ++b) sum[1] += own_tiles(b, &p);
@@ -157,7 +174,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
       if (lane >= off) incl[i] += up;
     }
   if (lane == 31) scratch[warp][0] = incl[0], scratch[warp][1] = incl[1];
-  __syncthreads();
+  heavy = __syncthreads_or(heavy) != 0;
   long long before[2] = {incl[0] - sum[0], incl[1] - sum[1]}, total[2] = {0, 0};
   for (int i = 0; i < kThreads / 32; ++i)
 #pragma unroll
@@ -167,7 +184,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
       total[j] += v;
     }
   const long long all = total[0] + total[1];
-  const int W = sched::active(all, workers);
+  const int W = active_workers(all, heavy, workers);
   const long long first = w < W ? sched::range_start(all, w, W) : all;
   if (tid == 0) {
     out->first = first;
@@ -180,7 +197,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
   long long at = before[0];
   if (write || (first >= at && first < at + sum[0]))
     for (int p = p0; p < p1; ++p) {
-      const long long n = Group(g, p).all(g);
+      const long long n = Group(g, p).costs(g);
       if (write) g.tiles_g[p] = at;
       if (first >= at && first < at + n) out->p = p, out->before_p = at;
       at += n;
@@ -196,7 +213,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
       at += n;
     }
   }
-  if (write && tid == 0) g.tiles_g[g.groups] = total[0], g.tiles_b[B] = total[1];
+  if (write && tid == 0) g.tiles_g[g.groups] = total[0], g.tiles_b[B] = total[1], *g.workers = W;
   __syncthreads();
 }
 
@@ -219,9 +236,11 @@ struct PSegment {
 __device__ __forceinline__ long long first_entry(const SharedArgs& g, const Group& p, int head,
                                                  int piece) {
   const int G = g.a.Hq / g.a.Hkv;
-  return 2ll * p.s0 * g.a.Hq + 2ll * head * (p.s1 - p.s0) * G + 2ll * piece * g.seqs * G;
+  return static_cast<long long>(p.s0) * g.a.Hq + static_cast<long long>(head) * (p.s1 - p.s0) * G +
+         2ll * piece * g.seqs * G;
 }
 
+// A tile belongs to the worker in whose range its first unit of cost lies.
 struct PrefixWalk {
   const SharedArgs& g;
   int p, w;
@@ -229,65 +248,81 @@ struct PrefixWalk {
   __device__ __forceinline__ PrefixWalk(const SharedArgs& g_, const SharedStart& s, int w_)
       : g(g_), p(s.p), w(w_), at(s.first), last(min(s.last, s.total_g)), before(s.before_p) {}
   __device__ __forceinline__ bool next(PSegment& sg) {
-    if (at >= last) return false;
-    for (; p < g.groups; ++p) {
+    for (; p < g.groups && at < last; ++p) {
       const Group gr(g, p);
-      const long long all = gr.all(g);
+      const long long all = gr.costs(g);
       if (at < before + all) {
-        const int pair = static_cast<int>((at - before) / gr.tiles);
-        const long long pair_start = before + static_cast<long long>(pair) * gr.tiles;
-        const int piece = pair % gr.supers;
-        sg.p = p;
-        sg.head = pair / gr.supers;
-        sg.k0 = static_cast<int>(at - pair_start) * kKeys;
-        const int g1 = static_cast<int>(min(static_cast<long long>(gr.tiles), last - pair_start));
-        sg.k1 = min(g1 * kKeys, gr.keys);
-        sg.s0 = gr.s0 + piece * 2 * g.seqs;
-        sg.n = min(2 * g.seqs, gr.s1 - sg.s0);
-        sg.both = sg.n > g.seqs;
-        sg.entry = first_entry(g, gr, sg.head, piece) + 2ll * w * g.seqs * (g.a.Hq / g.a.Hkv);
-        at = pair_start + g1;
-        return true;
+        const int up = gr.cost - 1;            // cost is 1 or 2: a shift, rounded up
+        const long long tile = (at - before + up) >> up;
+        const long long end = min(gr.all(g), (last - before + up) >> up);
+        if (tile < end) {
+          const int pair = static_cast<int>(tile / gr.tiles);
+          const long long pair_tile = static_cast<long long>(pair) * gr.tiles;
+          const int piece = pair % gr.supers;
+          const int g0 = static_cast<int>(tile - pair_tile);
+          const int g1 = static_cast<int>(min(static_cast<long long>(gr.tiles), end - pair_tile));
+          sg.p = p;
+          sg.head = pair / gr.supers;
+          sg.k0 = g0 * kKeys;
+          sg.k1 = min(g1 * kKeys, gr.keys);
+          sg.s0 = gr.s0 + piece * 2 * g.seqs;
+          sg.n = min(2 * g.seqs, gr.s1 - sg.s0);
+          sg.both = sg.n > g.seqs;
+          sg.entry = first_entry(g, gr, sg.head, piece) + 2ll * w * g.seqs * (g.a.Hq / g.a.Hkv);
+          at = before + ((pair_tile + g1) << up);
+          return true;
+        }
       }
       before += all;
+      at = max(at, before);
     }
     return false;
   }
 };
 
+// A worker's own segments: its first one begins inside a pair, the others with one.
 struct OwnWalk {
   const SharedArgs& g;
-  int b, p, w;
-  long long at, last, before;
+  int b, p, w, head, g0;
+  long long left;              // tiles of the worker's range that are still to come
+  int L, from, n;              // of sequence b: length, first own token, tiles of a head
   __device__ __forceinline__ OwnWalk(const SharedArgs& g_, const SharedStart& s, int w_)
-      : g(g_), b(s.b), p(s.pb), w(w_), at(max(s.first - s.total_g, 0ll)), last(s.last - s.total_g),
-        before(s.before_b) {}
-  __device__ __forceinline__ bool next(Segment& sg) {
-    if (at >= last) return false;
-    for (; b < g.a.B; ++b) {
-      while (p + 1 < g.groups && g.start[p + 1] <= b) ++p;
-      const int L = sched::clamp_len(g.a.cache_len, b, cap_of(g.a));
-      const Group gr(g, p);
-      const int from = shared_of(g, gr, b, L);
-      const int n = sched::granules<kKeys>(L - from);
-      const long long all = static_cast<long long>(n) * g.a.Hkv;
-      if (at < before + all) {
-        sg.b = b;
-        sg.head = static_cast<int>((at - before) / n);
-        sg.len = L;
-        sg.pair_start = before + static_cast<long long>(sg.head) * n;
-        const int g0 = static_cast<int>(at - sg.pair_start);
-        const int g1 = static_cast<int>(min(static_cast<long long>(n), last - sg.pair_start));
-        sg.k0 = from + g0 * kKeys;
-        sg.k1 = min(from + g1 * kKeys, L);
-        sg.whole = from == 0 && g0 == 0 && g1 == n;
-        sg.slot = b * g.a.Hkv + sg.head + w;
-        at = sg.pair_start + g1;
-        return true;
-      }
-      before += all;
+      : g(g_), b(s.b), p(s.pb), w(w_), left(s.last - max(s.first, s.total_g)) {
+    if (left <= 0 || b >= g.a.B) {
+      left = 0;
+      return;
     }
-    return false;
+    sequence();
+    const long long x = max(s.first - s.total_g, 0ll) - s.before_b;
+    head = static_cast<int>(x / n);            // find_start has found the sequence that holds it
+    g0 = static_cast<int>(x - static_cast<long long>(head) * n);
+  }
+  __device__ __forceinline__ void sequence() {
+    while (p + 1 < g.groups && g.start[p + 1] <= b) ++p;
+    const Group gr(g, p);
+    L = sched::clamp_len(g.a.cache_len, b, cap_of(g.a));
+    from = shared_of(g, gr, b, L);
+    n = sched::granules<kKeys>(L - from);
+    head = 0;
+  }
+  __device__ __forceinline__ bool next(Segment& sg) {
+    if (left <= 0) return false;
+    while (head >= g.a.Hkv || n == 0) {
+      if (++b >= g.a.B) return false;
+      sequence();
+    }
+    const int g1 = static_cast<int>(min(static_cast<long long>(n), g0 + left));
+    sg.b = b;
+    sg.head = head;
+    sg.len = L;
+    sg.k0 = from + g0 * kKeys;
+    sg.k1 = min(from + g1 * kKeys, L);
+    sg.whole = from == 0 && g0 == 0 && g1 == n;
+    sg.slot = b * g.a.Hkv + head + w;
+    left -= g1 - g0;
+    g0 = 0;
+    ++head;
+    return true;
   }
 };
 
@@ -318,7 +353,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
     bool ok = true;
     int n = 0, ns = 0;
     while (ok && walk.next(sg)) {
-      if (keys) {
+      if (!keys) {   // the queries with the values, which are needed later than the first keys
         if (ns > 0) {
           ok = mbar_wait_warp(&bars->q_empty, (ns - 1) & 1, abort_flag, a.err, a.wait_ns);
           if (!ok) break;
@@ -575,52 +610,82 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
         }
       }
       if (!ok) break;
-      // ---- the segment's partial results
+      // ---- the segment's partial results; tiles with the same rows are joined first
+      float l[2][2];
+      bool any[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const bool any = sg.count(t) > 0;
-        if (any) {
+        any[t] = sg.count(t) > 0;
+        if (any[t] && ok) {
           ok = mbar_wait_warp(&bars->o_done[t], n_out[t] & 1, abort_flag, a.err, a.wait_ns);
-          if (!ok) break;
           ++n_out[t];
-          tc_fence_after();
         }
-        float lA = l_part[t][0], lB = l_part[t][1];
-        lA += __shfl_xor_sync(0xffffffffu, lA, 1);
-        lB += __shfl_xor_sync(0xffffffffu, lB, 1);
-        lA += __shfl_xor_sync(0xffffffffu, lA, 2);
-        lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l[t][i] = l_part[t][i];
+          l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 1);
+          l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 2);
+        }
+      }
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t == 1 && !sg.both) break;
         // Rows of the tile, and the place of its first; group starts that are not ascending may
         // lead past the end, where nothing is written.
         const int rows = (sg.both ? (t == 0 ? g.seqs : sg.n - g.seqs) : sg.n) * G;
-        const long long e0 = sg.entry + (t == 0 ? 0 : (sg.both ? g.seqs : sg.n) * G);
+        const long long e0 = sg.entry + t * g.seqs * G;
         const bool wA = rA < rows && e0 + rA < g.entries, wB = rB < rows && e0 + rB < g.entries;
         float* outA = g.part + (e0 + rA) * TC<D>::PSTRIDE;
         float* outB = g.part + (e0 + rB) * TC<D>::PSTRIDE;
-        if (any) {
+        const bool join = !sg.both && any[1];
+        float M[2], w[2][2];     // of rows A and B
 #pragma unroll
-          for (int half = 0; half < D / 64; ++half) {
-            uint32_t ov[32];
-            tmem_ld_16x256b_x8_wait(lane_base + 256 + t * 128 + 64 * half, ov);
-#pragma unroll
-            for (int cc = 0; cc < 8; ++cc) {
-              const int col = 64 * half + 8 * cc + 2 * t4;
-              if (wA)
-                *reinterpret_cast<float2*>(outA + col) =
-                    make_float2(__uint_as_float(ov[4 * cc]), __uint_as_float(ov[4 * cc + 1]));
-              if (wB)
-                *reinterpret_cast<float2*>(outB + col) =
-                    make_float2(__uint_as_float(ov[4 * cc + 2]), __uint_as_float(ov[4 * cc + 3]));
-            }
+        for (int i = 0; i < 2; ++i) {
+          M[i] = m_run[t][i];
+          w[0][i] = w[1][i] = 1.f;
+          if (join) {
+            M[i] = fmaxf(m_run[0][i], m_run[1][i]);
+            const float use = M[i] == -INFINITY ? 0.f : M[i];
+            w[0][i] = ex2(m_run[0][i] - use);      // -inf gives 0
+            w[1][i] = ex2(m_run[1][i] - use);
           }
-          tc_fence_before();
-          mbar_arrive(&bars->o_empty[t]);
+        }
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          uint32_t ov[32];
+          tmem_ld_16x256b_x8_wait(lane_base + 256 + t * 128 + 64 * half, ov);
+          if (join) {
+            uint32_t o1[32];
+            tmem_ld_16x256b_x8_wait(lane_base + 384 + 64 * half, o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              ov[i] = __float_as_uint(__uint_as_float(ov[i]) * w[0][(i >> 1) & 1] +
+                                      __uint_as_float(o1[i]) * w[1][(i >> 1) & 1]);
+          }
+#pragma unroll
+          for (int cc = 0; cc < 8; ++cc) {
+            const int col = 64 * half + 8 * cc + 2 * t4;
+            if (wA)
+              *reinterpret_cast<float2*>(outA + col) =
+                  make_float2(__uint_as_float(ov[4 * cc]), __uint_as_float(ov[4 * cc + 1]));
+            if (wB)
+              *reinterpret_cast<float2*>(outB + col) =
+                  make_float2(__uint_as_float(ov[4 * cc + 2]), __uint_as_float(ov[4 * cc + 3]));
+          }
         }
         if (t4 == 0) {
-          if (wA) *reinterpret_cast<float2*>(outA + D) = make_float2(m_run[t][0], lA);
-          if (wB) *reinterpret_cast<float2*>(outB + D) = make_float2(m_run[t][1], lB);
+          const float lA = join ? l[0][0] * w[0][0] + l[1][0] * w[1][0] : l[t][0];
+          const float lB = join ? l[0][1] * w[0][1] + l[1][1] * w[1][1] : l[t][1];
+          if (wA) *reinterpret_cast<float2*>(outA + D) = make_float2(M[0], lA);
+          if (wB) *reinterpret_cast<float2*>(outB + D) = make_float2(M[1], lB);
         }
       }
+      tc_fence_before();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (any[t]) mbar_arrive(&bars->o_empty[t]);
     }
   }
 }
@@ -700,93 +765,120 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
   }
 }
 
-// Joins a row's partial results; o = 0, lse = -inf for an empty sequence.  A warp per (sequence,
-// query head).
-template <int D>
+// Joins a row's partial results; o = 0, lse = -inf for an empty sequence.  W warps (1 or 4) per
+// (sequence, query head), each with every W-th part.
+template <int D, int W>
 __global__ void __launch_bounds__(256) decode_shared_combine_kernel(
-    const __grid_constant__ SharedArgs g, int workers) {
+    const __grid_constant__ SharedArgs g) {
   constexpr int PS = TC<D>::PSTRIDE, PER = D / 32;
+  __shared__ float red[8][D + 2];                // a warp's columns, maximum and sum
   griddep_wait();
   griddep_launch_dependents();
   const PagedArgs& a = g.a;
-  const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
-  const long long row = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(a.B) * a.Hq) return;
-  const int b = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
-  const int head = hq / G, h = hq % G, p = g.group_of[b];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % W, G = a.Hq / a.Hkv;
+  const long long row = blockIdx.x * static_cast<long long>(8 / W) + warp / W;
+  const bool live = row < static_cast<long long>(a.B) * a.Hq;
+  const int b = live ? static_cast<int>(row / a.Hq) : 0, hq = live ? static_cast<int>(row % a.Hq) : 0;
+  const int head = hq / G, h = hq % G, p = g.group_of[b], workers = *g.workers;
   const long long total_g = g.tiles_g[g.groups], total = total_g + g.tiles_b[a.B];
   const long long t0 = g.tiles_b[b], n = (g.tiles_b[b + 1] - t0) / a.Hkv;
   const Group gr(g, p);
   const int shared = shared_of(g, gr, b, sched::clamp_len(a.cache_len, b, cap_of(a)));
-  workers = sched::active(total, workers);
-  int w0 = 0, own = 0;                           // the continuation's parts
+  int own = 0, pre = 0, step = 0;                // parts of the continuation, of the prefix
+  const float *own0 = nullptr, *pre0 = nullptr;  // the first ones
   if (n > 0) {
     const long long first = total_g + t0 + head * n;
-    w0 = sched::owner(first, total, workers);
+    const int w0 = sched::owner(first, total, workers);
     own = sched::owner(first + n - 1, total, workers) - w0 + 1;
-    if (shared == 0 && own == 1) return;         // finished by its CTA
+    own0 = a.part + ((static_cast<long long>(b) * a.Hkv + head + w0) * G + h) * PS;
   }
-  int v0 = 0, pre = 0, step = 0;                 // the prefix's
-  long long e0 = 0, e1 = 0;
   if (shared > 0) {
     const int piece = (b - gr.s0) / (2 * g.seqs), s = (b - gr.s0) % (2 * g.seqs);
-    const int seqs = min(2 * g.seqs, gr.s1 - gr.s0 - piece * 2 * g.seqs);
     const long long first =
-        g.tiles_g[p] + (static_cast<long long>(head) * gr.supers + piece) * gr.tiles;
-    v0 = sched::owner(first, total, workers);
-    pre = sched::owner(first + gr.tiles - 1, total, workers) - v0 + 1;
-    e0 = first_entry(g, gr, head, piece) + s * G + h;
+        g.tiles_g[p] +
+        (static_cast<long long>(head) * gr.supers + piece) * gr.tiles * gr.cost;
+    const int w0 = sched::owner(first, total, workers);
+    pre = sched::owner(first + static_cast<long long>(gr.tiles - 1) * gr.cost, total, workers) - w0 + 1;
     step = 2 * g.seqs * G;
-    // Rows of one tile only: two results a worker, of the even and the odd key tiles.
-    if (seqs <= g.seqs) e1 = seqs * G;
+    const long long e = first_entry(g, gr, head, piece) + s * G + h + static_cast<long long>(w0) * step;
+    pre = static_cast<int>(min(static_cast<long long>(pre), (g.entries - 1 - e) / step + 1));
+    pre0 = g.part + e * PS;
   }
-  const int twice = e1 > 0 ? 1 : 0, parts = (pre << twice) + own;
-  auto at = [&](int i) -> const float* {
-    if (i < pre << twice) {
-      const long long e =
-          e0 + static_cast<long long>(v0 + (i >> twice)) * step + (i & twice) * e1;
-      return g.part + min(e, g.entries - 1) * PS;
-    }
-    return a.part + ((static_cast<long long>(b) * a.Hkv + head + w0 + i - (pre << twice)) * G + h) * PS;
+  // A continuation that is all of its rows' keys and one CTA's is finished; W > 1: the block goes on
+  // to its barrier.
+  const bool todo = live && !(shared == 0 && own == 1);
+  const int parts = todo ? pre + own : 0;
+  auto at = [&](int i) {
+    return i < pre ? pre0 + static_cast<long long>(i) * step * PS : own0 + (i - pre) * G * PS;
   };
   float acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
   float M = -INFINITY, lsum = 0.f;
-  for (int base = 0; base < parts; base += 32) {
-    const int mine = base + lane;
-    const float* q = at(mine < parts ? mine : base);
-    const float m = mine < parts ? q[D] : -INFINITY, l = mine < parts ? q[D + 1] : 0.f;
+  for (int base = sub; base < parts; base += 32 * W) {
+    const int mine = base + lane * W;
+    const float2 ml = *reinterpret_cast<const float2*>(at(mine < parts ? mine : base) + D);
+    const float m = mine < parts ? ml.x : -INFINITY, l = mine < parts ? ml.y : 0.f;
     const float mb = fmaxf(M, warp_max(m));
     const float use = mb == -INFINITY ? 0.f : mb;
     const float keep = ex2(M - use);             // M = -inf gives 0
-    const float wt = ex2(m - use);
+    const float wt = ex2(m - use);               // a part without a visible key weighs 0
     M = mb;
     lsum = lsum * keep + l * wt;                 // without a key l is 0, of a NaN query NaN
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] *= keep;
-    const uint32_t has = __ballot_sync(0xffffffffu, m != -INFINITY);   // a part without a key has no o
-    const int cnt = min(32, parts - base);
-#pragma unroll 4
-    for (int j = 0; j < cnt; ++j) {
-      if (!(has >> j & 1u)) continue;
-      const float wj = __shfl_sync(0xffffffffu, wt, j);
-      const float* pj = at(base + j) + lane * PER;
-      if constexpr (PER == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(pj);
-        acc[0] = fmaf(wj, v.x, acc[0]);
-        acc[1] = fmaf(wj, v.y, acc[1]);
-        acc[2] = fmaf(wj, v.z, acc[2]);
-        acc[3] = fmaf(wj, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(pj);
-        acc[0] = fmaf(wj, v.x, acc[0]);
-        acc[1] = fmaf(wj, v.y, acc[1]);
+    const int cnt = min(32, (parts - base + W - 1) / W);
+    // Eight parts' loads in flight; those past the last repeat it with weight 0.
+    for (int j0 = 0; j0 < cnt; j0 += 8) {
+      float v[8][PER];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float* pj = at(base + min(j0 + j, cnt - 1) * W) + lane * PER;
+        if constexpr (PER == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(pj);
+          v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(pj);
+          v[j][0] = x.x, v[j][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
+        if (j0 + j >= cnt) break;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = fmaf(wj, v[j][i], acc[i]);
       }
     }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) red[warp][lane * PER + i] = acc[i];
+    if (lane == 0) {
+      red[warp][D] = M;
+      red[warp][D + 1] = lsum;
+    }
+    __syncthreads();
+    if (sub > 0) return;
+    float mw[W];
+    M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) M = fmaxf(M, mw[w] = red[warp + w][D]);
+    const float use = M == -INFINITY ? 0.f : M;
+    lsum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float wt = ex2(mw[w] - use);
+      lsum += red[warp + w][D + 1] * wt;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = fmaf(red[warp + w][lane * PER + i], wt, acc[i]);
+    }
+  }
+  if (!todo) return;
   const float inv = lsum == 0.f ? 0.f : 1.f / lsum;   // a NaN sum stays one
   __nv_bfloat16* orow = a.o + static_cast<size_t>(row) * D + lane * PER;
 #pragma unroll
@@ -807,12 +899,22 @@ cudaError_t launch_g(const CUtensorMap& mk, const CUtensorMap& mv, const CUtenso
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
-  cudaError_t e = launch_dependent(decode_shared_kernel<D, GP>, dim3(workers), dim3(kThreads),
-                                   TC<D>::SMEM, s, mk, mv, mq, mr, g);
+  // An ordinary launch: placed on the SMs while the kernel before still runs, some CTAs took nearly
+  // twice as long as the rest to their end (16 groups of 4 sequences, 2048 + 128 tokens: 66 us, 50 with
+  // the ordinary launch; the cause is not known).
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(workers);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = TC<D>::SMEM;
+  cfg.stream = s;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_shared_kernel<D, GP>, mk, mv, mq, mr, g);
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(g.a.B) * g.a.Hq;
-  return launch_dependent(decode_shared_combine_kernel<D>,
-                          dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, g, workers);
+  if (rows <= 4096)
+    return launch_dependent(decode_shared_combine_kernel<D, 4>,
+                            dim3(static_cast<unsigned>((rows + 1) / 2)), dim3(256), 0, s, g);
+  return launch_dependent(decode_shared_combine_kernel<D, 1>,
+                          dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, g);
 }
 
 template <int D>
@@ -834,10 +936,10 @@ cudaError_t launch_d(const void* q, const void* k, const void* v, long long page
   return launch_g<D, 1>(mk, mv, mq, mr, g, workers, s);
 }
 
-// Places for the prefixes' partial results: two a row (the even and the odd key tiles), and a
-// piece's rows for every worker that begins inside a pair.
+// Places for the prefixes' partial results: one a row, and a piece's rows for every worker that begins
+// inside a pair.
 long long prefix_entries(int B, int Hq, int G) {
-  return 2ll * B * Hq + 2ll * sm_count() * (kRows / G) * G;
+  return static_cast<long long>(B) * Hq + 2ll * sm_count() * (kRows / G) * G;
 }
 long long own_entries(int B, int Hkv, int G) {
   return (static_cast<long long>(B) * Hkv + sm_count()) * G;
@@ -850,7 +952,7 @@ size_t decode_shared_bytes(int B, int Hq, int Hkv, int d) {
   const size_t entry = (d + 4) * sizeof(float);
   return round_up(prefix_entries(B, Hq, G) * entry, 256) +
          round_up(own_entries(B, Hkv, G) * entry, 256) +
-         2 * (static_cast<size_t>(B) + 1) * sizeof(long long) + B * sizeof(int32_t);
+         2 * (static_cast<size_t>(B) + 1) * sizeof(long long) + (B + 1) * sizeof(int32_t);
 }
 
 cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
@@ -874,6 +976,7 @@ cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
   g.tiles_g = reinterpret_cast<long long*>(at);
   g.tiles_b = g.tiles_g + B + 1;
   g.group_of = reinterpret_cast<int32_t*>(g.tiles_b + B + 1);
+  g.workers = g.group_of + B;
   g.start = start;
   g.len = shared_len;
   g.groups = groups;
