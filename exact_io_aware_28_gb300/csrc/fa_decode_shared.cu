@@ -53,10 +53,13 @@ template <int D>
 struct PC {
   static constexpr int NSUB = D / 64;
   static constexpr int TILE = NSUB * kSub;
-  static constexpr int NST = D == 128 ? 2 : 4;   // stages of a K and a V tile each
-  static constexpr int SMEM = 2 * TILE + 2 * NST * TILE;
-  // The decode's barriers and statistics lie behind what the prefix phase uses.
-  static_assert(SMEM <= TC<D>::STAGES * TC<D>::STAGE, "shared memory");
+  // Stages of keys and of values (three and two of them at d = 128, with the barriers moved out of
+  // the tiles' way: 121 against 122 us for 256 sequences behind 32768 tokens, and 39 against 35 for
+  // continuations alone).
+  static constexpr int NK = D == 128 ? 2 : 4, NV = NK;
+  static constexpr int TILES = (2 + NK + NV) * TILE;
+  // The continuations' tiles take the same memory afterwards.
+  static_assert(TILES <= TC<D>::STAGES * TC<D>::STAGE, "the continuations' barriers lie behind");
 };
 constexpr int kSeen = 8;                         // row masks of the last key tiles
 
@@ -77,15 +80,79 @@ struct SharedArgs {
   const int32_t* len;          // [groups]
   int groups;
   int seqs;                    // sequences of a tile: 128 / G
-  float* part;                 // of the prefixes
-  long long entries;           // places in it
-  // For the combine kernel: exclusive sums over groups and sequences, the sequences' groups, the
-  // workers that have a range.
-  long long *tiles_g, *tiles_b;
-  int32_t *group_of, *workers;
+  // Of the prefixes: unnormalised o [entries][D], maximum and sum [entries].  Rows of whole sectors:
+  // the stores of a piece's 256 rows stall on any other.
+  float* part;
+  float2* stats;
+  long long entries;
+  struct Row* rows;            // [B], for the combine kernel
+  struct Line* line;
+  long long* tiles_g;          // [groups], costs before each group
+};
+
+// What the combine kernel needs to know of a sequence: where on the line its own tiles and its
+// piece's begin (head 0), and the places of its partial results.
+struct Row {
+  long long own, pre;
+  long long pre_head;          // from a head's tiles of the piece to the next head's
+  long long entry;             // place of the row of head 0 in the prefixes' results
+  int n;                       // own tiles of a head
+  int span;                    // from the piece's first tile to its last; -1: nothing shared
+  int entry_head;              // from one head's places to the next one's
+  int pad;
+};
+struct Line {
+  long long total;
+  int workers;                 // that have a range
 };
 
 __device__ __forceinline__ int cap_of(const PagedArgs& a) { return a.max_pages << a.page_shift; }
+
+// The arguments with the lists of lengths and groups: copies in shared memory where they fit (what
+// the tiles leave of it).
+constexpr int kListed = 160;
+struct Lists {
+  int32_t cache_len[kListed], len[kListed], start[kListed + 1];
+};
+struct Plan {
+  const SharedArgs& s;
+  const PagedArgs& a;
+  const int32_t *cache_len, *len, *start;
+  int groups, seqs;
+  // By all threads; before the block's barrier.
+  __device__ __forceinline__ Plan(const SharedArgs& g, Lists* lists)
+      : s(g), a(g.a), cache_len(g.a.cache_len), len(g.len), start(g.start), groups(g.groups),
+        seqs(g.seqs) {
+    if (a.B > kListed) return;                   // groups <= B
+    const int i = threadIdx.x;
+    if (i < a.B) lists->cache_len[i] = cache_len[i];
+    if (i < groups) lists->len[i] = len[i], lists->start[i] = start[i];
+    if (i == 0) lists->start[groups] = start[groups];
+    cache_len = lists->cache_len;
+    len = lists->len;
+    start = lists->start;
+  }
+};
+
+// x / n; 32 bits are enough but for huge batches.
+__device__ __forceinline__ int quotient(long long x, int n) {
+  if (x < (1ll << 31)) return static_cast<int>(x) / n;
+  return static_cast<int>(x / n);
+}
+
+// sched::range_start and sched::owner, by a division of 32 bits where that is enough (workers are SMs,
+// fewer than 512).
+__device__ __forceinline__ long long range_start(long long total, int w, int workers) {
+  if (total < (1 << 23)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(w) /
+                                  static_cast<uint32_t>(workers);
+  return sched::range_start(total, w, workers);
+}
+__device__ __forceinline__ int owner(long long x, long long total, int workers) {
+  if (total < (1 << 23))
+    return (static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(workers) - 1u) /
+           static_cast<uint32_t>(total);
+  return sched::owner(x, total, workers);
+}
 
 struct Group {
   int s0, s1;                  // its sequences
@@ -94,7 +161,7 @@ struct Group {
   int supers;                  // pieces of up to 2 x seqs sequences
   int tiles;
   int cost;                    // of a tile: 2 where pieces have rows for both tiles
-  __device__ __forceinline__ Group(const SharedArgs& g, int p) {
+  __device__ __forceinline__ Group(const Plan& g, int p) {
     s0 = min(max(g.start[p], 0), g.a.B);
     s1 = max(s0, min(max(g.start[p + 1], 0), g.a.B));
     const int box = min(kKeys, 1 << g.a.page_shift);
@@ -106,14 +173,14 @@ struct Group {
     cost = s1 - s0 > g.seqs ? 2 : 1;
   }
   // Its tiles of all heads and pieces, and what they cost.
-  __device__ __forceinline__ long long all(const SharedArgs& g) const {
+  __device__ __forceinline__ long long all(const Plan& g) const {
     return static_cast<long long>(tiles) * g.a.Hkv * supers;
   }
-  __device__ __forceinline__ long long costs(const SharedArgs& g) const { return all(g) * cost; }
+  __device__ __forceinline__ long long costs(const Plan& g) const { return all(g) * cost; }
 };
 
 // The group of sequence b: the last whose first sequence is not behind it.
-__device__ __forceinline__ int group_at(const SharedArgs& g, int b) {
+__device__ __forceinline__ int group_at(const Plan& g, int b) {
   int lo = 0, hi = g.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -123,7 +190,7 @@ __device__ __forceinline__ int group_at(const SharedArgs& g, int b) {
 }
 
 // Tokens of sequence b (length L) that it takes from its group.
-__device__ __forceinline__ int shared_of(const SharedArgs& g, const Group& p, int b, int L) {
+__device__ __forceinline__ int shared_of(const Plan& g, const Group& p, int b, int L) {
   return b >= p.s0 && b < p.s1 && L >= p.len ? p.keys : 0;
 }
 
@@ -140,19 +207,19 @@ __device__ __forceinline__ int active_workers(long long total, bool heavy, int w
   return sched::active(heavy ? (total + 1) >> 1 : total, workers);
 }
 
-// As sched::find_start, for both parts of the line.
+// As sched::find_start, for both parts of the line.  write: what the combine kernel reads.
 __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch)[2],
-                                           const SharedArgs& g, int w, int workers, bool write) {
+                                           const Plan& g, int w, int workers, bool write) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = g.a.B, cap = cap_of(g.a);
   const int per_p = (g.groups + kThreads - 1) / kThreads, per_b = (B + kThreads - 1) / kThreads;
   const int p0 = min(tid * per_p, g.groups), p1 = min(p0 + per_p, g.groups);
   const int b0 = min(tid * per_b, B), b1 = min(b0 + per_b, B);
   const int at0 = b0 < b1 ? group_at(g, b0) : 0;
-  auto own_tiles = [&](int b, int* p) {
+  auto own_tiles = [&](int b, int* p) {        // of a head
     while (*p + 1 < g.groups && g.start[*p + 1] <= b) ++*p;
-    const int L = sched::clamp_len(g.a.cache_len, b, cap);
+    const int L = sched::clamp_len(g.cache_len, b, cap);
     const Group gr(g, *p);
-    return static_cast<long long>(sched::granules<kKeys>(L - shared_of(g, gr, b, L))) * g.a.Hkv;
+    return sched::granules<kKeys>(L - shared_of(g, gr, b, L));
   };
   long long sum[2] = {0, 0};
   bool heavy = false;
@@ -163,7 +230,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
   }
   {
     int p = at0;
-    for (int b = b0; b < b1; ++b) sum[1] += own_tiles(b, &p);
+    for (int b = b0; b < b1; ++b) sum[1] += static_cast<long long>(own_tiles(b, &p)) * g.a.Hkv;
   }
   long long incl[2] = {sum[0], sum[1]};
 #pragma unroll
@@ -174,8 +241,13 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
       if (lane >= off) incl[i] += up;
     }
   if (lane == 31) scratch[warp][0] = incl[0], scratch[warp][1] = incl[1];
+  if (tid == 0) {
+    out->p = g.groups, out->b = B, out->pb = 0;
+    out->before_p = out->before_b = 0;
+  }
   heavy = __syncthreads_or(heavy) != 0;
   long long before[2] = {incl[0] - sum[0], incl[1] - sum[1]}, total[2] = {0, 0};
+#pragma unroll
   for (int i = 0; i < kThreads / 32; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -185,36 +257,58 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
     }
   const long long all = total[0] + total[1];
   const int W = active_workers(all, heavy, workers);
-  const long long first = w < W ? sched::range_start(all, w, W) : all;
+  const long long first = w < W ? range_start(all, w, W) : all;
   if (tid == 0) {
     out->first = first;
-    out->last = w < W ? sched::range_start(all, w + 1, W) : all;
+    out->last = w < W ? range_start(all, w + 1, W) : all;
     out->total_g = total[0];
-    out->p = g.groups, out->b = B, out->pb = 0;
-    out->before_p = out->before_b = 0;
   }
-  __syncthreads();
   long long at = before[0];
   if (write || (first >= at && first < at + sum[0]))
     for (int p = p0; p < p1; ++p) {
-      const long long n = Group(g, p).costs(g);
-      if (write) g.tiles_g[p] = at;
+      const long long n = p0 + 1 == p1 ? sum[0] : Group(g, p).costs(g);
+      if (write) g.s.tiles_g[p] = at;
       if (first >= at && first < at + n) out->p = p, out->before_p = at;
       at += n;
     }
   at = before[1];
   const long long own = first > total[0] ? first - total[0] : 0;
-  if (write || (own >= at && own < at + sum[1])) {
+  if (own >= at && own < at + sum[1]) {
     int p = at0;
     for (int b = b0; b < b1; ++b) {
-      const long long n = own_tiles(b, &p);
-      if (write) g.tiles_b[b] = at, g.group_of[b] = p;
+      const long long n = static_cast<long long>(own_tiles(b, &p)) * g.a.Hkv;
       if (own >= at && own < at + n) out->b = b, out->pb = p, out->before_b = at;
       at += n;
     }
   }
-  if (write && tid == 0) g.tiles_g[g.groups] = total[0], g.tiles_b[B] = total[1], *g.workers = W;
   __syncthreads();
+  if (write) {
+    if (tid == 0) *g.s.line = Line{all, W};
+    const int G = g.a.Hq / g.a.Hkv;
+    int p = at0;
+    at = total[0] + before[1];
+    for (int b = b0; b < b1; ++b) {
+      Row r;
+      r.n = own_tiles(b, &p);
+      r.own = at;
+      at += static_cast<long long>(r.n) * g.a.Hkv;
+      const Group gr(g, p);
+      const int L = sched::clamp_len(g.cache_len, b, cap);
+      r.span = -1;
+      r.pre = r.pre_head = r.entry = 0;
+      r.entry_head = r.pad = 0;
+      if (shared_of(g, gr, b, L) > 0) {
+        const int piece = (b - gr.s0) / (2 * g.seqs);
+        const long long tiles = static_cast<long long>(gr.tiles) * gr.cost;
+        r.span = (gr.tiles - 1) * gr.cost;
+        r.pre = g.s.tiles_g[p] + piece * tiles;
+        r.pre_head = gr.supers * tiles;
+        r.entry = static_cast<long long>(gr.s0) * g.a.Hq + static_cast<long long>(b - gr.s0) * G;
+        r.entry_head = (gr.s1 - gr.s0) * G;
+      }
+      g.s.rows[b] = r;
+    }
+  }
 }
 
 // One prefix segment: keys [k0, k1) of (group, head, piece).
@@ -233,7 +327,7 @@ struct PSegment {
 };
 
 // Places of a piece's rows before those of its pair's segments of other workers.
-__device__ __forceinline__ long long first_entry(const SharedArgs& g, const Group& p, int head,
+__device__ __forceinline__ long long first_entry(const Plan& g, const Group& p, int head,
                                                  int piece) {
   const int G = g.a.Hq / g.a.Hkv;
   return static_cast<long long>(p.s0) * g.a.Hq + static_cast<long long>(head) * (p.s1 - p.s0) * G +
@@ -242,10 +336,10 @@ __device__ __forceinline__ long long first_entry(const SharedArgs& g, const Grou
 
 // A tile belongs to the worker in whose range its first unit of cost lies.
 struct PrefixWalk {
-  const SharedArgs& g;
+  const Plan& g;
   int p, w;
   long long at, last, before;
-  __device__ __forceinline__ PrefixWalk(const SharedArgs& g_, const SharedStart& s, int w_)
+  __device__ __forceinline__ PrefixWalk(const Plan& g_, const SharedStart& s, int w_)
       : g(g_), p(s.p), w(w_), at(s.first), last(min(s.last, s.total_g)), before(s.before_p) {}
   __device__ __forceinline__ bool next(PSegment& sg) {
     for (; p < g.groups && at < last; ++p) {
@@ -256,7 +350,7 @@ struct PrefixWalk {
         const long long tile = (at - before + up) >> up;
         const long long end = min(gr.all(g), (last - before + up) >> up);
         if (tile < end) {
-          const int pair = static_cast<int>(tile / gr.tiles);
+          const int pair = quotient(tile, gr.tiles);
           const long long pair_tile = static_cast<long long>(pair) * gr.tiles;
           const int piece = pair % gr.supers;
           const int g0 = static_cast<int>(tile - pair_tile);
@@ -282,11 +376,11 @@ struct PrefixWalk {
 
 // A worker's own segments: its first one begins inside a pair, the others with one.
 struct OwnWalk {
-  const SharedArgs& g;
+  const Plan& g;
   int b, p, w, head, g0;
   long long left;              // tiles of the worker's range that are still to come
   int L, from, n;              // of sequence b: length, first own token, tiles of a head
-  __device__ __forceinline__ OwnWalk(const SharedArgs& g_, const SharedStart& s, int w_)
+  __device__ __forceinline__ OwnWalk(const Plan& g_, const SharedStart& s, int w_)
       : g(g_), b(s.b), p(s.pb), w(w_), left(s.last - max(s.first, s.total_g)) {
     if (left <= 0 || b >= g.a.B) {
       left = 0;
@@ -294,13 +388,13 @@ struct OwnWalk {
     }
     sequence();
     const long long x = max(s.first - s.total_g, 0ll) - s.before_b;
-    head = static_cast<int>(x / n);            // find_start has found the sequence that holds it
+    head = quotient(x, n);                       // find_start has found the sequence that holds it
     g0 = static_cast<int>(x - static_cast<long long>(head) * n);
   }
   __device__ __forceinline__ void sequence() {
     while (p + 1 < g.groups && g.start[p + 1] <= b) ++p;
     const Group gr(g, p);
-    L = sched::clamp_len(g.a.cache_len, b, cap_of(g.a));
+    L = sched::clamp_len(g.cache_len, b, cap_of(g.a));
     from = shared_of(g, gr, b, L);
     n = sched::granules<kKeys>(L - from);
     head = 0;
@@ -328,14 +422,14 @@ struct OwnWalk {
 
 template <int D>
 __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUtensorMap& mv,
-                                                const CUtensorMap& mr, const SharedArgs& g,
+                                                const CUtensorMap& mr, const Plan& g,
                                                 uint8_t* base, PBars* bars, uint32_t tb,
                                                 PrefixWalk walk) {
   using C = PC<D>;
   const PagedArgs& a = g.a;
   uint8_t* sQ = base;                            // [2][TILE]
-  uint8_t* sK = sQ + 2 * C::TILE;                // [NST][TILE]
-  uint8_t* sV = sK + C::NST * C::TILE;           // [NST][TILE]
+  uint8_t* sK = sQ + 2 * C::TILE;                // [NK][TILE]
+  uint8_t* sV = sK + C::NK * C::TILE;            // [NV][TILE]
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
@@ -350,8 +444,10 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
     const int shift = a.page_shift;
     const int rows = min(kKeys, 1 << shift), boxes = kKeys / rows;
     const uint32_t bits = (1u << (rows / 16)) - 1u;
+    const int stages = keys ? C::NK : C::NV;
     bool ok = true;
-    int n = 0, ns = 0;
+    int n = 0, ns = 0, st = 0;
+    uint32_t round = 0;                          // of the stages
     while (ok && walk.next(sg)) {
       if (!keys) {   // the queries with the values, which are needed later than the first keys
         if (ns > 0) {
@@ -372,20 +468,19 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
       int rep = -1;
       for (int b = gr.s0; rep < 0 && b < gr.s1; b += 32) {
         const bool has = b + lane < gr.s1 &&
-                         sched::clamp_len(a.cache_len, b + lane, cap_of(a)) >= gr.len;
+                         sched::clamp_len(g.cache_len, b + lane, cap_of(a)) >= gr.len;
         const uint32_t hit = __ballot_sync(0xffffffffu, has);
         if (hit) rep = b + __ffs(hit) - 1;
       }
       const int32_t* row = a.table + max(rep, 0) * a.table_stride;
       for (int k0 = sg.k0; k0 < sg.k1; k0 += kKeys, ++n) {
-        const int st = n % C::NST;
         const int x = k0 + lane * rows;
         int p = -1;
         if (lane < boxes && x < sg.k1 && rep >= 0) p = row[x >> shift];
         const bool in = p >= 0 && p < a.num_pages;
         const uint32_t pages = __ballot_sync(0xffffffffu, in);
-        if (n >= C::NST) {
-          ok = mbar_wait_warp(&empty[st], ((n / C::NST) - 1) & 1, abort_flag, a.err, a.wait_ns);
+        if (round > 0) {
+          ok = mbar_wait_warp(&empty[st], (round - 1) & 1, abort_flag, a.err, a.wait_ns);
           if (!ok) break;
         }
         if (lane == 0) {
@@ -405,6 +500,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
           for (int s = 0; s < C::NSUB; ++s)
             tma_load_4d(dst + s * kSub, map, &full[st], 64 * s, y, sg.head, p);
         }
+        if (++st == stages) st = 0, ++round;
       }
       ++ns;
     }
@@ -424,7 +520,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
       bool ok = true;
       int n = 0, ns = 0, npv = 0, nout = 0;
       auto scores = [&](int m) {         // of the m-th key tile
-        const uint64_t dK = dK0 + static_cast<uint64_t>(m % C::NST) * kTileD;
+        const uint64_t dK = dK0 + static_cast<uint64_t>(m % C::NK) * kTileD;
 #pragma unroll
         for (int q = 0; q < C::NSUB; ++q) {
           uint64_t da[4], db[4];
@@ -438,23 +534,23 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
         }
         mma_commit(&bars->s_full[t]);
       };
-      auto wait_full = [&](uint64_t* full, int m) {
-        ok = mbar_wait(&full[m % C::NST], (m / C::NST) & 1, abort_flag, a.err, a.wait_ns);
+      auto keys_in = [&](int m) {
+        ok = mbar_wait(&bars->k_full[m % C::NK], (m / C::NK) & 1, abort_flag, a.err, a.wait_ns);
+        tc_fence_after();
         return ok;
       };
       while (ok && walk.next(sg)) {
         const int blocks = sg.blocks(), mine = sg.count(t);
         ok = mbar_wait(&bars->q_full, ns & 1, abort_flag, a.err, a.wait_ns);
-        if (!ok || !wait_full(bars->k_full, n)) break;
-        tc_fence_after();
+        if (!ok || !keys_in(n)) break;
         if (sg.need(t, 0)) scores(n);
-        mma_commit(&bars->k_empty[n % C::NST]);
+        mma_commit(&bars->k_empty[n % C::NK]);
         if (blocks == 1) mma_commit(&bars->q_empty);
         int done = 0;
         for (int j = 0; j < blocks; ++j, ++n) {
-          if (!wait_full(bars->v_full, n)) break;
-          if (j + 1 < blocks && !wait_full(bars->k_full, n + 1)) break;
-          tc_fence_after();
+          ok = mbar_wait(&bars->v_full[n % C::NV], (n / C::NV) & 1, abort_flag, a.err, a.wait_ns);
+          // the next keys too, so that their scores are issued right behind this product
+          if (!ok || (j + 1 < blocks && !keys_in(n + 1))) break;
           if (sg.need(t, j)) {
             ok = mbar_wait(&bars->p_full[t], npv & 1, abort_flag, a.err, a.wait_ns);
             // the previous segment's O has been read
@@ -462,7 +558,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
               ok = mbar_wait(&bars->o_empty[t], (nout - 1) & 1, abort_flag, a.err, a.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dV = dV0 + static_cast<uint64_t>(n % C::NST) * kTileD;
+            const uint64_t dV = dV0 + static_cast<uint64_t>(n % C::NV) * kTileD;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint32_t ta[4];
@@ -477,10 +573,10 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
             ++npv;
             if (++done == mine) mma_commit(&bars->o_done[t]);
           }
-          mma_commit(&bars->v_empty[n % C::NST]);
+          mma_commit(&bars->v_empty[n % C::NV]);
           if (j + 1 < blocks) {
             if (sg.need(t, j + 1)) scores(n + 1);
-            mma_commit(&bars->k_empty[(n + 1) % C::NST]);
+            mma_commit(&bars->k_empty[(n + 1) % C::NK]);
             if (j + 2 == blocks) mma_commit(&bars->q_empty);
           }
         }
@@ -588,12 +684,12 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
           if (edge && (t == 0 || !sg.both)) {
             // Hidden rows of V: zero, so that 0 x (anything) stays 0.  The stage is this tile's once
             // its load has completed.
-            ok = mbar_wait_warp(&bars->v_full[n % C::NST], (n / C::NST) & 1, abort_flag, a.err,
+            ok = mbar_wait_warp(&bars->v_full[n % C::NV], (n / C::NV) & 1, abort_flag, a.err,
                                 a.wait_ns);
             if (!ok) break;
             const int i = tid - 128, r = i & 127;
             if (r >= lim || !((seen >> (r >> 4)) & 1u)) {
-              uint8_t* vt = sV + (n % C::NST) * C::TILE + r * 128;
+              uint8_t* vt = sV + (n % C::NV) * C::TILE + r * 128;
 #pragma unroll
               for (int ch = 0; ch < 4 * C::NSUB; ++ch) {
                 const int at = (i >> 7) * 4 * C::NSUB + ch;      // 16-byte piece of the row
@@ -636,9 +732,9 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
         // lead past the end, where nothing is written.
         const int rows = (sg.both ? (t == 0 ? g.seqs : sg.n - g.seqs) : sg.n) * G;
         const long long e0 = sg.entry + t * g.seqs * G;
-        const bool wA = rA < rows && e0 + rA < g.entries, wB = rB < rows && e0 + rB < g.entries;
-        float* outA = g.part + (e0 + rA) * TC<D>::PSTRIDE;
-        float* outB = g.part + (e0 + rB) * TC<D>::PSTRIDE;
+        const bool wA = rA < rows && e0 + rA < g.s.entries, wB = rB < rows && e0 + rB < g.s.entries;
+        float* outA = g.s.part + (e0 + rA) * D;
+        float* outB = g.s.part + (e0 + rB) * D;
         const bool join = !sg.both && any[1];
         float M[2], w[2][2];     // of rows A and B
 #pragma unroll
@@ -664,22 +760,25 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
               ov[i] = __float_as_uint(__uint_as_float(ov[i]) * w[0][(i >> 1) & 1] +
                                       __uint_as_float(o1[i]) * w[1][(i >> 1) & 1]);
           }
+          // Neighbouring threads of a row exchange halves of two column groups: four columns each.
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
-            const int col = 64 * half + 8 * cc + 2 * t4;
-            if (wA)
-              *reinterpret_cast<float2*>(outA + col) =
-                  make_float2(__uint_as_float(ov[4 * cc]), __uint_as_float(ov[4 * cc + 1]));
-            if (wB)
-              *reinterpret_cast<float2*>(outB + col) =
-                  make_float2(__uint_as_float(ov[4 * cc + 2]), __uint_as_float(ov[4 * cc + 3]));
+          for (int cc = 0; cc < 8; cc += 2) {
+            const int odd = t4 & 1, col = 64 * half + 8 * (cc + odd) + 4 * (t4 >> 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {        // row A, row B
+              const uint32_t* u = ov + 4 * cc + 2 * i;
+              const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? u[0] : u[4], 1);
+              const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? u[1] : u[5], 1);
+              const uint4 q = odd ? make_uint4(x, y, u[4], u[5]) : make_uint4(u[0], u[1], x, y);
+              if (i ? wB : wA) *reinterpret_cast<uint4*>((i ? outB : outA) + col) = q;
+            }
           }
         }
         if (t4 == 0) {
           const float lA = join ? l[0][0] * w[0][0] + l[1][0] * w[1][0] : l[t][0];
           const float lB = join ? l[0][1] * w[0][1] + l[1][1] * w[1][1] : l[t][1];
-          if (wA) *reinterpret_cast<float2*>(outA + D) = make_float2(M[0], lA);
-          if (wB) *reinterpret_cast<float2*>(outB + D) = make_float2(M[1], lB);
+          if (wA) g.s.stats[e0 + rA] = make_float2(M[0], lA);
+          if (wB) g.s.stats[e0 + rB] = make_float2(M[1], lB);
         }
       }
       tc_fence_before();
@@ -690,6 +789,9 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
   }
 }
 
+static_assert(TC<64>::SMEM + sizeof(Lists) + 600 <= 227 * 1024 &&
+                  TC<128>::SMEM + sizeof(Lists) + 600 <= 227 * 1024, "shared memory");
+
 template <int D, int GP>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -698,16 +800,18 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const Smem<D> sh(base);
   __shared__ PBars pb;
+  const Smem<D> sh(base);
+  Bars* db = sh.bars;                            // of the continuations
   __shared__ SharedStart start;
   __shared__ long long scan[kThreads / 32][2];
+  __shared__ Lists lists;
   const int tid = threadIdx.x, warp = tid >> 5;
 
   if (tid == 0) {
     mbar_init(&pb.q_full, 1);
     mbar_init(&pb.q_empty, 2);
-    for (int s = 0; s < PC<D>::NST; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&pb.k_full[s], 1);
       mbar_init(&pb.k_empty[s], 2);
       mbar_init(&pb.v_full[s], 1);
@@ -722,7 +826,7 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
     mbar_init(&pb.drain, 2);
     pb.abort = 0;
     pb.never = 0;
-    init_bars<D>(sh.bars);
+    init_bars<D>(db);
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
     tma_prefetch_desc(&mq);
@@ -734,13 +838,14 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
   }
   griddep_wait();
   griddep_launch_dependents();
+  const Plan plan(g, &lists);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  find_start(&start, scan, g, blockIdx.x, gridDim.x, blockIdx.x == 0);
+  find_start(&start, scan, plan, blockIdx.x, gridDim.x, blockIdx.x == 0);
   const uint32_t tb = pb.tmem_base;
   if (start.first < min(start.last, start.total_g)) {
-    prefix_segments<D>(mk, mv, mr, g, base, &pb, tb, PrefixWalk(g, start, blockIdx.x));
+    prefix_segments<D>(mk, mv, mr, plan, base, &pb, tb, PrefixWalk(plan, start, blockIdx.x));
     // The tiles' memory, shared and tensor, goes over to the continuations.
     fence_proxy_async_smem();
     tc_fence_before();
@@ -748,11 +853,11 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
     tc_fence_after();
   }
   if (!pb.abort && start.last > max(start.first, start.total_g))
-    segments<D, GP>(mk, mv, mq, g.a, sh, tb, OwnWalk(g, start, blockIdx.x));
+    segments<D, GP>(mk, mv, mq, g.a, sh, tb, OwnWalk(plan, start, blockIdx.x));
 
   tc_fence_before();
   __syncthreads();
-  if ((pb.abort || sh.bars->abort) && tid == 0) {
+  if ((pb.abort || db->abort) && tid == 0) {
     // Let any copy still in flight land before the CTA's shared memory is released.
     const uint64_t t0 = globaltimer();
     while (globaltimer() - t0 < 1000000ull) {
@@ -779,37 +884,38 @@ __global__ void __launch_bounds__(256) decode_shared_combine_kernel(
   const long long row = blockIdx.x * static_cast<long long>(8 / W) + warp / W;
   const bool live = row < static_cast<long long>(a.B) * a.Hq;
   const int b = live ? static_cast<int>(row / a.Hq) : 0, hq = live ? static_cast<int>(row % a.Hq) : 0;
-  const int head = hq / G, h = hq % G, p = g.group_of[b], workers = *g.workers;
-  const long long total_g = g.tiles_g[g.groups], total = total_g + g.tiles_b[a.B];
-  const long long t0 = g.tiles_b[b], n = (g.tiles_b[b + 1] - t0) / a.Hkv;
-  const Group gr(g, p);
-  const int shared = shared_of(g, gr, b, sched::clamp_len(a.cache_len, b, cap_of(a)));
+  const int head = hq / G, h = hq % G;
+  const Line line = *g.line;
+  const Row r = g.rows[b];
   int own = 0, pre = 0, step = 0;                // parts of the continuation, of the prefix
-  const float *own0 = nullptr, *pre0 = nullptr;  // the first ones
-  if (n > 0) {
-    const long long first = total_g + t0 + head * n;
-    const int w0 = sched::owner(first, total, workers);
-    own = sched::owner(first + n - 1, total, workers) - w0 + 1;
+  const float* own0 = nullptr;                   // the first ones
+  long long pre0 = 0;
+  if (r.n > 0) {
+    const long long first = r.own + static_cast<long long>(head) * r.n;
+    const int w0 = owner(first, line.total, line.workers);
+    own = owner(first + r.n - 1, line.total, line.workers) - w0 + 1;
     own0 = a.part + ((static_cast<long long>(b) * a.Hkv + head + w0) * G + h) * PS;
   }
-  if (shared > 0) {
-    const int piece = (b - gr.s0) / (2 * g.seqs), s = (b - gr.s0) % (2 * g.seqs);
-    const long long first =
-        g.tiles_g[p] +
-        (static_cast<long long>(head) * gr.supers + piece) * gr.tiles * gr.cost;
-    const int w0 = sched::owner(first, total, workers);
-    pre = sched::owner(first + static_cast<long long>(gr.tiles - 1) * gr.cost, total, workers) - w0 + 1;
+  if (r.span >= 0) {
+    const long long first = r.pre + head * r.pre_head;
+    const int w0 = owner(first, line.total, line.workers);
+    pre = owner(first + r.span, line.total, line.workers) - w0 + 1;
     step = 2 * g.seqs * G;
-    const long long e = first_entry(g, gr, head, piece) + s * G + h + static_cast<long long>(w0) * step;
-    pre = static_cast<int>(min(static_cast<long long>(pre), (g.entries - 1 - e) / step + 1));
-    pre0 = g.part + e * PS;
+    pre0 = r.entry + static_cast<long long>(head) * r.entry_head + h +
+           static_cast<long long>(w0) * step;
+    pre = static_cast<int>(min(static_cast<long long>(pre), (g.entries - 1 - pre0) / step + 1));
   }
   // A continuation that is all of its rows' keys and one CTA's is finished; W > 1: the block goes on
   // to its barrier.
-  const bool todo = live && !(shared == 0 && own == 1);
+  const bool todo = live && !(r.span < 0 && own == 1);
   const int parts = todo ? pre + own : 0;
-  auto at = [&](int i) {
-    return i < pre ? pre0 + static_cast<long long>(i) * step * PS : own0 + (i - pre) * G * PS;
+  auto o_at = [&](int i) {
+    return i < pre ? g.part + (pre0 + static_cast<long long>(i) * step) * D
+                   : own0 + (i - pre) * G * PS;
+  };
+  auto stats_at = [&](int i) {
+    return i < pre ? g.stats + (pre0 + static_cast<long long>(i) * step)
+                   : reinterpret_cast<const float2*>(own0 + (i - pre) * G * PS + D);
   };
   float acc[PER];
 #pragma unroll
@@ -817,7 +923,25 @@ __global__ void __launch_bounds__(256) decode_shared_combine_kernel(
   float M = -INFINITY, lsum = 0.f;
   for (int base = sub; base < parts; base += 32 * W) {
     const int mine = base + lane * W;
-    const float2 ml = *reinterpret_cast<const float2*>(at(mine < parts ? mine : base) + D);
+    const int cnt = min(32, (parts - base + W - 1) / W);
+    // Eight parts' loads in flight, the first ones beside their statistics'; those past the last repeat
+    // it with weight 0.
+    float v[8][PER];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float* pj = o_at(base + min(j0 + j, cnt - 1) * W) + lane * PER;
+        if constexpr (PER == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(pj);
+          v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(pj);
+          v[j][0] = x.x, v[j][1] = x.y;
+        }
+      }
+    };
+    const float2 ml = *stats_at(mine < parts ? mine : base);
+    load(0);
     const float m = mine < parts ? ml.x : -INFINITY, l = mine < parts ? ml.y : 0.f;
     const float mb = fmaxf(M, warp_max(m));
     const float use = mb == -INFINITY ? 0.f : mb;
@@ -827,21 +951,8 @@ __global__ void __launch_bounds__(256) decode_shared_combine_kernel(
     lsum = lsum * keep + l * wt;                 // without a key l is 0, of a NaN query NaN
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] *= keep;
-    const int cnt = min(32, (parts - base + W - 1) / W);
-    // Eight parts' loads in flight; those past the last repeat it with weight 0.
     for (int j0 = 0; j0 < cnt; j0 += 8) {
-      float v[8][PER];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float* pj = at(base + min(j0 + j, cnt - 1) * W) + lane * PER;
-        if constexpr (PER == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(pj);
-          v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(pj);
-          v[j][0] = x.x, v[j][1] = x.y;
-        }
-      }
+      if (j0 > 0) load(j0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float wj = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
@@ -950,9 +1061,9 @@ long long own_entries(int B, int Hkv, int G) {
 size_t decode_shared_bytes(int B, int Hq, int Hkv, int d) {
   const int G = Hq / Hkv;
   const size_t entry = (d + 4) * sizeof(float);
-  return round_up(prefix_entries(B, Hq, G) * entry, 256) +
+  return round_up(prefix_entries(B, Hq, G) * (d * sizeof(float) + sizeof(float2)), 256) +
          round_up(own_entries(B, Hkv, G) * entry, 256) +
-         2 * (static_cast<size_t>(B) + 1) * sizeof(long long) + (B + 1) * sizeof(int32_t);
+         B * (sizeof(Row) + sizeof(long long)) + sizeof(Line);
 }
 
 cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
@@ -968,15 +1079,15 @@ cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
   SharedArgs g{};
   g.entries = prefix_entries(B, Hq, G);
   g.part = reinterpret_cast<float*>(at);
-  at += round_up(g.entries * entry, 256);
+  g.stats = reinterpret_cast<float2*>(g.part + g.entries * d);
+  at += round_up(g.entries * (d * sizeof(float) + sizeof(float2)), 256);
   g.a = PagedArgs{table, table_stride, max_pages, page_shift, num_pages, cache_len, B, Hq, Hkv,
                   scale * kLog2e, static_cast<__nv_bfloat16*>(o), lse,
                   reinterpret_cast<float*>(at), nullptr, err, wait_ns};
   at += round_up(own_entries(B, Hkv, G) * entry, 256);
-  g.tiles_g = reinterpret_cast<long long*>(at);
-  g.tiles_b = g.tiles_g + B + 1;
-  g.group_of = reinterpret_cast<int32_t*>(g.tiles_b + B + 1);
-  g.workers = g.group_of + B;
+  g.rows = reinterpret_cast<Row*>(at);
+  g.line = reinterpret_cast<Line*>(g.rows + B);
+  g.tiles_g = reinterpret_cast<long long*>(g.line + 1);
   g.start = start;
   g.len = shared_len;
   g.groups = groups;
