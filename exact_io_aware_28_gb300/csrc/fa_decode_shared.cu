@@ -11,15 +11,14 @@
 // What bounds it: the bytes of the prefixes, once, and of the continuations; with many sequences a
 // group also the products over the prefix, 4 S d operations a row, on the tensor cores.
 //
-// Work.  All tiles of 128 keys lie on one line: first the prefixes' (group by group, head by head,
-// 256 rows by 256 rows), then the continuations' (sequence by sequence, head by head).  A tile of
-// either kind costs about the same: 64 KB at d = 128 from HBM take an SM some 2.8k cycles when all
-// read, and 256 rows of a prefix tile some 2.6k of products and exponentials.  Worker w of W takes
-// the tiles [total w / W, total (w + 1) / W), so every SM has the same share of the whole, and the
-// one launch has no seam between prefixes and continuations.  Every segment of a pair in a worker's
-// range leaves a partial result in a place of its own: (pair) + (worker) grows along the line, so
-// no two meet.  A combine kernel joins them.  The cut depends on lengths, groups and W alone: the
-// same call gives the same bits.
+// Work.  The tiles of 128 keys of all prefixes lie on one line (group by group, head by head, 256 rows
+// by 256 rows), those of the continuations on another (sequence by sequence, head by head).  The
+// CTAs, one an SM, are shared out between the two by what the tiles cost, and worker w of a line's W
+// takes its tiles [total w / W, total (w + 1) / W): both kinds run side by side, products of the one
+// beside loads of the other, and end at about the same time.  Every segment of a pair in a worker's
+// range leaves a partial result in a place of its own: (pair) + (worker) grows along the line, so no
+// two meet.  A combine kernel joins them.  The cut depends on lengths, groups and the number of SMs
+// alone: the same call gives the same bits.
 //
 // A prefix segment (one CTA, two tiles of up to 128 query rows; a tile holds 128 / G sequences of
 // G heads, in whole sequences):
@@ -87,7 +86,7 @@ struct SharedArgs {
   long long entries;
   struct Row* rows;            // [B], for the combine kernel
   struct Line* line;
-  long long* tiles_g;          // [groups], costs before each group
+  long long* tiles_g;          // [groups], tiles before each group
 };
 
 // What the combine kernel needs to know of a sequence: where on the line its own tiles and its
@@ -102,15 +101,15 @@ struct Row {
   int pad;
 };
 struct Line {
-  long long total;
-  int workers;                 // that have a range
+  long long total[2];          // tiles of the prefixes, of the continuations
+  int workers[2];              // that have a range
 };
 
 __device__ __forceinline__ int cap_of(const PagedArgs& a) { return a.max_pages << a.page_shift; }
 
 // The arguments with the lists of lengths and groups: copies in shared memory where they fit (what
 // the tiles leave of it).
-constexpr int kListed = 160;
+constexpr int kListed = 150;
 struct Lists {
   int32_t cache_len[kListed], len[kListed], start[kListed + 1];
 };
@@ -154,13 +153,17 @@ __device__ __forceinline__ int owner(long long x, long long total, int workers) 
   return sched::owner(x, total, workers);
 }
 
+// What a tile costs: a prefix's with rows for both row tiles, for one; a continuation's; and what a
+// pair adds to its tiles (queries, results): a prefix's, a continuation's.
+constexpr int kCostBoth = 9, kCostOne = 5, kCostOwn = 4, kCostPrefixPair = 4, kCostOwnPair = 2;
+
 struct Group {
   int s0, s1;                  // its sequences
   int len;                     // shared tokens; shorter sequences take no part
   int keys;                    // of them, those read once: whole boxes
   int supers;                  // pieces of up to 2 x seqs sequences
   int tiles;
-  int cost;                    // of a tile: 2 where pieces have rows for both tiles
+  int cost;                    // of a tile
   __device__ __forceinline__ Group(const Plan& g, int p) {
     s0 = min(max(g.start[p], 0), g.a.B);
     s1 = max(s0, min(max(g.start[p + 1], 0), g.a.B));
@@ -170,13 +173,12 @@ struct Group {
     keys = len & ~(box - 1);
     supers = (s1 - s0 + 2 * g.seqs - 1) / (2 * g.seqs);
     tiles = sched::granules<kKeys>(keys);
-    cost = s1 - s0 > g.seqs ? 2 : 1;
+    cost = s1 - s0 > g.seqs ? kCostBoth : kCostOne;
   }
-  // Its tiles of all heads and pieces, and what they cost.
+  // Its tiles of all heads and pieces.
   __device__ __forceinline__ long long all(const Plan& g) const {
     return static_cast<long long>(tiles) * g.a.Hkv * supers;
   }
-  __device__ __forceinline__ long long costs(const Plan& g) const { return all(g) * cost; }
 };
 
 // The group of sequence b: the last whose first sequence is not behind it.
@@ -195,21 +197,32 @@ __device__ __forceinline__ int shared_of(const Plan& g, const Group& p, int b, i
 }
 
 struct SharedStart {
-  long long first, last;       // the worker's range of the line
-  long long total_g;           // cost of the prefixes' tiles
-  int p, b, pb;                // group of the first prefix tile; sequence of the first own tile, its group
-  long long before_p, before_b;
+  int mine;                    // 0: the CTA works on prefixes, 1: on continuations
+  int w;                       // which of their workers it is
+  long long first, last;       // its range of their tiles
+  int p, b, pb;                // group of the first tile; sequence of the first tile, and its group
+  long long before;            // tiles before that group or sequence
 };
 
-// Workers that have a range.  Every range holds the beginning of a tile: with tiles of cost 2 it is
-// two long at least.
-__device__ __forceinline__ int active_workers(long long total, bool heavy, int workers) {
-  return sched::active(heavy ? (total + 1) >> 1 : total, workers);
+// How many of W workers go to the prefixes: their share of the cost.  The two SMs of a pair (the CTAs
+// 2 i and 2 i + 1) do the same: with one on a prefix and one on continuations both take up to twice
+// as long (the cause is not known).
+__device__ __forceinline__ int prefix_workers(int W, float cost_g, float cost_b) {
+  if (cost_g == 0.f || cost_b == 0.f) return cost_g == 0.f ? 0 : W;
+  int n = static_cast<int>(W * (cost_g / (cost_g + cost_b)) + 0.5f);
+  n = max(1, min(W - 1, n));
+  if ((n & 1) && W > 2) n += 2 * n <= W ? 1 : -1;
+  return n;
 }
 
-// As sched::find_start, for both parts of the line.  write: what the combine kernel reads.
-__device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch)[2],
-                                           const Plan& g, int w, int workers, bool write) {
+struct Sums {
+  long long tiles[2];
+  float cost[2];
+};
+
+// The CTA's part of the work, as sched::find_start.  write: what the combine kernel reads.
+__device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
+                                           const Plan& g) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = g.a.B, cap = cap_of(g.a);
   const int per_p = (g.groups + kThreads - 1) / kThreads, per_b = (B + kThreads - 1) / kThreads;
   const int p0 = min(tid * per_p, g.groups), p1 = min(p0 + per_p, g.groups);
@@ -222,15 +235,21 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
     return sched::granules<kKeys>(L - shared_of(g, gr, b, L));
   };
   long long sum[2] = {0, 0};
-  bool heavy = false;
+  float cost[2] = {0.f, 0.f};
   for (int p = p0; p < p1; ++p) {
     const Group gr(g, p);
-    sum[0] += gr.costs(g);
-    heavy |= gr.tiles > 0 && gr.cost > 1;
+    sum[0] += gr.all(g);
+    if (gr.tiles > 0)
+      cost[0] += static_cast<float>(gr.tiles * gr.cost + kCostPrefixPair) *
+                 static_cast<float>(g.a.Hkv * gr.supers);
   }
   {
     int p = at0;
-    for (int b = b0; b < b1; ++b) sum[1] += static_cast<long long>(own_tiles(b, &p)) * g.a.Hkv;
+    for (int b = b0; b < b1; ++b) {
+      const int n = own_tiles(b, &p);
+      sum[1] += static_cast<long long>(n) * g.a.Hkv;
+      if (n > 0) cost[1] += static_cast<float>(n * kCostOwn + kCostOwnPair) * g.a.Hkv;
+    }
   }
   long long incl[2] = {sum[0], sum[1]};
 #pragma unroll
@@ -240,53 +259,63 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
       const long long up = __shfl_up_sync(0xffffffffu, incl[i], off);
       if (lane >= off) incl[i] += up;
     }
-  if (lane == 31) scratch[warp][0] = incl[0], scratch[warp][1] = incl[1];
-  if (tid == 0) {
-    out->p = g.groups, out->b = B, out->pb = 0;
-    out->before_p = out->before_b = 0;
-  }
-  heavy = __syncthreads_or(heavy) != 0;
-  long long before[2] = {incl[0] - sum[0], incl[1] - sum[1]}, total[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i)
+  for (int off = 16; off > 0; off >>= 1) {
+    cost[0] += __shfl_xor_sync(0xffffffffu, cost[0], off);
+    cost[1] += __shfl_xor_sync(0xffffffffu, cost[1], off);
+  }
+  if (lane == 31) scratch[warp] = Sums{{incl[0], incl[1]}, {cost[0], cost[1]}};
+  __syncthreads();
+  long long before[2] = {incl[0] - sum[0], incl[1] - sum[1]}, total[2] = {0, 0};
+  cost[0] = cost[1] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const long long v = scratch[i][j];
+      const long long v = scratch[i].tiles[j];
       if (i < warp) before[j] += v;
       total[j] += v;
+      cost[j] += scratch[i].cost[j];
     }
-  const long long all = total[0] + total[1];
-  const int W = active_workers(all, heavy, workers);
-  const long long first = w < W ? range_start(all, w, W) : all;
-  if (tid == 0) {
-    out->first = first;
-    out->last = w < W ? range_start(all, w + 1, W) : all;
-    out->total_g = total[0];
   }
+  const int share = prefix_workers(gridDim.x, cost[0], cost[1]);
+  const int W0 = sched::active(total[0], share);
+  const int W1 = sched::active(total[1], static_cast<int>(gridDim.x) - share);
+  const int block = blockIdx.x, mine = block < share ? 0 : 1, w = block - (mine ? share : 0);
+  const int W = mine ? W1 : W0;
+  const long long all = mine ? total[1] : total[0];
+  const bool works = w < W;
+  const long long first = works ? range_start(all, w, W) : 0;
+  if (tid == 0) {
+    out->mine = mine;
+    out->w = w;
+    out->first = first;
+    out->last = works ? range_start(all, w + 1, W) : 0;
+  }
+  const bool write = block == 0;
   long long at = before[0];
-  if (write || (first >= at && first < at + sum[0]))
+  if (write || (works && mine == 0 && first >= at && first < at + sum[0]))
     for (int p = p0; p < p1; ++p) {
-      const long long n = p0 + 1 == p1 ? sum[0] : Group(g, p).costs(g);
+      const long long n = p0 + 1 == p1 ? sum[0] : Group(g, p).all(g);
       if (write) g.s.tiles_g[p] = at;
-      if (first >= at && first < at + n) out->p = p, out->before_p = at;
+      if (mine == 0 && first >= at && first < at + n) out->p = p, out->before = at;
       at += n;
     }
   at = before[1];
-  const long long own = first > total[0] ? first - total[0] : 0;
-  if (own >= at && own < at + sum[1]) {
+  if (works && mine == 1 && first >= at && first < at + sum[1]) {
     int p = at0;
     for (int b = b0; b < b1; ++b) {
       const long long n = static_cast<long long>(own_tiles(b, &p)) * g.a.Hkv;
-      if (own >= at && own < at + n) out->b = b, out->pb = p, out->before_b = at;
+      if (first >= at && first < at + n) out->b = b, out->pb = p, out->before = at;
       at += n;
     }
   }
   __syncthreads();
   if (write) {
-    if (tid == 0) *g.s.line = Line{all, W};
+    if (tid == 0) *g.s.line = Line{{total[0], total[1]}, {W0, W1}};
     const int G = g.a.Hq / g.a.Hkv;
     int p = at0;
-    at = total[0] + before[1];
+    at = before[1];
     for (int b = b0; b < b1; ++b) {
       Row r;
       r.n = own_tiles(b, &p);
@@ -299,10 +328,9 @@ __device__ __forceinline__ void find_start(SharedStart* out, long long (*scratch
       r.entry_head = r.pad = 0;
       if (shared_of(g, gr, b, L) > 0) {
         const int piece = (b - gr.s0) / (2 * g.seqs);
-        const long long tiles = static_cast<long long>(gr.tiles) * gr.cost;
-        r.span = (gr.tiles - 1) * gr.cost;
-        r.pre = g.s.tiles_g[p] + piece * tiles;
-        r.pre_head = gr.supers * tiles;
+        r.span = gr.tiles - 1;
+        r.pre = g.s.tiles_g[p] + static_cast<long long>(piece) * gr.tiles;
+        r.pre_head = static_cast<long long>(gr.supers) * gr.tiles;
         r.entry = static_cast<long long>(gr.s0) * g.a.Hq + static_cast<long long>(b - gr.s0) * G;
         r.entry_head = (gr.s1 - gr.s0) * G;
       }
@@ -334,60 +362,50 @@ __device__ __forceinline__ long long first_entry(const Plan& g, const Group& p, 
          2ll * piece * g.seqs * G;
 }
 
-// A tile belongs to the worker in whose range its first unit of cost lies.
 struct PrefixWalk {
   const Plan& g;
   int p, w;
   long long at, last, before;
-  __device__ __forceinline__ PrefixWalk(const Plan& g_, const SharedStart& s, int w_)
-      : g(g_), p(s.p), w(w_), at(s.first), last(min(s.last, s.total_g)), before(s.before_p) {}
+  __device__ __forceinline__ PrefixWalk(const Plan& g_, const SharedStart& s)
+      : g(g_), p(s.p), w(s.w), at(s.first), last(s.last), before(s.before) {}
   __device__ __forceinline__ bool next(PSegment& sg) {
-    for (; p < g.groups && at < last; ++p) {
+    if (at >= last) return false;
+    for (; p < g.groups; ++p) {
       const Group gr(g, p);
-      const long long all = gr.costs(g);
+      const long long all = gr.all(g);
       if (at < before + all) {
-        const int up = gr.cost - 1;            // cost is 1 or 2: a shift, rounded up
-        const long long tile = (at - before + up) >> up;
-        const long long end = min(gr.all(g), (last - before + up) >> up);
-        if (tile < end) {
-          const int pair = quotient(tile, gr.tiles);
-          const long long pair_tile = static_cast<long long>(pair) * gr.tiles;
-          const int piece = pair % gr.supers;
-          const int g0 = static_cast<int>(tile - pair_tile);
-          const int g1 = static_cast<int>(min(static_cast<long long>(gr.tiles), end - pair_tile));
-          sg.p = p;
-          sg.head = pair / gr.supers;
-          sg.k0 = g0 * kKeys;
-          sg.k1 = min(g1 * kKeys, gr.keys);
-          sg.s0 = gr.s0 + piece * 2 * g.seqs;
-          sg.n = min(2 * g.seqs, gr.s1 - sg.s0);
-          sg.both = sg.n > g.seqs;
-          sg.entry = first_entry(g, gr, sg.head, piece) + 2ll * w * g.seqs * (g.a.Hq / g.a.Hkv);
-          at = before + ((pair_tile + g1) << up);
-          return true;
-        }
+        const int pair = quotient(at - before, gr.tiles);
+        const long long pair_start = before + static_cast<long long>(pair) * gr.tiles;
+        const int piece = pair % gr.supers;
+        const int g1 = static_cast<int>(min(static_cast<long long>(gr.tiles), last - pair_start));
+        sg.p = p;
+        sg.head = pair / gr.supers;
+        sg.k0 = static_cast<int>(at - pair_start) * kKeys;
+        sg.k1 = min(g1 * kKeys, gr.keys);
+        sg.s0 = gr.s0 + piece * 2 * g.seqs;
+        sg.n = min(2 * g.seqs, gr.s1 - sg.s0);
+        sg.both = sg.n > g.seqs;
+        sg.entry = first_entry(g, gr, sg.head, piece) + 2ll * w * g.seqs * (g.a.Hq / g.a.Hkv);
+        at = pair_start + g1;
+        return true;
       }
       before += all;
-      at = max(at, before);
     }
     return false;
   }
 };
 
-// A worker's own segments: its first one begins inside a pair, the others with one.
+// The first segment begins inside a pair, the others with one.
 struct OwnWalk {
   const Plan& g;
   int b, p, w, head, g0;
   long long left;              // tiles of the worker's range that are still to come
   int L, from, n;              // of sequence b: length, first own token, tiles of a head
-  __device__ __forceinline__ OwnWalk(const Plan& g_, const SharedStart& s, int w_)
-      : g(g_), b(s.b), p(s.pb), w(w_), left(s.last - max(s.first, s.total_g)) {
-    if (left <= 0 || b >= g.a.B) {
-      left = 0;
-      return;
-    }
+  __device__ __forceinline__ OwnWalk(const Plan& g_, const SharedStart& s)
+      : g(g_), b(s.b), p(s.pb), w(s.w), left(s.last - s.first) {
+    if (left <= 0) return;
     sequence();
-    const long long x = max(s.first - s.total_g, 0ll) - s.before_b;
+    const long long x = s.first - s.before;
     head = quotient(x, n);                       // find_start has found the sequence that holds it
     g0 = static_cast<int>(x - static_cast<long long>(head) * n);
   }
@@ -601,11 +619,13 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
       const int blocks = sg.blocks();
       float m_run[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
       float l_part[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-      for (int j = 0; j < blocks && ok; ++j, ++n) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || !sg.need(t, j)) continue;
-          ok = mbar_wait_warp(&bars->s_full[t], n_s[t] & 1, abort_flag, a.err, a.wait_ns);
+      // One copy of the code for both tiles (state [0] is the current one's): it has to share the
+      // instruction caches with the continuations'.
+#pragma unroll 1
+      for (int jt = 0; jt < 2 * blocks; ++jt) {
+        const int j = jt >> 1, t = jt & 1;
+        if (sg.need(t, j)) {
+          ok = mbar_wait_warp(&bars->s_full[t], n_s[0] & 1, abort_flag, a.err, a.wait_ns);
           if (!ok) break;
           tc_fence_after();
           uint32_t v[64];
@@ -640,7 +660,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
           mB = fmaxf(mB, __shfl_xor_sync(0xffffffffu, mB, 2));
           mA *= a.c;
           mB *= a.c;
-          const float oldA = m_run[t][0], oldB = m_run[t][1];
+          const float oldA = m_run[0][0], oldB = m_run[0][1];
           const float newA = mA > oldA + kRescaleThreshold ? mA : oldA;
           const float newB = mB > oldB + kRescaleThreshold ? mB : oldB;
           const bool chA = newA != oldA, chB = newB != oldB;
@@ -664,10 +684,10 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
           }
           tmem_st_16x128b_x16(lane_base + t * 128, pk);
           const float2 sa = f2_unpack(accA), sb = f2_unpack(accB);
-          l_part[t][0] = l_part[t][0] * alphaA + (sa.x + sa.y);
-          l_part[t][1] = l_part[t][1] * alphaB + (sb.x + sb.y);
-          m_run[t][0] = newA;
-          m_run[t][1] = newB;
+          l_part[0][0] = l_part[0][0] * alphaA + (sa.x + sa.y);
+          l_part[0][1] = l_part[0][1] * alphaB + (sb.x + sb.y);
+          m_run[0][0] = newA;
+          m_run[0][1] = newB;
           // Rescale the running O; the products issued before the scores just read are done.
           if (j > (sg.both ? 0 : t) && __any_sync(0xffffffffu, chA || chB)) {
 #pragma unroll
@@ -702,8 +722,18 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars->p_full[t]);
-          ++n_s[t];
+          ++n_s[0];
         }
+        n += t;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float m = m_run[0][i], l = l_part[0][i];
+          m_run[0][i] = m_run[1][i], l_part[0][i] = l_part[1][i];
+          m_run[1][i] = m, l_part[1][i] = l;
+        }
+        const int s = n_s[0];
+        n_s[0] = n_s[1];
+        n_s[1] = s;
       }
       if (!ok) break;
       // ---- the segment's partial results; tiles with the same rows are joined first
@@ -804,7 +834,7 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
   const Smem<D> sh(base);
   Bars* db = sh.bars;                            // of the continuations
   __shared__ SharedStart start;
-  __shared__ long long scan[kThreads / 32][2];
+  __shared__ Sums scan[kThreads / 32];
   __shared__ Lists lists;
   const int tid = threadIdx.x, warp = tid >> 5;
 
@@ -842,18 +872,14 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  find_start(&start, scan, plan, blockIdx.x, gridDim.x, blockIdx.x == 0);
+  find_start(&start, scan, plan);
   const uint32_t tb = pb.tmem_base;
-  if (start.first < min(start.last, start.total_g)) {
-    prefix_segments<D>(mk, mv, mr, plan, base, &pb, tb, PrefixWalk(plan, start, blockIdx.x));
-    // The tiles' memory, shared and tensor, goes over to the continuations.
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+  if (start.first < start.last) {
+    if (start.mine == 0)
+      prefix_segments<D>(mk, mv, mr, plan, base, &pb, tb, PrefixWalk(plan, start));
+    else
+      segments<D, GP>(mk, mv, mq, g.a, sh, tb, OwnWalk(plan, start));
   }
-  if (!pb.abort && start.last > max(start.first, start.total_g))
-    segments<D, GP>(mk, mv, mq, g.a, sh, tb, OwnWalk(plan, start, blockIdx.x));
 
   tc_fence_before();
   __syncthreads();
@@ -892,14 +918,14 @@ __global__ void __launch_bounds__(256) decode_shared_combine_kernel(
   long long pre0 = 0;
   if (r.n > 0) {
     const long long first = r.own + static_cast<long long>(head) * r.n;
-    const int w0 = owner(first, line.total, line.workers);
-    own = owner(first + r.n - 1, line.total, line.workers) - w0 + 1;
+    const int w0 = owner(first, line.total[1], line.workers[1]);
+    own = owner(first + r.n - 1, line.total[1], line.workers[1]) - w0 + 1;
     own0 = a.part + ((static_cast<long long>(b) * a.Hkv + head + w0) * G + h) * PS;
   }
   if (r.span >= 0) {
     const long long first = r.pre + head * r.pre_head;
-    const int w0 = owner(first, line.total, line.workers);
-    pre = owner(first + r.span, line.total, line.workers) - w0 + 1;
+    const int w0 = owner(first, line.total[0], line.workers[0]);
+    pre = owner(first + r.span, line.total[0], line.workers[0]) - w0 + 1;
     step = 2 * g.seqs * G;
     pre0 = r.entry + static_cast<long long>(head) * r.entry_head + h +
            static_cast<long long>(w0) * step;
