@@ -153,9 +153,11 @@ __device__ __forceinline__ int owner(long long x, long long total, int workers) 
   return sched::owner(x, total, workers);
 }
 
-// What a tile costs: a prefix's with rows for both row tiles, for one; a continuation's; and what a
-// pair adds to its tiles (queries, results): a prefix's, a continuation's.
-constexpr int kCostBoth = 9, kCostOne = 5, kCostOwn = 4, kCostPrefixPair = 4, kCostOwnPair = 2;
+// What a tile costs, in some 0.3 us: a prefix's with rows for both row tiles, for one; a
+// continuation's; what a pair adds to its tiles (queries, results): a prefix's, a continuation's; and
+// what a prefix's CTA takes more than another, however few its tiles are.
+constexpr int kCostBoth = 6, kCostOne = 4, kCostOwn = 4, kCostPrefixPair = 4, kCostOwnPair = 3;
+constexpr int kCostPrefixMore = 24;
 
 struct Group {
   int s0, s1;                  // its sequences
@@ -204,15 +206,21 @@ struct SharedStart {
   long long before;            // tiles before that group or sequence
 };
 
-// How many of W workers go to the prefixes: their share of the cost.  The two SMs of a pair (the CTAs
-// 2 i and 2 i + 1) do the same: with one on a prefix and one on continuations both take up to twice
-// as long (the cause is not known).
-__device__ __forceinline__ int prefix_workers(int W, float cost_g, float cost_b) {
-  if (cost_g == 0.f || cost_b == 0.f) return cost_g == 0.f ? 0 : W;
-  int n = static_cast<int>(W * (cost_g / (cost_g + cost_b)) + 0.5f);
-  n = max(1, min(W - 1, n));
-  if ((n & 1) && W > 2) n += 2 * n <= W ? 1 : -1;
-  return n;
+// How many of W workers go to the prefixes: so many, n, that both kinds end at the same time,
+//   cost_g / n + D = cost_b / (W - n),   D = kCostPrefixMore,
+// and none that one kind has no tile for while the other has.  The two SMs of a pair (the CTAs 2 i and
+// 2 i + 1) do the same: with one on a prefix and one on continuations both take up to twice as long
+// (16 groups of 4 sequences, 2048 + 128 tokens, so mixed throughout: 81 us against 47; the cause is
+// not known).
+__device__ __forceinline__ int prefix_workers(int W, long long tiles_g, long long tiles_b,
+                                              float cost_g, float cost_b) {
+  if (tiles_g == 0 || tiles_b == 0) return tiles_g == 0 ? 0 : W;
+  if (tiles_g + tiles_b <= W) return static_cast<int>(tiles_g);
+  const float D = kCostPrefixMore, p = D * W - cost_g - cost_b;
+  long long n = static_cast<long long>((p + sqrtf(p * p + 4.f * D * cost_g * W)) / (2.f * D) + 0.5f);
+  n += 2 * n <= W ? n & 1 : -(n & 1);
+  n = max(min(n, tiles_g), W - tiles_b);
+  return static_cast<int>(max(1ll, min(W - 1ll, n)));
 }
 
 struct Sums {
@@ -278,7 +286,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
       cost[j] += scratch[i].cost[j];
     }
   }
-  const int share = prefix_workers(gridDim.x, cost[0], cost[1]);
+  const int share = prefix_workers(gridDim.x, total[0], total[1], cost[0], cost[1]);
   const int W0 = sched::active(total[0], share);
   const int W1 = sched::active(total[1], static_cast<int>(gridDim.x) - share);
   const int block = blockIdx.x, mine = block < share ? 0 : 1, w = block - (mine ? share : 0);
