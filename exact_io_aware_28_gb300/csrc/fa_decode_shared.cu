@@ -186,6 +186,7 @@ struct Group {
 // The group of sequence b: the last whose first sequence is not behind it.
 __device__ __forceinline__ int group_at(const Plan& g, int b) {
   int lo = 0, hi = g.groups;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (g.start[mid] <= b) lo = mid; else hi = mid;
@@ -237,6 +238,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
   const int b0 = min(tid * per_b, B), b1 = min(b0 + per_b, B);
   const int at0 = b0 < b1 ? group_at(g, b0) : 0;
   auto own_tiles = [&](int b, int* p) {        // of a head
+#pragma unroll 1
     while (*p + 1 < g.groups && g.start[*p + 1] <= b) ++*p;
     const int L = sched::clamp_len(g.cache_len, b, cap);
     const Group gr(g, *p);
@@ -244,6 +246,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
   };
   long long sum[2] = {0, 0};
   float cost[2] = {0.f, 0.f};
+#pragma unroll 1
   for (int p = p0; p < p1; ++p) {
     const Group gr(g, p);
     sum[0] += gr.all(g);
@@ -253,6 +256,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
   }
   {
     int p = at0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int n = own_tiles(b, &p);
       sum[1] += static_cast<long long>(n) * g.a.Hkv;
@@ -303,6 +307,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
   const bool write = block == 0;
   long long at = before[0];
   if (write || (works && mine == 0 && first >= at && first < at + sum[0]))
+#pragma unroll 1
     for (int p = p0; p < p1; ++p) {
       const long long n = p0 + 1 == p1 ? sum[0] : Group(g, p).all(g);
       if (write) g.s.tiles_g[p] = at;
@@ -312,6 +317,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
   at = before[1];
   if (works && mine == 1 && first >= at && first < at + sum[1]) {
     int p = at0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const long long n = static_cast<long long>(own_tiles(b, &p)) * g.a.Hkv;
       if (first >= at && first < at + n) out->b = b, out->pb = p, out->before = at;
@@ -324,6 +330,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
     const int G = g.a.Hq / g.a.Hkv;
     int p = at0;
     at = before[1];
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       Row r;
       r.n = own_tiles(b, &p);
@@ -378,6 +385,7 @@ struct PrefixWalk {
       : g(g_), p(s.p), w(s.w), at(s.first), last(s.last), before(s.before) {}
   __device__ __forceinline__ bool next(PSegment& sg) {
     if (at >= last) return false;
+#pragma unroll 1
     for (; p < g.groups; ++p) {
       const Group gr(g, p);
       const long long all = gr.all(g);
@@ -418,6 +426,7 @@ struct OwnWalk {
     g0 = static_cast<int>(x - static_cast<long long>(head) * n);
   }
   __device__ __forceinline__ void sequence() {
+#pragma unroll 1
     while (p + 1 < g.groups && g.start[p + 1] <= b) ++p;
     const Group gr(g, p);
     L = sched::clamp_len(g.cache_len, b, cap_of(g.a));
@@ -483,6 +492,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
         if (lane == 0) {
           const uint32_t box = static_cast<uint32_t>(g.seqs) * G * 128;
           mbar_arrive_expect_tx(&bars->q_full, 2 * C::NSUB * box);
+#pragma unroll 1
           for (int t = 0; t < 2; ++t)
             for (int s = 0; s < C::NSUB; ++s)
               tma_load_4d(sQ + t * C::TILE + s * kSub, &mr, &bars->q_full, 64 * s, 0, sg.head,
@@ -492,6 +502,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
       // The table row of the group's first sequence that has all of the shared tokens.
       const Group gr(g, sg.p);
       int rep = -1;
+#pragma unroll 1
       for (int b = gr.s0; rep < 0 && b < gr.s1; b += 32) {
         const bool has = b + lane < gr.s1 &&
                          sched::clamp_len(g.cache_len, b + lane, cap_of(a)) >= gr.len;
@@ -512,6 +523,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
         if (lane == 0) {
           if (keys) {
             uint32_t seen = 0;
+#pragma unroll 1
             for (int i = 0; i < boxes; ++i)
               if (pages >> i & 1u) seen |= bits << (i * (rows / 16));
             bars->seen[n % kSeen] = seen;
@@ -745,84 +757,76 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
       }
       if (!ok) break;
       // ---- the segment's partial results; tiles with the same rows are joined first
-      float l[2][2];
-      bool any[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        any[t] = sg.count(t) > 0;
-        if (any[t] && ok) {
-          ok = mbar_wait_warp(&bars->o_done[t], n_out[t] & 1, abort_flag, a.err, a.wait_ns);
-          ++n_out[t];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          l[t][i] = l_part[t][i];
-          l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 1);
-          l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 2);
-        }
+      const bool two = sg.count(1) > 0, join = !sg.both && two;
+      ok = mbar_wait_warp(&bars->o_done[0], n_out[0] & 1, abort_flag, a.err, a.wait_ns);
+      ++n_out[0];
+      if (ok && two) {
+        ok = mbar_wait_warp(&bars->o_done[1], n_out[1] & 1, abort_flag, a.err, a.wait_ns);
+        ++n_out[1];
       }
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t == 1 && !sg.both) break;
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l_part[t][i] += __shfl_xor_sync(0xffffffffu, l_part[t][i], 1);
+          l_part[t][i] += __shfl_xor_sync(0xffffffffu, l_part[t][i], 2);
+        }
+      float w[2][2] = {{1.f, 1.f}, {0.f, 0.f}};    // of the tiles' rows A and B, where they are joined
+      if (join) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float M = fmaxf(m_run[0][i], m_run[1][i]), use = M == -INFINITY ? 0.f : M;
+          w[0][i] = ex2(m_run[0][i] - use);        // -inf gives 0
+          w[1][i] = ex2(m_run[1][i] - use);
+          m_run[0][i] = M;
+          l_part[0][i] = l_part[0][i] * w[0][i] + l_part[1][i] * w[1][i];
+        }
+      }
+      // One copy of the code for the tiles and their halves, as above.
+#pragma unroll 1
+      for (int th = 0; th < (sg.both ? 2 : 1) * (D / 64); ++th) {
+        const int t = th / (D / 64), half = th % (D / 64);
         // Rows of the tile, and the place of its first; group starts that are not ascending may
         // lead past the end, where nothing is written.
         const int rows = (sg.both ? (t == 0 ? g.seqs : sg.n - g.seqs) : sg.n) * G;
         const long long e0 = sg.entry + t * g.seqs * G;
         const bool wA = rA < rows && e0 + rA < g.s.entries, wB = rB < rows && e0 + rB < g.s.entries;
-        float* outA = g.s.part + (e0 + rA) * D;
-        float* outB = g.s.part + (e0 + rB) * D;
-        const bool join = !sg.both && any[1];
-        float M[2], w[2][2];     // of rows A and B
+        float* outA = g.s.part + (e0 + rA) * D + 64 * half;
+        float* outB = g.s.part + (e0 + rB) * D + 64 * half;
+        uint32_t ov[32];
+        tmem_ld_16x256b_x8_wait(lane_base + 256 + t * 128 + 64 * half, ov);
+        if (join) {
+          uint32_t o1[32];
+          tmem_ld_16x256b_x8_wait(lane_base + 384 + 64 * half, o1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          M[i] = m_run[t][i];
-          w[0][i] = w[1][i] = 1.f;
-          if (join) {
-            M[i] = fmaxf(m_run[0][i], m_run[1][i]);
-            const float use = M[i] == -INFINITY ? 0.f : M[i];
-            w[0][i] = ex2(m_run[0][i] - use);      // -inf gives 0
-            w[1][i] = ex2(m_run[1][i] - use);
+          for (int i = 0; i < 32; ++i)
+            ov[i] = __float_as_uint(__uint_as_float(ov[i]) * w[0][(i >> 1) & 1] +
+                                    __uint_as_float(o1[i]) * w[1][(i >> 1) & 1]);
+        }
+        // Neighbouring threads of a row exchange halves of two column groups: four columns each.
+        const int odd = t4 & 1;
+#pragma unroll
+        for (int cc = 0; cc < 8; cc += 2) {
+          const int col = 8 * (cc + odd) + 4 * (t4 >> 1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {        // row A, row B
+            const uint32_t* u = ov + 4 * cc + 2 * i;
+            const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? u[0] : u[4], 1);
+            const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? u[1] : u[5], 1);
+            const uint4 q = odd ? make_uint4(x, y, u[4], u[5]) : make_uint4(u[0], u[1], x, y);
+            if (i ? wB : wA) *reinterpret_cast<uint4*>((i ? outB : outA) + col) = q;
           }
         }
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          uint32_t ov[32];
-          tmem_ld_16x256b_x8_wait(lane_base + 256 + t * 128 + 64 * half, ov);
-          if (join) {
-            uint32_t o1[32];
-            tmem_ld_16x256b_x8_wait(lane_base + 384 + 64 * half, o1);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              ov[i] = __float_as_uint(__uint_as_float(ov[i]) * w[0][(i >> 1) & 1] +
-                                      __uint_as_float(o1[i]) * w[1][(i >> 1) & 1]);
-          }
-          // Neighbouring threads of a row exchange halves of two column groups: four columns each.
-#pragma unroll
-          for (int cc = 0; cc < 8; cc += 2) {
-            const int odd = t4 & 1, col = 64 * half + 8 * (cc + odd) + 4 * (t4 >> 1);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {        // row A, row B
-              const uint32_t* u = ov + 4 * cc + 2 * i;
-              const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? u[0] : u[4], 1);
-              const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? u[1] : u[5], 1);
-              const uint4 q = odd ? make_uint4(x, y, u[4], u[5]) : make_uint4(u[0], u[1], x, y);
-              if (i ? wB : wA) *reinterpret_cast<uint4*>((i ? outB : outA) + col) = q;
-            }
-          }
-        }
-        if (t4 == 0) {
-          const float lA = join ? l[0][0] * w[0][0] + l[1][0] * w[1][0] : l[t][0];
-          const float lB = join ? l[0][1] * w[0][1] + l[1][1] * w[1][1] : l[t][1];
-          if (wA) g.s.stats[e0 + rA] = make_float2(M[0], lA);
-          if (wB) g.s.stats[e0 + rB] = make_float2(M[1], lB);
+        if (t4 == 0 && half == 0) {
+          if (wA) g.s.stats[e0 + rA] = make_float2(t ? m_run[1][0] : m_run[0][0], t ? l_part[1][0] : l_part[0][0]);
+          if (wB) g.s.stats[e0 + rB] = make_float2(t ? m_run[1][1] : m_run[0][1], t ? l_part[1][1] : l_part[0][1]);
         }
       }
       tc_fence_before();
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (any[t]) mbar_arrive(&bars->o_empty[t]);
+      mbar_arrive(&bars->o_empty[0]);
+      if (two) mbar_arrive(&bars->o_empty[1]);
     }
   }
 }
@@ -904,10 +908,10 @@ decode_shared_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
   }
 }
 
-// Joins a row's partial results; o = 0, lse = -inf for an empty sequence.  W warps (1 or 4) per
+// Joins a row's partial results; o = 0, lse = -inf for an empty sequence.  W warps (1, 2 or 4) per
 // (sequence, query head), each with every W-th part.
 template <int D, int W>
-__global__ void __launch_bounds__(256) decode_shared_combine_kernel(
+__global__ void __launch_bounds__(256, 4) decode_shared_combine_kernel(
     const __grid_constant__ SharedArgs g) {
   constexpr int PS = TC<D>::PSTRIDE, PER = D / 32;
   __shared__ float red[8][D + 2];                // a warp's columns, maximum and sum
@@ -1032,6 +1036,14 @@ __global__ void __launch_bounds__(256) decode_shared_combine_kernel(
   if (lane == 0) a.lse[row] = lsum == 0.f ? -INFINITY : (M + __log2f(lsum)) * kLn2;
 }
 
+template <int D, int W>
+cudaError_t launch_combine(const SharedArgs& g, long long rows, cudaStream_t s) {
+  constexpr int kEach = 8 / W;
+  return launch_dependent(decode_shared_combine_kernel<D, W>,
+                          dim3(static_cast<unsigned>((rows + kEach - 1) / kEach)), dim3(256), 0, s,
+                          g);
+}
+
 template <int D, int GP>
 cudaError_t launch_g(const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
                      const CUtensorMap& mr, const SharedArgs& g, int workers, cudaStream_t s) {
@@ -1054,12 +1066,12 @@ cudaError_t launch_g(const CUtensorMap& mk, const CUtensorMap& mv, const CUtenso
   cfg.stream = s;
   cudaError_t e = cudaLaunchKernelEx(&cfg, decode_shared_kernel<D, GP>, mk, mv, mq, mr, g);
   if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(g.a.B) * g.a.Hq;
-  if (rows <= 4096)
-    return launch_dependent(decode_shared_combine_kernel<D, 4>,
-                            dim3(static_cast<unsigned>((rows + 1) / 2)), dim3(256), 0, s, g);
-  return launch_dependent(decode_shared_combine_kernel<D, 1>,
-                          dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, g);
+  // As many warps a row as are resident at once (four blocks an SM): 64 sequences of 32 heads, 8192 +
+  // 512 tokens, with two waves of blocks 1.5 us more.
+  const long long rows = static_cast<long long>(g.a.B) * g.a.Hq, most = 32ll * sm_count();
+  if (4 * rows <= most) return launch_combine<D, 4>(g, rows, s);
+  if (2 * rows <= most) return launch_combine<D, 2>(g, rows, s);
+  return launch_combine<D, 1>(g, rows, s);
 }
 
 template <int D>

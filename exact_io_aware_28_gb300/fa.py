@@ -580,7 +580,7 @@ def _same_gpu(stream, *ts) -> int:
                 raise ValueError("the library takes CUDA tensors (device memory); got a "
                                  f"{bad.device.type} tensor")
             raise ValueError(f"tensors on {ts[0].device} and {t.device}: one device a call")
-    if here != torch.cuda.current_device():
+    if here != torch._C._cuda_getDevice():     # the tensors are there: CUDA is initialised
         raise ValueError(f"tensors on {ts[0].device}, but the current device is cuda:"
                          f"{torch.cuda.current_device()}: enter torch.cuda.device(...) for them")
     if stream is None:
@@ -794,11 +794,8 @@ def alloc_decode_shared_workspace(B: int, Hq: int, Hkv: int, d: int, device="cud
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def fa_decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, o, lse, workspace,
-                     scale=None, stream=None) -> None:
-    """fa_decode_paged for groups of sequences with a prefix in common: group p are the sequences
-    group_start[p] .. group_start[p + 1] - 1 (int32 [groups + 1]), whose first shared_len[p] tokens
-    (int32 [groups]) are in the same pages."""
+def _shared_inputs(q, k, v, block_table, cache_len, group_start, shared_len):
+    """Checks; returns what fa_decode_shared is called with, in its order, but for the outputs."""
     heads, pool = q.shape, k.shape
     if len(heads) != 3 or len(pool) != 4 or pool[3] != heads[2]:
         raise ValueError("q must be [B, Hq, d] and k [num_pages, Hkv, page_size, d]; got "
@@ -814,19 +811,31 @@ def fa_decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, o
     _shaped("cache_len", cache_len, (B,), torch.int32)
     _shaped("shared_len", shared_len, (groups,), torch.int32)
     _shaped("group_start", group_start, (groups + 1,), torch.int32)
-    _shaped("o", o, heads, torch.bfloat16)
-    _shaped("lse", lse, (B, Hq), torch.float32)
-    _scratch(workspace)
-    handle = _same_gpu(stream, q, k, v, block_table, cache_len, group_start, shared_len, o, lse,
-                       workspace)
-    st = load().fa_decode_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), kp,
-                                 block_table.data_ptr(), stride, block_table.shape[1],
-                                 cache_len.data_ptr(), group_start.data_ptr(),
-                                 shared_len.data_ptr(), groups, o.data_ptr(), lse.data_ptr(), B,
-                                 Hq, Hkv, P, page, d, 1.0 / d ** 0.5 if scale is None else scale,
+    return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), kp, block_table.data_ptr(), stride,
+             block_table.shape[1], cache_len.data_ptr(), group_start.data_ptr(),
+             shared_len.data_ptr(), groups), (B, Hq, Hkv, P, page, d))
+
+
+def _shared_call(ins, sizes, o, lse, workspace, scale, handle):
+    st = load().fa_decode_shared(*ins, o.data_ptr(), lse.data_ptr(), *sizes,
+                                 1.0 / sizes[5] ** 0.5 if scale is None else scale,
                                  workspace.data_ptr(), workspace.nbytes, handle)
     if st != FA_OK:
         raise FaError(st, "fa_decode_shared")
+
+
+def fa_decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, o, lse, workspace,
+                     scale=None, stream=None) -> None:
+    """fa_decode_paged for groups of sequences with a prefix in common: group p are the sequences
+    group_start[p] .. group_start[p + 1] - 1 (int32 [groups + 1]), whose first shared_len[p] tokens
+    (int32 [groups]) are in the same pages."""
+    ins, sizes = _shared_inputs(q, k, v, block_table, cache_len, group_start, shared_len)
+    _shaped("o", o, q.shape, torch.bfloat16)
+    _shaped("lse", lse, sizes[:2], torch.float32)
+    _scratch(workspace)
+    handle = _same_gpu(stream, q, k, v, block_table, cache_len, group_start, shared_len, o, lse,
+                       workspace)
+    _shared_call(ins, sizes, o, lse, workspace, scale, handle)
 
 
 def decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, scale=None,
@@ -835,40 +844,50 @@ def decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, scal
     if stream is not None:
         return _on_stream(stream, decode_shared, q, k, v, block_table, cache_len, group_start,
                           shared_len, scale, workspace)
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    ins, sizes = _shared_inputs(q, k, v, block_table, cache_len, group_start, shared_len)
     if workspace is None:
-        workspace = alloc_decode_shared_workspace(*q.shape[:2], k.shape[1], q.shape[2], q.device)
-    fa_decode_shared(q, k, v, block_table, cache_len, group_start, shared_len, o, lse, workspace,
-                     scale)
+        handle = _same_gpu(None, q, k, v, block_table, cache_len, group_start, shared_len)
+        workspace = alloc_decode_shared_workspace(*sizes[:3], sizes[5], q.device)
+    else:
+        _scratch(workspace)
+        handle = _same_gpu(None, q, k, v, block_table, cache_len, group_start, shared_len,
+                           workspace)
+    o = torch.empty_like(q)
+    lse = torch.empty(sizes[:2], dtype=torch.float32, device=q.device)
+    _shared_call(ins, sizes, o, lse, workspace, scale, handle)
     return o, lse
 
 
 # ----------------------------------------------------------- pages
+
+def _i32(name, t, n):
+    """``t`` is dense int32 [n]; its address."""
+    if t.dtype is torch.int32 and t.shape == (n,) and t.is_contiguous():
+        return t.data_ptr()
+    return _shaped(name, t, (n,), torch.int32)     # raises
+
+
+def _call(name, *args):
+    st = getattr(load(), name)(*args)
+    if st != FA_OK:
+        raise FaError(st, name)
+
 
 def fa_paged_fork(cache_len, block_table, free_pages, src, dst, copy_src, copy_dst, copy_rows,
                   pages_taken, page_size: int, num_pages: int, stream=None) -> None:
     """Requests dst[i] become copies of src[i] (int32 tensors throughout): cache_len [B] and
     block_table [B, max_pages] in and out, free_pages [F] in; out: what fa_paged_copy is to copy,
     copy_src, copy_dst, copy_rows [n], and pages_taken [1]."""
-    B, i32 = cache_len.numel(), torch.int32
-    F, n = free_pages.numel(), src.numel()
-    _shaped("cache_len", cache_len, (B,), i32)
-    _shaped("free_pages", free_pages, (F,), i32)
-    for name, t in (("src", src), ("dst", dst), ("copy_src", copy_src), ("copy_dst", copy_dst),
-                    ("copy_rows", copy_rows)):
-        _shaped(name, t, (n,), i32)
-    _shaped("pages_taken", pages_taken, (1,), i32)
+    B, F, n = cache_len.numel(), free_pages.numel(), src.numel()
+    lens, free = _i32("cache_len", cache_len, B), _i32("free_pages", free_pages, F)
+    pairs = _i32("src", src, n), _i32("dst", dst, n)
+    outs = (_i32("copy_src", copy_src, n), _i32("copy_dst", copy_dst, n),
+            _i32("copy_rows", copy_rows, n), _i32("pages_taken", pages_taken, 1))
     stride = _table(block_table, B)
     handle = _same_gpu(stream, cache_len, block_table, free_pages, src, dst, copy_src, copy_dst,
                        copy_rows, pages_taken)
-    st = load().fa_paged_fork(cache_len.data_ptr(), block_table.data_ptr(), stride,
-                              block_table.shape[1], free_pages.data_ptr(), F, src.data_ptr(),
-                              dst.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
-                              copy_rows.data_ptr(), pages_taken.data_ptr(), B, page_size,
-                              num_pages, handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_paged_fork")
+    _call("fa_paged_fork", lens, block_table.data_ptr(), stride, block_table.shape[1], free, F,
+          *pairs, n, *outs, B, page_size, num_pages, handle)
 
 
 def paged_fork(cache_len, block_table, free_pages, src, dst, page_size: int, num_pages: int,
@@ -878,32 +897,30 @@ def paged_fork(cache_len, block_table, free_pages, src, dst, page_size: int, num
     if stream is not None:
         return _on_stream(stream, paged_fork, cache_len, block_table, free_pages, src, dst,
                           page_size, num_pages)
-    n = src.numel()
-    buf = torch.empty(3 * n + 1, dtype=torch.int32, device=cache_len.device)
-    frm, to, rows, taken = buf.split((n, n, n, 1))
-    fa_paged_fork(cache_len, block_table, free_pages, src, dst, frm, to, rows, taken, page_size,
-                  num_pages)
-    return frm, to, rows, taken
+    B, F, n = cache_len.numel(), free_pages.numel(), src.numel()
+    lens, free = _i32("cache_len", cache_len, B), _i32("free_pages", free_pages, F)
+    pairs = _i32("src", src, n), _i32("dst", dst, n)
+    stride = _table(block_table, B)
+    handle = _same_gpu(None, cache_len, block_table, free_pages, src, dst)
+    buf = src.new_empty(3 * n + 1)
+    at = buf.data_ptr()
+    _call("fa_paged_fork", lens, block_table.data_ptr(), stride, block_table.shape[1], free, F,
+          *pairs, n, at, at + 4 * n, at + 8 * n, at + 12 * n, B, page_size, num_pages, handle)
+    return buf.split_with_sizes((n, n, n, 1))
 
 
 def fa_paged_free(cache_len, block_table, rows, refs, free_pages, n_free, page_size: int,
                   num_pages: int, stream=None) -> None:
     """Requests rows [n] end (int32 tensors throughout): cache_len [B] and block_table
     [B, max_pages] in and out; out: refs and free_pages [num_pages], n_free [1]."""
-    B, n, i32 = cache_len.numel(), rows.numel(), torch.int32
-    _shaped("cache_len", cache_len, (B,), i32)
-    _shaped("rows", rows, (n,), i32)
-    _shaped("refs", refs, (num_pages,), i32)
-    _shaped("free_pages", free_pages, (num_pages,), i32)
-    _shaped("n_free", n_free, (1,), i32)
+    B, n = cache_len.numel(), rows.numel()
+    lens, ended = _i32("cache_len", cache_len, B), _i32("rows", rows, n)
+    outs = (_i32("refs", refs, num_pages), _i32("free_pages", free_pages, num_pages),
+            _i32("n_free", n_free, 1))
     stride = _table(block_table, B)
     handle = _same_gpu(stream, cache_len, block_table, rows, refs, free_pages, n_free)
-    st = load().fa_paged_free(cache_len.data_ptr(), block_table.data_ptr(), stride,
-                              block_table.shape[1], rows.data_ptr(), n, refs.data_ptr(),
-                              free_pages.data_ptr(), n_free.data_ptr(), B, page_size, num_pages,
-                              handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_paged_free")
+    _call("fa_paged_free", lens, block_table.data_ptr(), stride, block_table.shape[1], ended, n,
+          *outs, B, page_size, num_pages, handle)
 
 
 def paged_free(cache_len, block_table, rows, page_size: int, num_pages: int, stream=None):
@@ -911,10 +928,15 @@ def paged_free(cache_len, block_table, rows, page_size: int, num_pages: int, str
     Returns (refs, free_pages, n_free)."""
     if stream is not None:
         return _on_stream(stream, paged_free, cache_len, block_table, rows, page_size, num_pages)
-    buf = torch.empty(2 * num_pages + 1, dtype=torch.int32, device=cache_len.device)
-    refs, free, count = buf.split((num_pages, num_pages, 1))
-    fa_paged_free(cache_len, block_table, rows, refs, free, count, page_size, num_pages)
-    return refs, free, count
+    B, n = cache_len.numel(), rows.numel()
+    lens, ended = _i32("cache_len", cache_len, B), _i32("rows", rows, n)
+    stride = _table(block_table, B)
+    handle = _same_gpu(None, cache_len, block_table, rows)
+    buf = cache_len.new_empty(2 * num_pages + 1)
+    at = buf.data_ptr()
+    _call("fa_paged_free", lens, block_table.data_ptr(), stride, block_table.shape[1], ended, n, at,
+          at + 4 * num_pages, at + 8 * num_pages, B, page_size, num_pages, handle)
+    return buf.split_with_sizes((num_pages, num_pages, 1))
 
 
 def fa_paged_compact(cache_len, block_table, moved, copy_src, copy_dst, n_used, page_size: int,
@@ -922,20 +944,13 @@ def fa_paged_compact(cache_len, block_table, moved, copy_src, copy_dst, n_used, 
     """The pages in use move to the front of the pool (int32 tensors throughout): cache_len [B] in,
     block_table [B, max_pages] in and out; out: moved [num_pages], copy_src and copy_dst (at least
     num_pages / 2 each), n_used [1]."""
-    B, n, i32 = cache_len.numel(), copy_src.numel(), torch.int32
-    _shaped("cache_len", cache_len, (B,), i32)
-    _shaped("moved", moved, (num_pages,), i32)
-    _shaped("copy_src", copy_src, (n,), i32)
-    _shaped("copy_dst", copy_dst, (n,), i32)
-    _shaped("n_used", n_used, (1,), i32)
-    stride = _table(block_table, B)
+    B, n = cache_len.numel(), copy_src.numel()
+    lens, new = _i32("cache_len", cache_len, B), _i32("moved", moved, num_pages)
+    frm, to = _i32("copy_src", copy_src, n), _i32("copy_dst", copy_dst, n)
+    used, stride = _i32("n_used", n_used, 1), _table(block_table, B)
     handle = _same_gpu(stream, cache_len, block_table, moved, copy_src, copy_dst, n_used)
-    st = load().fa_paged_compact(cache_len.data_ptr(), block_table.data_ptr(), stride,
-                                 block_table.shape[1], moved.data_ptr(), copy_src.data_ptr(),
-                                 copy_dst.data_ptr(), n, n_used.data_ptr(), B, page_size,
-                                 num_pages, handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_paged_compact")
+    _call("fa_paged_compact", lens, block_table.data_ptr(), stride, block_table.shape[1], new, frm,
+          to, n, used, B, page_size, num_pages, handle)
 
 
 def paged_compact(cache_len, block_table, page_size: int, num_pages: int, stream=None):
@@ -943,11 +958,14 @@ def paged_compact(cache_len, block_table, page_size: int, num_pages: int, stream
     Returns (moved, copy_src, copy_dst, n_used), the copies for paged_copy."""
     if stream is not None:
         return _on_stream(stream, paged_compact, cache_len, block_table, page_size, num_pages)
-    n = max(1, num_pages // 2)
-    buf = torch.empty(num_pages + 2 * n + 1, dtype=torch.int32, device=cache_len.device)
-    moved, frm, to, used = buf.split((num_pages, n, n, 1))
-    fa_paged_compact(cache_len, block_table, moved, frm, to, used, page_size, num_pages)
-    return moved, frm, to, used
+    B, n = cache_len.numel(), max(1, num_pages // 2)
+    lens, stride = _i32("cache_len", cache_len, B), _table(block_table, B)
+    handle = _same_gpu(None, cache_len, block_table)
+    buf = cache_len.new_empty(num_pages + 2 * n + 1)
+    at, lists = buf.data_ptr(), buf.data_ptr() + 4 * num_pages
+    _call("fa_paged_compact", lens, block_table.data_ptr(), stride, block_table.shape[1], at, lists,
+          lists + 4 * n, n, lists + 8 * n, B, page_size, num_pages, handle)
+    return buf.split_with_sizes((num_pages, n, n, 1))
 
 
 def fa_paged_copy(k_cache, v_cache, copy_src, copy_dst, copy_rows=None, stream=None) -> None:
@@ -964,16 +982,11 @@ def fa_paged_copy(k_cache, v_cache, copy_src, copy_dst, copy_rows=None, stream=N
                          f"{list(pool)}")
     if v_cache is not None and _rows("v_cache", v_cache, pool) != stride:
         raise ValueError("k_cache and v_cache must have the same stride between pages")
-    _shaped("copy_src", copy_src, (n,), torch.int32)
-    _shaped("copy_dst", copy_dst, (n,), torch.int32)
-    if copy_rows is not None:
-        _shaped("copy_rows", copy_rows, (n,), torch.int32)
+    frm, to = _i32("copy_src", copy_src, n), _i32("copy_dst", copy_dst, n)
+    rows = None if copy_rows is None else _i32("copy_rows", copy_rows, n)
     handle = _same_gpu(stream, *_given(k_cache, v_cache, copy_src, copy_dst, copy_rows))
-    st = load().fa_paged_copy(k_cache.data_ptr(), _at(v_cache), stride, copy_src.data_ptr(),
-                              copy_dst.data_ptr(), _at(copy_rows), n, pool[0], heads, pool[-2],
-                              pool[-1], handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_paged_copy")
+    _call("fa_paged_copy", k_cache.data_ptr(), _at(v_cache), stride, frm, to, rows, n, pool[0],
+          heads, pool[-2], pool[-1], handle)
 
 
 def paged_copy(k_cache, v_cache, copy_src, copy_dst, copy_rows=None, stream=None) -> None:
@@ -1020,53 +1033,57 @@ def _plan(table):
     return turns, axis, 2 * pairs
 
 
-def fa_rope(x, y, pos, table, interleaved: bool = False, inverse: bool = False,
-            stream=None) -> None:
-    """Rows of x [B, H, N, d] (bf16 or fp32; any strides, rows dense) turned into y by their
-    positions pos int32 [axes, B, N]; ``table`` as of rope_table.  y may be x."""
+def _rope(x, y, pos, table, interleaved, inverse, stream):
+    """fa_rope; y None: into a new tensor, which is returned."""
     shape = x.shape
     if len(shape) != 4:
         raise ValueError(f"x must be [B, H, N, d], not {list(shape)}")
     B, H, N, d = shape
-    code = _dtype_code(x)
-    if y.shape != shape or y.dtype != x.dtype:
-        raise ValueError(f"y must be {list(shape)} of {x.dtype}, as x is")
-    xs, ys, ps = x.stride(), y.stride(), pos.stride()
-    if d > 1 and (xs[3] != 1 or ys[3] != 1):
-        raise ValueError("rows of x and y must be dense")
+    code, xs, ps = _dtype_code(x), x.stride(), pos.stride()
+    if d > 1 and xs[3] != 1:
+        raise ValueError("rows of x must be dense")
     if pos.dtype is not torch.int32:
         raise TypeError("pos must be torch.int32")
     if pos.dim() != 3 or pos.shape[1:] != (B, N) or (N > 1 and ps[2] != 1):
         raise ValueError(f"pos must be [axes, {B}, {N}], dense along the last, not "
                          f"{list(pos.shape)}")
     turns, axis, rot = _plan(table)
-    handle = _same_gpu(stream, x, y, pos, turns, axis)
-    st = load().fa_rope(x.data_ptr(), y.data_ptr(), xs[0], xs[1], xs[2], ys[0], ys[1], ys[2],
-                        pos.data_ptr(), ps[0], ps[1], pos.shape[0], turns.data_ptr(),
-                        axis.data_ptr(), B, H, N, d, rot, int(interleaved), int(inverse), code,
-                        handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_rope")
+    if y is None:
+        handle = _same_gpu(stream, x, pos, turns, axis)
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        ys = (H * N * d, N * d, d)
+    else:
+        ys = y.stride()
+        if y.shape != shape or y.dtype != x.dtype:
+            raise ValueError(f"y must be {list(shape)} of {x.dtype}, as x is")
+        if d > 1 and ys[3] != 1:
+            raise ValueError("rows of y must be dense")
+        handle = _same_gpu(stream, x, y, pos, turns, axis)
+    _call("fa_rope", x.data_ptr(), y.data_ptr(), *xs[:3], *ys[:3], pos.data_ptr(), ps[0], ps[1],
+          pos.shape[0], turns.data_ptr(), axis.data_ptr(), B, H, N, d, rot, int(interleaved), int(inverse),
+          code, handle)
+    return y
+
+
+def fa_rope(x, y, pos, table, interleaved: bool = False, inverse: bool = False,
+            stream=None) -> None:
+    """Rows of x [B, H, N, d] (bf16 or fp32; any strides, rows dense) turned into y by their
+    positions pos int32 [axes, B, N]; ``table`` as of rope_table.  y may be x."""
+    _rope(x, y, pos, table, interleaved, inverse, stream)
 
 
 def rope(x, pos, table, interleaved: bool = False, out=None, stream=None):
     """Rotary positions: x [B, H, N, d] turned, into ``out`` (which may be x) or a new tensor."""
     if stream is not None:
         return _on_stream(stream, rope, x, pos, table, interleaved, out)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    fa_rope(x, out, pos, table, interleaved)
-    return out
+    return _rope(x, out, pos, table, interleaved, False, None)
 
 
 def rope_backward(dy, pos, table, interleaved: bool = False, out=None, stream=None):
     """The gradient of rope: dy turned back, into ``out`` (which may be dy) or a new tensor."""
     if stream is not None:
         return _on_stream(stream, rope_backward, dy, pos, table, interleaved, out)
-    if out is None:
-        out = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-    fa_rope(dy, out, pos, table, interleaved, True)
-    return out
+    return _rope(dy, out, pos, table, interleaved, True, None)
 
 
 def fa_rope_append(q, k, v, pos, table, q_out, k_cache, v_cache, slots, interleaved: bool = False,
@@ -1085,20 +1102,17 @@ def fa_rope_append(q, k, v, pos, table, q_out, k_cache, v_cache, slots, interlea
     qo, kp = _rows("q_out", q_out, heads), _rows("k_cache", k_cache, pool)
     if kp != _rows("v_cache", v_cache, pool):
         raise ValueError("k_cache and v_cache must have the same stride between pages")
-    _shaped("slots", slots, (T,), torch.int32)
+    slot = _i32("slots", slots, T)
     if pos.dtype is not torch.int32:
         raise TypeError("pos must be torch.int32")
     if pos.dim() != 2 or pos.shape[1] != T or (T > 1 and pos.stride(1) != 1):
         raise ValueError(f"pos must be [axes, {T}], dense along the last, not {list(pos.shape)}")
     turns, axis, rot = _plan(table)
     handle = _same_gpu(stream, q, k, v, pos, turns, axis, q_out, k_cache, v_cache, slots)
-    st = load().fa_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
-                               q_out.data_ptr(), qo, k_cache.data_ptr(), v_cache.data_ptr(), kp,
-                               slots.data_ptr(), pos.data_ptr(), pos.stride(0), pos.shape[0],
-                               turns.data_ptr(), axis.data_ptr(), T, heads[1], Hkv, pool[0],
-                               pool[2], d, rot, int(interleaved), handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_rope_append")
+    _call("fa_rope_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, q_out.data_ptr(),
+          qo, k_cache.data_ptr(), v_cache.data_ptr(), kp, slot, pos.data_ptr(), pos.stride(0),
+          pos.shape[0], turns.data_ptr(), axis.data_ptr(), T, heads[1], Hkv, pool[0], pool[2], d,
+          rot, int(interleaved), handle)
 
 
 def rope_append(q, k, v, pos, table, k_cache, v_cache, slots, interleaved: bool = False, out=None,
