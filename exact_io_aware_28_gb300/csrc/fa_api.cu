@@ -862,6 +862,9 @@ fa_status fa_decode_shared(const void* q, const void* k, const void* v, long lon
       bad4(cache_len) || bad4(group_start) || bad4(shared_len) || groups < 1 || groups > B ||
       bad_softmax_scale(scale))
     return FA_ERR_INVALID_ARG;
+  // tiles of 128 tokens are counted in 32 bits
+  if ((long long)B * Hkv * (((long long)max_pages * page_size + 127) / 128) >= (1ll << 29))
+    return FA_ERR_UNSUPPORTED;
   const size_t need = fa_decode_shared_workspace_bytes(B, Hq, Hkv, d);
   if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
   const long long rows = (long long)B * Hq;

@@ -83,25 +83,25 @@ struct SharedArgs {
   // the stores of a piece's 256 rows stall on any other.
   float* part;
   float2* stats;
-  long long entries;
+  int entries;
   struct Row* rows;            // [B], for the combine kernel
   struct Line* line;
-  long long* tiles_g;          // [groups], tiles before each group
+  int* tiles_g;                // [groups], tiles before each group
 };
 
 // What the combine kernel needs to know of a sequence: where on the line its own tiles and its
 // piece's begin (head 0), and the places of its partial results.
 struct Row {
-  long long own, pre;
-  long long pre_head;          // from a head's tiles of the piece to the next head's
-  long long entry;             // place of the row of head 0 in the prefixes' results
+  int own, pre;
+  int pre_head;                // from a head's tiles of the piece to the next head's
+  int entry;                   // place of the row of head 0 in the prefixes' results
   int n;                       // own tiles of a head
   int span;                    // from the piece's first tile to its last; -1: nothing shared
   int entry_head;              // from one head's places to the next one's
   int pad;
 };
 struct Line {
-  long long total[2];          // tiles of the prefixes, of the continuations
+  int total[2];                // tiles of the prefixes, of the continuations
   int workers[2];              // that have a range
 };
 
@@ -133,24 +133,20 @@ struct Plan {
   }
 };
 
-// x / n; 32 bits are enough but for huge batches.
-__device__ __forceinline__ int quotient(long long x, int n) {
-  if (x < (1ll << 31)) return static_cast<int>(x) / n;
-  return static_cast<int>(x / n);
+// floor(total w / workers) and the worker whose range holds x, in 32 bits: with total = q workers + r
+// the first is q w + floor(r w / workers), workers being SMs (r w fits); the second is a quotient in
+// fp32, off by one at most.
+__device__ __forceinline__ int range_start(int total, int w, int workers) {
+  const int q = total / workers;
+  return q * w + (total - q * workers) * w / workers;
 }
-
-// sched::range_start and sched::owner, by a division of 32 bits where that is enough (workers are SMs,
-// fewer than 512).
-__device__ __forceinline__ long long range_start(long long total, int w, int workers) {
-  if (total < (1 << 23)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(w) /
-                                  static_cast<uint32_t>(workers);
-  return sched::range_start(total, w, workers);
-}
-__device__ __forceinline__ int owner(long long x, long long total, int workers) {
-  if (total < (1 << 23))
-    return (static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(workers) - 1u) /
-           static_cast<uint32_t>(total);
-  return sched::owner(x, total, workers);
+__device__ __forceinline__ int owner(int x, int total, int workers) {
+  int w = static_cast<int>(static_cast<float>(x) * static_cast<float>(workers) /
+                           static_cast<float>(total));
+  w = min(w, workers - 1);
+  if (range_start(total, w, workers) > x) --w;
+  else if (w + 1 < workers && range_start(total, w + 1, workers) <= x) ++w;
+  return w;
 }
 
 // What a tile costs, in some 0.3 us: a prefix's with rows for both row tiles, for one; a
@@ -178,8 +174,8 @@ struct Group {
     cost = s1 - s0 > g.seqs ? kCostBoth : kCostOne;
   }
   // Its tiles of all heads and pieces.
-  __device__ __forceinline__ long long all(const Plan& g) const {
-    return static_cast<long long>(tiles) * g.a.Hkv * supers;
+  __device__ __forceinline__ int all(const Plan& g) const {
+    return tiles * g.a.Hkv * supers;
   }
 };
 
@@ -202,9 +198,9 @@ __device__ __forceinline__ int shared_of(const Plan& g, const Group& p, int b, i
 struct SharedStart {
   int mine;                    // 0: the CTA works on prefixes, 1: on continuations
   int w;                       // which of their workers it is
-  long long first, last;       // its range of their tiles
+  int first, last;             // its range of their tiles
   int p, b, pb;                // group of the first tile; sequence of the first tile, and its group
-  long long before;            // tiles before that group or sequence
+  int before;                  // tiles before that group or sequence
 };
 
 // How many of W workers go to the prefixes: so many, n, that both kinds end at the same time,
@@ -213,19 +209,19 @@ struct SharedStart {
 // 2 i + 1) do the same: with one on a prefix and one on continuations both take up to twice as long
 // (16 groups of 4 sequences, 2048 + 128 tokens, so mixed throughout: 81 us against 47; the cause is
 // not known).
-__device__ __forceinline__ int prefix_workers(int W, long long tiles_g, long long tiles_b,
-                                              float cost_g, float cost_b) {
+__device__ __forceinline__ int prefix_workers(int W, int tiles_g, int tiles_b, float cost_g,
+                                              float cost_b) {
   if (tiles_g == 0 || tiles_b == 0) return tiles_g == 0 ? 0 : W;
   if (tiles_g + tiles_b <= W) return static_cast<int>(tiles_g);
   const float D = kCostPrefixMore, p = D * W - cost_g - cost_b;
-  long long n = static_cast<long long>((p + sqrtf(p * p + 4.f * D * cost_g * W)) / (2.f * D) + 0.5f);
+  int n = static_cast<int>((p + sqrtf(p * p + 4.f * D * cost_g * W)) / (2.f * D) + 0.5f);
   n += 2 * n <= W ? n & 1 : -(n & 1);
   n = max(min(n, tiles_g), W - tiles_b);
-  return static_cast<int>(max(1ll, min(W - 1ll, n)));
+  return max(1, min(W - 1, n));
 }
 
 struct Sums {
-  long long tiles[2];
+  int tiles[2];
   float cost[2];
 };
 
@@ -244,7 +240,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
     const Group gr(g, *p);
     return sched::granules<kKeys>(L - shared_of(g, gr, b, L));
   };
-  long long sum[2] = {0, 0};
+  int sum[2] = {0, 0};
   float cost[2] = {0.f, 0.f};
 #pragma unroll 1
   for (int p = p0; p < p1; ++p) {
@@ -259,16 +255,16 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int n = own_tiles(b, &p);
-      sum[1] += static_cast<long long>(n) * g.a.Hkv;
+      sum[1] += n * g.a.Hkv;
       if (n > 0) cost[1] += static_cast<float>(n * kCostOwn + kCostOwnPair) * g.a.Hkv;
     }
   }
-  long long incl[2] = {sum[0], sum[1]};
+  int incl[2] = {sum[0], sum[1]};
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl[i], off);
+      const int up = __shfl_up_sync(0xffffffffu, incl[i], off);
       if (lane >= off) incl[i] += up;
     }
 #pragma unroll
@@ -278,26 +274,29 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
   }
   if (lane == 31) scratch[warp] = Sums{{incl[0], incl[1]}, {cost[0], cost[1]}};
   __syncthreads();
-  long long before[2] = {incl[0] - sum[0], incl[1] - sum[1]}, total[2] = {0, 0};
+  int before[2] = {incl[0] - sum[0], incl[1] - sum[1]}, total[2] = {0, 0};
   cost[0] = cost[1] = 0.f;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const long long v = scratch[i].tiles[j];
+      const int v = scratch[i].tiles[j];
       if (i < warp) before[j] += v;
       total[j] += v;
       cost[j] += scratch[i].cost[j];
     }
   }
+  // Group starts that are not ascending can name more tiles than 32 bits hold: nothing is done then
+  // (with ascending ones the cost is below 6 + 4 times 2^29).
+  if (cost[0] > 7e9f) total[0] = total[1] = 0;
   const int share = prefix_workers(gridDim.x, total[0], total[1], cost[0], cost[1]);
   const int W0 = sched::active(total[0], share);
   const int W1 = sched::active(total[1], static_cast<int>(gridDim.x) - share);
   const int block = blockIdx.x, mine = block < share ? 0 : 1, w = block - (mine ? share : 0);
   const int W = mine ? W1 : W0;
-  const long long all = mine ? total[1] : total[0];
+  const int all = mine ? total[1] : total[0];
   const bool works = w < W;
-  const long long first = works ? range_start(all, w, W) : 0;
+  const int first = works ? range_start(all, w, W) : 0;
   if (tid == 0) {
     out->mine = mine;
     out->w = w;
@@ -305,11 +304,11 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
     out->last = works ? range_start(all, w + 1, W) : 0;
   }
   const bool write = block == 0;
-  long long at = before[0];
+  int at = before[0];
   if (write || (works && mine == 0 && first >= at && first < at + sum[0]))
 #pragma unroll 1
     for (int p = p0; p < p1; ++p) {
-      const long long n = p0 + 1 == p1 ? sum[0] : Group(g, p).all(g);
+      const int n = p0 + 1 == p1 ? sum[0] : Group(g, p).all(g);
       if (write) g.s.tiles_g[p] = at;
       if (mine == 0 && first >= at && first < at + n) out->p = p, out->before = at;
       at += n;
@@ -319,7 +318,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
     int p = at0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const long long n = static_cast<long long>(own_tiles(b, &p)) * g.a.Hkv;
+      const int n = own_tiles(b, &p) * g.a.Hkv;
       if (first >= at && first < at + n) out->b = b, out->pb = p, out->before = at;
       at += n;
     }
@@ -335,7 +334,7 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
       Row r;
       r.n = own_tiles(b, &p);
       r.own = at;
-      at += static_cast<long long>(r.n) * g.a.Hkv;
+      at += r.n * g.a.Hkv;
       const Group gr(g, p);
       const int L = sched::clamp_len(g.cache_len, b, cap);
       r.span = -1;
@@ -344,9 +343,9 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
       if (shared_of(g, gr, b, L) > 0) {
         const int piece = (b - gr.s0) / (2 * g.seqs);
         r.span = gr.tiles - 1;
-        r.pre = g.s.tiles_g[p] + static_cast<long long>(piece) * gr.tiles;
-        r.pre_head = static_cast<long long>(gr.supers) * gr.tiles;
-        r.entry = static_cast<long long>(gr.s0) * g.a.Hq + static_cast<long long>(b - gr.s0) * G;
+        r.pre = g.s.tiles_g[p] + piece * gr.tiles;
+        r.pre_head = gr.supers * gr.tiles;
+        r.entry = gr.s0 * g.a.Hq + (b - gr.s0) * G;
         r.entry_head = (gr.s1 - gr.s0) * G;
       }
       g.s.rows[b] = r;
@@ -359,7 +358,7 @@ struct PSegment {
   int p, head, k0, k1;
   int s0, n;                   // the piece's sequences
   bool both;                   // it has rows for both tiles
-  long long entry;             // place of its first partial result
+  int entry;                   // place of its first partial result
   __device__ __forceinline__ int blocks() const { return (k1 - k0 + kKeys - 1) / kKeys; }
   // Does tile t take the segment's key tile j?
   __device__ __forceinline__ bool need(int t, int j) const { return both || (j & 1) == t; }
@@ -370,17 +369,15 @@ struct PSegment {
 };
 
 // Places of a piece's rows before those of its pair's segments of other workers.
-__device__ __forceinline__ long long first_entry(const Plan& g, const Group& p, int head,
-                                                 int piece) {
+__device__ __forceinline__ int first_entry(const Plan& g, const Group& p, int head, int piece) {
   const int G = g.a.Hq / g.a.Hkv;
-  return static_cast<long long>(p.s0) * g.a.Hq + static_cast<long long>(head) * (p.s1 - p.s0) * G +
-         2ll * piece * g.seqs * G;
+  return p.s0 * g.a.Hq + head * (p.s1 - p.s0) * G + 2 * piece * g.seqs * G;
 }
 
 struct PrefixWalk {
   const Plan& g;
   int p, w;
-  long long at, last, before;
+  int at, last, before;
   __device__ __forceinline__ PrefixWalk(const Plan& g_, const SharedStart& s)
       : g(g_), p(s.p), w(s.w), at(s.first), last(s.last), before(s.before) {}
   __device__ __forceinline__ bool next(PSegment& sg) {
@@ -388,12 +385,12 @@ struct PrefixWalk {
 #pragma unroll 1
     for (; p < g.groups; ++p) {
       const Group gr(g, p);
-      const long long all = gr.all(g);
+      const int all = gr.all(g);
       if (at < before + all) {
-        const int pair = quotient(at - before, gr.tiles);
-        const long long pair_start = before + static_cast<long long>(pair) * gr.tiles;
+        const int pair = (at - before) / gr.tiles;
+        const int pair_start = before + pair * gr.tiles;
         const int piece = pair % gr.supers;
-        const int g1 = static_cast<int>(min(static_cast<long long>(gr.tiles), last - pair_start));
+        const int g1 = min(gr.tiles, last - pair_start);
         sg.p = p;
         sg.head = pair / gr.supers;
         sg.k0 = static_cast<int>(at - pair_start) * kKeys;
@@ -401,7 +398,7 @@ struct PrefixWalk {
         sg.s0 = gr.s0 + piece * 2 * g.seqs;
         sg.n = min(2 * g.seqs, gr.s1 - sg.s0);
         sg.both = sg.n > g.seqs;
-        sg.entry = first_entry(g, gr, sg.head, piece) + 2ll * w * g.seqs * (g.a.Hq / g.a.Hkv);
+        sg.entry = first_entry(g, gr, sg.head, piece) + 2 * w * g.seqs * (g.a.Hq / g.a.Hkv);
         at = pair_start + g1;
         return true;
       }
@@ -415,15 +412,15 @@ struct PrefixWalk {
 struct OwnWalk {
   const Plan& g;
   int b, p, w, head, g0;
-  long long left;              // tiles of the worker's range that are still to come
+  int left;                    // tiles of the worker's range that are still to come
   int L, from, n;              // of sequence b: length, first own token, tiles of a head
   __device__ __forceinline__ OwnWalk(const Plan& g_, const SharedStart& s)
       : g(g_), b(s.b), p(s.pb), w(s.w), left(s.last - s.first) {
     if (left <= 0) return;
     sequence();
-    const long long x = s.first - s.before;
-    head = quotient(x, n);                       // find_start has found the sequence that holds it
-    g0 = static_cast<int>(x - static_cast<long long>(head) * n);
+    const int x = s.first - s.before;
+    head = x / n;                                // find_start has found the sequence that holds it
+    g0 = x - head * n;
   }
   __device__ __forceinline__ void sequence() {
 #pragma unroll 1
@@ -440,7 +437,7 @@ struct OwnWalk {
       if (++b >= g.a.B) return false;
       sequence();
     }
-    const int g1 = static_cast<int>(min(static_cast<long long>(n), g0 + left));
+    const int g1 = min(n, g0 + left);
     sg.b = b;
     sg.head = head;
     sg.len = L;
@@ -791,7 +788,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
         // Rows of the tile, and the place of its first; group starts that are not ascending may
         // lead past the end, where nothing is written.
         const int rows = (sg.both ? (t == 0 ? g.seqs : sg.n - g.seqs) : sg.n) * G;
-        const long long e0 = sg.entry + t * g.seqs * G;
+        const int e0 = sg.entry + t * g.seqs * G;
         const bool wA = rA < rows && e0 + rA < g.s.entries, wB = rB < rows && e0 + rB < g.s.entries;
         float* outA = g.s.part + (e0 + rA) * D + 64 * half;
         float* outB = g.s.part + (e0 + rB) * D + 64 * half;
@@ -919,40 +916,39 @@ __global__ void __launch_bounds__(256, 4) decode_shared_combine_kernel(
   griddep_launch_dependents();
   const PagedArgs& a = g.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % W, G = a.Hq / a.Hkv;
-  const long long row = blockIdx.x * static_cast<long long>(8 / W) + warp / W;
-  const bool live = row < static_cast<long long>(a.B) * a.Hq;
+  const int row = blockIdx.x * (8 / W) + warp / W;
+  const bool live = row < a.B * a.Hq;
   const int b = live ? static_cast<int>(row / a.Hq) : 0, hq = live ? static_cast<int>(row % a.Hq) : 0;
   const int head = hq / G, h = hq % G;
   const Line line = *g.line;
   const Row r = g.rows[b];
   int own = 0, pre = 0, step = 0;                // parts of the continuation, of the prefix
   const float* own0 = nullptr;                   // the first ones
-  long long pre0 = 0;
-  if (r.n > 0) {
-    const long long first = r.own + static_cast<long long>(head) * r.n;
+  int pre0 = 0;
+  if (r.n > 0 && line.workers[1] > 0) {
+    const int first = r.own + head * r.n;
     const int w0 = owner(first, line.total[1], line.workers[1]);
     own = owner(first + r.n - 1, line.total[1], line.workers[1]) - w0 + 1;
-    own0 = a.part + ((static_cast<long long>(b) * a.Hkv + head + w0) * G + h) * PS;
+    own0 = a.part + ((b * a.Hkv + head + w0) * G + h) * PS;
   }
-  if (r.span >= 0) {
-    const long long first = r.pre + head * r.pre_head;
+  if (r.span >= 0 && line.workers[0] > 0) {
+    const int first = r.pre + head * r.pre_head;
     const int w0 = owner(first, line.total[0], line.workers[0]);
     pre = owner(first + r.span, line.total[0], line.workers[0]) - w0 + 1;
     step = 2 * g.seqs * G;
-    pre0 = r.entry + static_cast<long long>(head) * r.entry_head + h +
-           static_cast<long long>(w0) * step;
-    pre = static_cast<int>(min(static_cast<long long>(pre), (g.entries - 1 - pre0) / step + 1));
+    pre0 = r.entry + head * r.entry_head + h + w0 * step;
+    pre = min(pre, (g.entries - 1 - pre0) / step + 1);
   }
   // A continuation that is all of its rows' keys and one CTA's is finished; W > 1: the block goes on
   // to its barrier.
   const bool todo = live && !(r.span < 0 && own == 1);
   const int parts = todo ? pre + own : 0;
   auto o_at = [&](int i) {
-    return i < pre ? g.part + (pre0 + static_cast<long long>(i) * step) * D
+    return i < pre ? g.part + (pre0 + i * step) * D
                    : own0 + (i - pre) * G * PS;
   };
   auto stats_at = [&](int i) {
-    return i < pre ? g.stats + (pre0 + static_cast<long long>(i) * step)
+    return i < pre ? g.stats + (pre0 + i * step)
                    : reinterpret_cast<const float2*>(own0 + (i - pre) * G * PS + D);
   };
   float acc[PER];
@@ -1095,11 +1091,11 @@ cudaError_t launch_d(const void* q, const void* k, const void* v, long long page
 
 // Places for the prefixes' partial results: one a row, and a piece's rows for every worker that begins
 // inside a pair.
-long long prefix_entries(int B, int Hq, int G) {
-  return static_cast<long long>(B) * Hq + 2ll * sm_count() * (kRows / G) * G;
+int prefix_entries(int B, int Hq, int G) {
+  return B * Hq + 2 * sm_count() * (kRows / G) * G;
 }
-long long own_entries(int B, int Hkv, int G) {
-  return (static_cast<long long>(B) * Hkv + sm_count()) * G;
+int own_entries(int B, int Hkv, int G) {
+  return (B * Hkv + sm_count()) * G;
 }
 
 }  // namespace
@@ -1109,7 +1105,7 @@ size_t decode_shared_bytes(int B, int Hq, int Hkv, int d) {
   const size_t entry = (d + 4) * sizeof(float);
   return round_up(prefix_entries(B, Hq, G) * (d * sizeof(float) + sizeof(float2)), 256) +
          round_up(own_entries(B, Hkv, G) * entry, 256) +
-         B * (sizeof(Row) + sizeof(long long)) + sizeof(Line);
+         B * (sizeof(Row) + sizeof(int)) + sizeof(Line);
 }
 
 cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
@@ -1133,7 +1129,7 @@ cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
   at += round_up(own_entries(B, Hkv, G) * entry, 256);
   g.rows = reinterpret_cast<Row*>(at);
   g.line = reinterpret_cast<Line*>(g.rows + B);
-  g.tiles_g = reinterpret_cast<long long*>(g.line + 1);
+  g.tiles_g = reinterpret_cast<int*>(g.line + 1);
   g.start = start;
   g.len = shared_len;
   g.groups = groups;

@@ -147,6 +147,7 @@ SHARED = dict(q=X[0], k=X[1], v=X[2], ps=8 * 16 * 64, table=X[3], stride=16, M=1
     ({"d": 96}, UNS), ({"page": 24}, UNS), ({"P": 0}, INV), ({"stride": 3}, INV),
     ({"ps": 8 * 16 * 64 - 8}, INV), ({"scale": 0.0}, INV), ({"scale": float("nan")}, INV),
     ({"B": 8192, "Hq": 8}, UNS),
+    ({"B": 4096, "M": 1 << 17, "stride": 1 << 17, "Hq": 8, "Hkv": 8}, UNS),
     ({"o": X[0]}, INV), ({"o": X[1] + 64}, INV), ({"lse": X[4]}, INV), ({"lse": X[5] + 16}, INV),
     ({"ws": X[3] + 112}, INV), ({"ws": X[8] - 16}, INV), ({"lse": X[9] + 4}, INV), ({"o": X[8]}, INV),
 ])
