@@ -729,7 +729,8 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
               uint8_t* vt = sV + (n % C::NV) * C::TILE + r * 128;
 #pragma unroll
               for (int ch = 0; ch < 4 * C::NSUB; ++ch) {
-                const int at = (i >> 7) * 4 * C::NSUB + ch;      // 16-byte piece of the row
+                // 16-byte pieces of the row, every lane from another one on (banks)
+                const int at = (i >> 7) * 4 * C::NSUB + ((ch + lane) & (4 * C::NSUB - 1));
                 *reinterpret_cast<uint4*>(vt + (at >> 3) * kSub + (at & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
               }

@@ -334,12 +334,15 @@ __device__ __forceinline__ void segments(const CUtensorMap& mk, const CUtensorMa
           *reinterpret_cast<__nv_bfloat16*>(pt + nk_offset(h, r)) = __float2bfloat16_rn(p);
         }
         if (!vis) {  // a hidden row: zero its V so that 0 x (anything) stays 0
-          uint8_t* vt = sKV + st * kStage + C::NSUB * kSub;
+          // every lane from another 16 bytes on: all at the same would be the same banks (sequences of
+          // up to 256 tokens, B = 256: 63 us, so 50)
+          uint8_t* vt = sKV + st * kStage + C::NSUB * kSub + r * 128;
 #pragma unroll
           for (int s = 0; s < C::NSUB; ++s)
 #pragma unroll
             for (int ch = 0; ch < 8; ++ch)
-              *reinterpret_cast<uint4*>(vt + s * kSub + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(vt + s * kSub + ((ch + lane) & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
         }
         // Rescale the group's O^T (lane = d) when a maximum moved after its first tile; the
         // product of its previous tile must have completed.
