@@ -13,8 +13,8 @@
 // N = 16 columns and the CUDA cores only see the 128 x G scores of a tile:
 //   S^T = K Q^T    A = K tile [128 keys][d] (K-major),  B = the group's query rows [16][d]
 //   O^T += V^T P^T A = V tile read MN-major,            B = P^T [16][128 keys] (bf16)
-// A tile is 128 keys = 128 / page boxes of page rows (one box when pages are larger); the lanes
-// of the producer warp each take a page: its table entry and its boxes.  A page that lies
+// A tile is 128 keys, in boxes of a page's rows or 32 of them; the lanes of the producer warp each
+// take a box: its table entry and its loads.  A page that lies
 // outside the pool is not loaded, and its rows, like those past the length, are hidden: their
 // scores are replaced, never computed with, and their V rows are zeroed in shared memory.
 //
@@ -244,7 +244,7 @@ template <int D>
 cudaError_t launch_d(const void* q, const void* k, const void* v, long long page_stride,
                      const PagedArgs& a, int workers, cudaStream_t s) {
   CUtensorMap mk, mv, mq;
-  const int page = 1 << a.page_shift, rows = page < kKeys ? page : kKeys;
+  const int page = 1 << a.page_shift, rows = page < kBox ? page : kBox;
   if (!make_page_map(&mk, k, a.num_pages, a.Hkv, page, D, page_stride, rows) ||
       !make_page_map(&mv, v, a.num_pages, a.Hkv, page, D, page_stride, rows) ||
       !make_head_map_rows(&mq, q, 1, a.B * a.Hq, D, kN))

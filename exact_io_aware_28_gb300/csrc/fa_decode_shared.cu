@@ -165,7 +165,7 @@ struct Group {
   __device__ __forceinline__ Group(const Plan& g, int p) {
     s0 = min(max(g.start[p], 0), g.a.B);
     s1 = max(s0, min(max(g.start[p + 1], 0), g.a.B));
-    const int box = min(kKeys, 1 << g.a.page_shift);
+    const int box = min(kBox, 1 << g.a.page_shift);
     // one sequence alone shares with nobody
     len = s1 - s0 > 1 ? sched::clamp_len(g.len, p, cap_of(g.a)) : 0;
     keys = len & ~(box - 1);
@@ -474,7 +474,7 @@ __device__ __forceinline__ void prefix_segments(const CUtensorMap& mk, const CUt
     uint64_t* full = keys ? bars->k_full : bars->v_full;
     uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
     const int shift = a.page_shift;
-    const int rows = min(kKeys, 1 << shift), boxes = kKeys / rows;
+    const int rows = min(kBox, 1 << shift), boxes = kKeys / rows;
     const uint32_t bits = (1u << (rows / 16)) - 1u;
     const int stages = keys ? C::NK : C::NV;
     bool ok = true;
@@ -1076,7 +1076,7 @@ cudaError_t launch_d(const void* q, const void* k, const void* v, long long page
                      const SharedArgs& g, int workers, cudaStream_t s) {
   CUtensorMap mk, mv, mq, mr;
   const PagedArgs& a = g.a;
-  const int page = 1 << a.page_shift, rows = page < kKeys ? page : kKeys, G = a.Hq / a.Hkv;
+  const int page = 1 << a.page_shift, rows = page < kBox ? page : kBox, G = a.Hq / a.Hkv;
   // The rows of a prefix tile: G heads of `seqs` sequences, from [B, Hkv, G, d].
   if (!make_page_map(&mk, k, a.num_pages, a.Hkv, page, D, page_stride, rows) ||
       !make_page_map(&mv, v, a.num_pages, a.Hkv, page, D, page_stride, rows) ||
