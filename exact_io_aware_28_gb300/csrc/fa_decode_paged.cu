@@ -14,9 +14,9 @@
 //   S^T = K Q^T    A = K tile [128 keys][d] (K-major),  B = the group's query rows [16][d]
 //   O^T += V^T P^T A = V tile read MN-major,            B = P^T [16][128 keys] (bf16)
 // A tile is 128 keys, in boxes of a page's rows or 32 of them; the lanes of the producer warp each
-// take a box: its table entry and its loads.  A page that lies
-// outside the pool is not loaded, and its rows, like those past the length, are hidden: their
-// scores are replaced, never computed with, and their V rows are zeroed in shared memory.
+// take a box: its table entry and its loads.  A page that lies outside the pool is not loaded, and
+// its rows, like those past the length, are hidden: their scores are replaced, never computed with,
+// and their V rows are zeroed in shared memory.
 //
 // A tile's way (scores, maximum, P, P V) is a chain of about 2.5k cycles, at d = 64 twice what HBM
 // takes for its 32 KB, and an issuing thread spends some 1.8k cycles on a tile's twelve MMAs,

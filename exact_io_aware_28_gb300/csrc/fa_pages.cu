@@ -17,8 +17,11 @@
 //
 // Free and compact need the whole count before the first rank and the whole renumbering before the
 // first entry: one cluster does all of it, its barrier (some 0.3 us) in place of further launches.
-// Latency bounds all three.  Every kernel launches as a dependent kernel (it waits for the previous
-// kernel in the stream before touching global memory).
+// Latency bounds all three.  Measured: a fork of 3 requests 4 us, of 240 of up to 8192 tokens with the
+// copy of their last pages 31; freeing 16 of 64 requests of 4096 tokens in pages of 64 10 us, the
+// compaction after it 14, the copies of the pages that it moves (1 GB read and written in all) at 6.5
+// TB/s, 0.96 of a plain copy's rate.  Every kernel launches as a dependent kernel (it waits for the
+// previous kernel in the stream before touching global memory).
 #include <limits.h>
 
 #include "fa_internal.cuh"

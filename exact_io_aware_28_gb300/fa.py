@@ -1060,8 +1060,8 @@ def _rope(x, y, pos, table, interleaved, inverse, stream):
             raise ValueError("rows of y must be dense")
         handle = _same_gpu(stream, x, y, pos, turns, axis)
     _call("fa_rope", x.data_ptr(), y.data_ptr(), *xs[:3], *ys[:3], pos.data_ptr(), ps[0], ps[1],
-          pos.shape[0], turns.data_ptr(), axis.data_ptr(), B, H, N, d, rot, int(interleaved), int(inverse),
-          code, handle)
+          pos.shape[0], turns.data_ptr(), axis.data_ptr(), B, H, N, d, rot, int(interleaved),
+          int(inverse), code, handle)
     return y
 
 

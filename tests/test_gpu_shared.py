@@ -162,6 +162,14 @@ def test_shared_long_prefix_and_large_batch():
                  seed=13))
 
 
+@pytest.mark.parametrize("B, G", [(60, 16), (180, 16)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_many_rows_to_join(B, G, d):
+    # more rows than the combine has warps for four each, or for two
+    rng = np.random.default_rng(B)
+    _check(_case([(160, (160 + rng.integers(0, 40, B)).tolist())], 2 * G, 2, d, 32, seed=B + d))
+
+
 def test_shared_strided_pages_and_tables():
     x = _case([(96, [96, 200, 130])], 4, 2, 64, 32, seed=14)
     both = torch.full((x[1].shape[0], 2) + x[1].shape[1:], float("nan"), device="cuda").bfloat16()
