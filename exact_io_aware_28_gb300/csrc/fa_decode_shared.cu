@@ -11,7 +11,7 @@
 // What bounds it: the bytes of the prefixes, once, and of the continuations; with many sequences a
 // group also the products over the prefix, 4 S d operations a row, on the tensor cores.  Measured
 // (32 / 8 heads, d = 128): 64 sequences, 8192 shared tokens and 512 of their own, pages of 64, 43 us
-// for 25 us of bytes (read for every sequence, as fa_decode_paged does, 328 us); 256 sequences, 32768
+// for 25 us of bytes (fa_decode_paged, with the prefix from L2 for all but the first, 173); 256 sequences, 32768
 // shared, pages of 128, 118 us for 72 us of operations.  A prefix tile with all 256 rows is a chain
 // of 1.8 to 2 us, as in the forward kernel, 1.0 to 1.2 us with rows for one tile at d = 64; 10 us do
 // not grow with the lengths: lengths, tables and the first tiles 5, the join 5.
@@ -34,6 +34,7 @@
 // A sequence shorter than its group's shared tokens takes no part in them: it reads its own keys
 // from the first on, and the products it is in are never joined.  Pages outside the pool are holes,
 // as in fa_decode_paged.cu: not loaded, their scores replaced, their V rows zeroed.
+// With few tiles for each SM the sequences are decoded apart, by fa_decode_paged.cu (decode_apart).
 // Every wait is bounded; on expiry the CTA records FA_ERR_TIMEOUT and leaves.
 #include <atomic>
 
@@ -1104,14 +1105,29 @@ int own_entries(int B, int Hkv, int G) {
   return (B * Hkv + sm_count()) * G;
 }
 
+// Is there so little to read that sharing it costs more than it saves?  Apart the sequences have
+// `tiles` tiles (by the width of the table; the lengths are on the device), some 1 us an SM each; the
+// two kinds of CTAs and the join add 3 to 5 us, and what they save grows with the sequences a group.
+// Measured (d = 64 and 128, 1 to 16 heads a group, one key/value head to eight; tiles an SM at which
+// both take as long): groups of 2 sequences 25 to 30, of 4 14, of 8 10, of 16 and more 5 to 7.  Four
+// sequences of 700 tokens: 11.4 us shared, 8.9 apart; 32 of 1084 tokens, d = 128, 8 key/value heads,
+// one group (15 tiles an SM): 16.0 and 23.5.
+bool decode_apart(long long tiles, int B, int groups) {
+  return tiles * B <= (4ll * B + 40ll * groups) * sm_count();
+}
+
 }  // namespace
 
 size_t decode_shared_bytes(int B, int Hq, int Hkv, int d) {
   const int G = Hq / Hkv;
   const size_t entry = (d + 4) * sizeof(float);
-  return round_up(prefix_entries(B, Hq, G) * (d * sizeof(float) + sizeof(float2)), 256) +
-         round_up(own_entries(B, Hkv, G) * entry, 256) +
-         B * (sizeof(Row) + sizeof(int)) + sizeof(Line);
+  const size_t shared =
+      round_up(prefix_entries(B, Hq, G) * (d * sizeof(float) + sizeof(float2)), 256) +
+      round_up(own_entries(B, Hkv, G) * entry, 256) + B * (sizeof(Row) + sizeof(int)) +
+      sizeof(Line);
+  const size_t apart = decode_paged_part_bytes(G, d) +
+                       (static_cast<size_t>(B) + 1) * sizeof(long long);
+  return shared > apart ? shared : apart;
 }
 
 cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
@@ -1121,6 +1137,12 @@ cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
                                  const int32_t* shared_len, int groups, void* o, float* lse, int B,
                                  int Hq, int Hkv, int d, float scale, void* workspace, int* err,
                                  unsigned long long wait_ns, cudaStream_t s) {
+  const long long most = (static_cast<long long>(max_pages) << page_shift) + kKeys - 1;
+  const long long tiles = static_cast<long long>(B) * Hkv * (most / kKeys);
+  if (decode_apart(tiles, B, groups))
+    return launch_decode_paged(q, k, v, page_stride, table, table_stride, max_pages, page_shift,
+                               num_pages, cache_len, o, lse, B, Hq, Hkv, d, scale, workspace, err,
+                               wait_ns, s);
   const int G = Hq / Hkv;
   const size_t entry = (d + 4) * sizeof(float);
   char* at = static_cast<char*>(workspace);
@@ -1140,10 +1162,7 @@ cudaError_t launch_decode_shared(const void* q, const void* k, const void* v,
   g.len = shared_len;
   g.groups = groups;
   g.seqs = kRows / G;
-  // No more CTAs than there can be tiles: a sequence's own, and with two of them a prefix's.
-  const long long most = (static_cast<long long>(max_pages) << page_shift) + kKeys - 1;
-  const long long tiles = 2ll * B * Hkv * (most / kKeys);
-  const int workers = tiles < sm_count() ? static_cast<int>(tiles) : sm_count();
+  const int workers = sm_count();                // there may be more tiles
   return d == 64 ? launch_d<64>(q, k, v, page_stride, g, workers, s)
                  : launch_d<128>(q, k, v, page_stride, g, workers, s);
 }

@@ -413,10 +413,11 @@ fa_status fa_decode_paged(const void* q, const void* k, const void* v, long long
  *                 same pages up to there; they are read from the first one that is long enough.
  * A sequence shorter than its group's shared tokens (an empty one that pads the batch, say) is
  * computed from its own length and table.  groups is 1 .. B (FA_ERR_INVALID_ARG otherwise), B * Hkv *
- * max_pages * page_size below 2^36 (FA_ERR_UNSUPPORTED otherwise); starts
- * that are not ascending give no defined result, and touch no other memory.  The result is that of
- * fa_decode_paged but for the order of sums.  Two kernels run on `stream`; no atomics: the same call
- * gives the same bits.
+ * max_pages * page_size below 2^36 (FA_ERR_UNSUPPORTED otherwise); starts that are not ascending give
+ * no defined result, and touch no other memory.  The result is that of fa_decode_paged but for the
+ * order of sums; a batch whose table has room for few tiles of 128 tokens (up to 4 + 40 groups / B an
+ * SM) is computed by that call's kernels, which are faster then.  Two kernels run on `stream`; no
+ * atomics: the same call gives the same bits.
  */
 size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d);
 fa_status fa_decode_shared(const void* q, const void* k, const void* v, long long page_stride,

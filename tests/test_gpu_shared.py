@@ -16,9 +16,15 @@ pytestmark = pytest.mark.gpu
 I32, BF = torch.int32, torch.bfloat16
 
 
+def _columns(B, Hkv, page):
+    """Columns of a table with so much room that the groups' tokens are read together at any lengths."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return (44 * sms // (B * Hkv) + 2) * 128 // page
+
+
 def _case(groups, Hq, Hkv, d, page, seed, M=None, nan=True, spare=3):
     """groups: [(shared tokens, [lengths])].  Sequences of a group that reach its shared tokens name the
-    same pages for them; rows outside the lengths hold NaN and infinity."""
+    same pages for them; rows outside the lengths hold NaN and infinity.  The table is a wide one."""
     g = _gen(seed)
     lens = [n for _, l in groups for n in l]
     B = len(lens)
@@ -50,20 +56,31 @@ def _case(groups, Hq, Hkv, d, page, seed, M=None, nan=True, spare=3):
         k.masked_fill_(~inside[:, None, :, None], float("nan"))
         v.masked_fill_(~inside[:, None, :, None], float("inf"))
     q = torch.randn(B, Hq, d, generator=g).bfloat16()
+    table = torch.cat([table, table.new_full((B, _columns(B, Hkv, page)), -1)], 1)
     return [q.cuda(), k.cuda(), v.cuda(), table.cuda(), _i32(lens), _i32(start),
             _i32([s for s, _ in groups])]
 
 
+def _narrow(x):
+    """The same batch with the table's columns behind the last page left out."""
+    used = (x[3] != -1).any(0).nonzero()
+    return x[:3] + [x[3][:, :int(used.max()) + 1 if used.numel() else 1].contiguous()] + x[4:]
+
+
 def _check(x, scale=None, run=None):
-    o, lse = fa.decode_shared(*x, scale) if run is None else run
+    """Without `run` also of the narrow table, with which a small batch is decoded apart."""
+    runs = [run]
+    if run is None:
+        runs = [fa.decode_shared(*y, scale) for y in (x, _narrow(x))]
     _ok()
     q, k, v, table, lens = x[:5]
     ro, rlse, spread = paged.decode(_np(q), _np(k), _np(v), table.cpu().numpy(), lens.tolist(),
                                     1 / q.shape[-1] ** 0.5 if scale is None else scale)
-    assert torch.isfinite(o.float()).all()
-    check_o(_np(o), ro, spread)
-    check_lse(_np(lse), rlse)
-    return o, lse
+    for o, lse in runs:
+        assert torch.isfinite(o.float()).all()
+        check_o(_np(o), ro, spread)
+        check_lse(_np(lse), rlse)
+    return runs[0]
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -119,7 +136,7 @@ def test_shared_sequences_in_no_group():
 def test_shared_lengths_are_clamped():
     x = _case([(64, [64, 64]), (64, [64, 80])], 4, 2, 64, 32, seed=7, M=3)
     x[4][0], x[4][1] = 1000, -7
-    x[3][0] = torch.arange(3)
+    x[3][0, :3] = torch.arange(3)
     x[1][:3], x[2][:3] = 1.0, 2.0
     x[6] = _i32([-3, 100000])
     _check(x)
@@ -243,13 +260,24 @@ def test_shared_past_32_bit_offsets():
     for p in at:
         k[p], v[p] = (torch.randn(Hkv, page, d, generator=g).bfloat16().cuda() for _ in range(2))
     q = torch.randn(2, 2 * Hkv, d, generator=g).bfloat16().cuda()
-    table, lens = _i32([[P - 1, 5, P - 2], [P - 1, 5, P - 3]]), _i32([300, 290])
+    table, lens = torch.full((2, _columns(2, Hkv, page)), -1, dtype=I32, device="cuda"), _i32([300, 290])
+    table[:, :3] = _i32([[P - 1, 5, P - 2], [P - 1, 5, P - 3]])
     o, lse = fa.decode_shared(q, k, v, table, lens, _i32([0, 2]), _i32([256]))
     _ok()
     small = np.array([[0, 1, 2], [0, 1, 3]])
     ro, rlse, spread = paged.decode(_np(q), _np(k[at]), _np(v[at]), small, [300, 290], d ** -0.5)
     check_o(_np(o), ro, spread)
     check_lse(_np(lse), rlse)
+
+
+def test_shared_small_batches_are_decoded_apart():
+    # a table with room for few tiles: the kernels of the paged decode, so its bits
+    x = _narrow(_case([(500, [500, 640, 700, 64]), (0, [0])], 8, 2, 64, 16, seed=23))
+    ws = fa.alloc_decode_shared_workspace(5, 8, 2, 64)
+    ws.fill_(0xff)
+    (o, lse), (po, plse) = fa.decode_shared(*x, workspace=ws), fa.decode_paged(*x[:5])
+    _check(x, run=(o, lse))
+    assert torch.equal(o, po) and torch.equal(lse, plse)
 
 
 def test_shared_equals_the_paged_decode_of_the_same_tables():
@@ -294,7 +322,8 @@ def test_samples_of_prompts_forked_grown_freed_and_compacted():
     """Two prompts are written with their positions, each is forked, the samples grow token by token in
     pages of their own, some end, the pool is compacted, the rest grows on; every step's outputs are
     those of the definition over the whole history."""
-    B, M, page, P, Hq, Hkv, d = 7, 12, 16, 90, 4, 2, 64
+    B, page, P, Hq, Hkv, d = 7, 16, 90, 4, 2, 64
+    M = _columns(B, Hkv, page)
     g = _gen(30)
     table, lens = torch.full((B, M), -1, dtype=I32, device="cuda"), torch.zeros(B, dtype=I32, device="cuda")
     kc, vc = (torch.full((P, Hkv, page, d), float("nan"), dtype=BF, device="cuda") for _ in range(2))
