@@ -430,9 +430,9 @@ cudaError_t launch_paged_fork(int32_t* cache_len, int32_t* table, long long tabl
   ForkArgs a{cache_len, table, table_stride, max_pages, free_pages, n_free, src, dst, n, copy_src,
              copy_dst, copy_rows, pages_taken, B, page_shift, num_pages};
   const size_t smem = sizeof(int) * (static_cast<size_t>(B) + n);
-  if (smem > 48 * 1024) {
+  if (smem > 48 * 1024) {       // to the most that a call takes: calls at once set the same
     cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         2 * kMaxRows * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
   }
   const int blocks = n < 1 ? 1 : n < 2 * sm_count() ? n : 2 * sm_count();

@@ -648,7 +648,7 @@ def _on_stream(stream, fn, *args, **kw):
         stream = torch.cuda.ExternalStream(int(stream))
     if stream != torch.cuda.current_stream():
         for x in (*args, *kw.values()):
-            for t in x if isinstance(x, tuple) else (x,):
+            for t in x if isinstance(x, (tuple, list)) else (x,):
                 if isinstance(t, torch.Tensor) and t.is_cuda:
                     t.record_stream(stream)
     with torch.cuda.stream(stream):
