@@ -158,8 +158,8 @@ __device__ __forceinline__ int owner(int x, int total, int workers) {
 // What a tile costs, in some 0.3 us: a prefix's with rows for both row tiles, for one; a
 // continuation's; what a pair adds to its tiles (queries, results): a prefix's, a continuation's; and
 // what a prefix's CTA takes more than another, however few its tiles are.
-constexpr int kCostBoth = 6, kCostOne = 4, kCostOwn = 4, kCostPrefixPair = 4, kCostOwnPair = 3;
-constexpr int kCostPrefixMore = 24;
+constexpr int kCostBoth = 7, kCostOne = 4, kCostOwn = 4, kCostPrefixPair = 4, kCostOwnPair = 3;
+constexpr int kCostPrefixMore = 20;
 
 struct Group {
   int s0, s1;                  // its sequences
