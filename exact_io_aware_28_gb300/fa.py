@@ -614,18 +614,14 @@ def _rows(name, t, shape, dtype=torch.bfloat16):
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    dense = 1
-    for n in shape[1:]:
-        dense *= n
-    if not t.is_contiguous():
-        inner = 1
-        for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-            if n != 1 and st != inner:
-                raise ValueError(f"{name} must be dense behind its first dimension")
-            inner *= n
-        if shape[0] > 1:
-            return t.stride(0)
-    return dense   # a single entry's stride says nothing
+    st, dense, whole = t.stride(), 1, True
+    for i in range(len(shape) - 1, 0, -1):
+        if st[i] != dense and shape[i] != 1:
+            whole = False
+        dense *= shape[i]
+    if not whole and not t.is_contiguous():      # (an empty tensor is, whatever its strides)
+        raise ValueError(f"{name} must be dense behind its first dimension")
+    return st[0] if whole and shape[0] > 1 else dense   # a single entry's stride says nothing
 
 
 def _table(t, B):
