@@ -416,8 +416,11 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     // ------------------------------------------------------------ epilogue
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (ok && n_t[t] > 0) {
-        ok = mbar_wait_warp(&bars->o_done[t], 0, abort_flag, p.err, p.wait_ns);
+      // O goes into the tile's Q buffer.  A tile with keys waits for its last product; one without
+      // waits for the load of Q, which would land on the rows staged there.
+      if (ok) {
+        ok = mbar_wait_warp(n_t[t] > 0 ? &bars->o_done[t] : &bars->q_full, 0, abort_flag, p.err,
+                            p.wait_ns);
         tc_fence_after();
       }
       if (!ok) break;
@@ -432,9 +435,9 @@ fwd_sm103_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         invB *= p.drop_scale;
       }
       const int rowA = u.q0 + t * kBlk + rA, rowB = rowA + 8;
-      // O / l as bf16 into this tile's Q buffer (every S MMA that read it has completed: they
-      // precede the last P V product of this tile), in the 128-byte-swizzled layout of the
-      // TMA box; one thread then stores the tile with the TMA (rows past N are clipped).
+      // O / l as bf16 into this tile's Q buffer (Q has landed, and every S MMA that read it has
+      // completed: they precede the last P V product of this tile), in the 128-byte-swizzled layout
+      // of the TMA box; one thread then stores the tile with the TMA (rows past N are clipped).
       uint8_t* stage = sQ + t * C::TILE;
 #pragma unroll
       for (int half = 0; half < D / 64; ++half) {
