@@ -31,6 +31,7 @@ namespace fa {
 namespace {
 
 constexpr int kForkThreads = 256;
+constexpr int kForkWarps = kForkThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kPageThreads = 512;
 constexpr int kWarps = kPageThreads / 32;
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs a) {
   extern __shared__ int sh[];
   int* first = sh;              // [B] the first pair that names the row as its destination
   int* list = sh + a.B;         // [n] the pair's place in the free list, -1: none, -2: skipped
-  __shared__ int warp_sum[kForkThreads / 32];
+  int* warp_sum = list + a.n;   // [kForkWarps]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = a.max_pages << a.shift, round = (1 << a.shift) - 1;
   for (int b = tid; b < a.B; b += kForkThreads) first[b] = INT_MAX;
@@ -429,10 +430,12 @@ cudaError_t launch_paged_fork(int32_t* cache_len, int32_t* table, long long tabl
                               int page_shift, int num_pages, cudaStream_t s) {
   ForkArgs a{cache_len, table, table_stride, max_pages, free_pages, n_free, src, dst, n, copy_src,
              copy_dst, copy_rows, pages_taken, B, page_shift, num_pages};
-  const size_t smem = sizeof(int) * (static_cast<size_t>(B) + n);
+  // All of the kernel's shared memory: what is declared in it would count beside this.
+  const size_t smem = sizeof(int) * (static_cast<size_t>(B) + n + kForkWarps);
   if (smem > 48 * 1024) {       // to the most that a call takes: calls at once set the same
     cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         2 * kMaxRows * static_cast<int>(sizeof(int)));
+                                         (2 * kMaxRows + kForkWarps) *
+                                             static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
   }
   const int blocks = n < 1 ? 1 : n < 2 * sm_count() ? n : 2 * sm_count();

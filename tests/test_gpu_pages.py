@@ -1,5 +1,9 @@
 """Forking, freeing, compacting and copying the pages of a paged cache, on the GPU, against the
 oracle: all of it whole numbers and moved rows, so equal or wrong."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -81,6 +85,29 @@ def test_fork_of_the_largest_batch():
     rows = rng.permutation(B)
     _run_fork(lens, table, 2 * B + rng.permutation(B), np.concatenate([rows[:4096]] * 2),
               np.concatenate([rows[4096:], np.full(4096, -1)]), 16, 3 * B)
+
+
+def test_fork_of_any_size_in_a_new_process():
+    # around 48 KB of shared memory, in ascending order: a larger call before would have raised what
+    # the device grants to all that follow
+    script = """
+import numpy as np
+import test_gpu_pages as t
+B = 8192
+rng = np.random.default_rng(0)
+for n in (4080, 4081, 4088, 4089, 4096, 4097, 8192):
+    rows = rng.permutation(B)
+    src, dst = np.full(n, -1), np.full(n, -1)
+    m = min(n, B // 2)
+    src[:m], dst[:m] = rows[:m], rows[m:2 * m]
+    t._run_fork(rng.integers(0, 33, B), np.arange(2 * B).reshape(B, 2), 2 * B + rng.permutation(B),
+                src, dst, 16, 3 * B)
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    path = os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")])
+    done = subprocess.run([sys.executable, "-c", script], env={**os.environ, "PYTHONPATH": path},
+                          capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_fork_leaves_what_lies_beside_a_view():
