@@ -21,6 +21,12 @@ namespace fa {
 namespace {
 
 constexpr int kTableThreads = 256;
+constexpr int kTableWarps = kTableThreads / 32;
+constexpr int kMaxRequests = 8192;         // of a call
+// All of the tables' shared memory: what the kernel declared would count beside it.
+constexpr int table_smem(int B) {
+  return kTableWarps * static_cast<int>(sizeof(int2)) + 2 * (B + 1) * static_cast<int>(sizeof(int));
+}
 
 // Index of the last of sums[0..n) that is <= x (sums[0] = 0 <= x; equal entries are empty
 // ranges, of which the last one holds x).
@@ -39,10 +45,9 @@ tables_kernel(const int32_t* __restrict__ cache_len, const int32_t* __restrict__
               long long table_stride, int max_pages, int32_t* __restrict__ total_len,
               int32_t* __restrict__ token_start, int32_t* __restrict__ slots, int n_slots,
               int32_t* __restrict__ pages_taken, int B, int shift, int num_pages) {
-  extern __shared__ int sums[];            // [B + 1] token starts, then [B + 1] list offsets
-  __shared__ int2 warp_sum[kTableThreads / 32];
-  int* start = sums;
-  int* off = sums + B + 1;
+  extern __shared__ int2 warp_sum[];       // [kTableWarps]
+  int* start = reinterpret_cast<int*>(warp_sum + kTableWarps);   // [B + 1] token starts
+  int* off = start + B + 1;                // [B + 1] list offsets
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = max_pages << shift, round = (1 << shift) - 1;
   ptx::griddep_wait();
@@ -197,10 +202,10 @@ cudaError_t launch_paged_tables(const int32_t* cache_len, const int32_t* new_len
                                 int32_t* token_start, int32_t* slots, int n_slots,
                                 int32_t* pages_taken, int B, int page_shift, int num_pages,
                                 cudaStream_t s) {
-  const size_t smem = 2 * sizeof(int) * (static_cast<size_t>(B) + 1);
-  if (smem > 48 * 1024) {
+  const int smem = table_smem(B);
+  if (smem > 48 * 1024) {       // to the most that a call takes: calls at once set the same
     cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         table_smem(kMaxRequests));
     if (e != cudaSuccess) return e;
   }
   long long work = n_slots > B ? n_slots : B;

@@ -87,10 +87,18 @@ def test_fork_of_the_largest_batch():
               np.concatenate([rows[4096:], np.full(4096, -1)]), 16, 3 * B)
 
 
+def _in_a_new_process(script):
+    here = os.path.dirname(os.path.abspath(__file__))
+    path = os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")])
+    done = subprocess.run([sys.executable, "-c", script], env={**os.environ, "PYTHONPATH": path},
+                          capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
 def test_fork_of_any_size_in_a_new_process():
     # around 48 KB of shared memory, in ascending order: a larger call before would have raised what
     # the device grants to all that follow
-    script = """
+    _in_a_new_process("""
 import numpy as np
 import test_gpu_pages as t
 B = 8192
@@ -102,12 +110,20 @@ for n in (4080, 4081, 4088, 4089, 4096, 4097, 8192):
     src[:m], dst[:m] = rows[:m], rows[m:2 * m]
     t._run_fork(rng.integers(0, 33, B), np.arange(2 * B).reshape(B, 2), 2 * B + rng.permutation(B),
                 src, dst, 16, 3 * B)
-"""
-    here = os.path.dirname(os.path.abspath(__file__))
-    path = os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")])
-    done = subprocess.run([sys.executable, "-c", script], env={**os.environ, "PYTHONPATH": path},
-                          capture_output=True, text=True, timeout=300)
-    assert done.returncode == 0, done.stderr[-2000:]
+""")
+
+
+def test_tables_of_any_size_in_a_new_process():
+    # as above, 8 B + 72 bytes
+    _in_a_new_process("""
+import numpy as np
+import test_gpu_paged as t
+rng = np.random.default_rng(0)
+for B in (6134, 6135, 6136, 6140, 6143, 6144, 8192):
+    old, new = rng.integers(0, 20, B), rng.integers(0, 3, B)
+    t._run_tables(old, new, 2 * B + rng.permutation(B), np.arange(2 * B).reshape(B, 2), 16, 4 * B,
+                  int(new.sum()) + 3)
+""")
 
 
 def test_fork_leaves_what_lies_beside_a_view():
