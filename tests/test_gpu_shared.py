@@ -142,6 +142,42 @@ def test_shared_lengths_are_clamped():
     _check(x)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_lengths_past_a_wide_row_are_clamped(d):
+    # The row is wide enough for the kernels that share, and full; lengths and shared lengths lie past
+    # it.  Behind it the buffer goes on with pages whose values would show.
+    B, Hq, Hkv, page = 16, 8, 4, 16
+    M = _columns(B, Hkv, page)
+    cap, far, P = M * page, 2 ** 31 - 1, 4 * M + 12
+    lens = [cap + 1000, far, cap, cap - 5, -7, 80, far, 40, 0, cap + 1] + [9, 0, 33, cap + 16, 5, -1]
+    start, shared = [0, 4, 6, 9, 10], [cap + 300, -3, far, 5]
+    g = _gen(24 + d)
+    ids = torch.randperm(P - 2, generator=g).int()
+    wide = torch.full((B, M + 6), -1, dtype=I32)
+    for b, at in ((0, 0), (6, M), (9, 2 * M), (13, 3 * M)):
+        wide[b, :M] = ids[at:at + M]
+    wide[1:4] = wide[0]
+    for i, b in enumerate((5, 7, 10, 12, 14)):
+        wide[b, :5] = ids[4 * M + 2 * i % 5:][:5]
+    wide[:, M:] = torch.tensor([P - 2, P - 1, P - 2, P - 1, P - 2, P - 1])
+    q = torch.randn(B, Hq, d, generator=g).bfloat16()
+    k, v = (torch.randn(P, Hkv, page, d, generator=g).bfloat16() for _ in range(2))
+    v[P - 2:] = 1000.0
+    table = wide.cuda()[:, :M]
+    runs = fa.decode_shared(q.cuda(), k.cuda(), v.cuda(), table, _i32(lens), _i32(start), _i32(shared))
+    _ok()
+    args = [_np(t) for t in (q, k, v)]
+    ro, rlse, spread = paged.decode(*args, wide[:, :M].numpy(), lens, d ** -0.5)
+    check_o(_np(runs[0]), ro, spread)
+    check_lse(_np(runs[1]), rlse)
+    # one token more of the full rows is far outside the bounds
+    long = [i for i, n in enumerate(lens) if n > cap]
+    po, _, _ = paged.decode(args[0][long], *args[1:], wide[long].numpy(), [cap + 1] * len(long), d ** -0.5)
+    for i, b in enumerate(long):
+        with pytest.raises(AssertionError):
+            check_o(po[i], ro[b], spread[b])
+
+
 @pytest.mark.parametrize("page", [16, 128])
 def test_shared_holes_hide_their_keys(page):
     x = _case([(640, [640, 700, 900, 641]), (256, [256, 300])], 4, 2, 64, page, seed=8)
