@@ -23,7 +23,8 @@
 // the one beside loads of the other, and end at about the same time.  Every segment of a pair in a
 // worker's range leaves a partial result in a place of its own: (pair) + (worker) grows along the
 // line, so no two meet.  A combine kernel joins them.  The cut depends on lengths, groups and the
-// number of SMs alone: the same call gives the same bits.
+// number of SMs alone: the same call gives the same bits.  Which kernels run depends on the width of
+// the table too (decode_apart): another width may give the same batch other bits.
 //
 // A prefix segment (one CTA, two tiles of up to 128 query rows; a tile holds 128 / G sequences of
 // G heads, in whole sequences):
@@ -163,6 +164,10 @@ __device__ __forceinline__ int owner(int x, int total, int workers) {
 // 40.4, a continuation's pair at 4 39.6, at 2 40.1.)
 constexpr int kCostBoth = 7, kCostOne = 4, kCostOwn = 4, kCostPrefixPair = 4, kCostOwnPair = 3;
 constexpr int kCostPrefixMore = 20;
+// What the prefixes cost with ascending starts, whose tiles are fewer than 2^29 (and pairs no more than
+// tiles), with room for the rounding of the sum; below it the tiles of any starts fit in 32 bits.
+constexpr float kMostCost = 1.1f * (kCostBoth + kCostPrefixPair) * 0x1p29f;
+static_assert(kCostOne <= kCostBoth && kMostCost < kCostOne * 0x1p31f, "tiles in 32 bits");
 
 struct Group {
   int s0, s1;                  // its sequences
@@ -234,7 +239,7 @@ struct Sums {
   float cost[2];
 };
 
-// The CTA's part of the work, as sched::find_start.  write: what the combine kernel reads.
+// The CTA's part of the work, as sched::find_start; block 0 writes what the combine kernel reads.
 __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
                                            const Plan& g) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = g.a.B, cap = cap_of(g.a);
@@ -295,9 +300,8 @@ __device__ __forceinline__ void find_start(SharedStart* out, Sums* scratch,
       cost[j] += scratch[i].cost[j];
     }
   }
-  // Group starts that are not ascending can name more tiles than 32 bits hold: nothing is done then
-  // (with ascending ones the cost is below 6 + 4 times 2^29).
-  if (cost[0] > 7e9f) total[0] = total[1] = 0;
+  // Group starts that are not ascending can name more tiles than 32 bits hold: nothing is done then.
+  if (cost[0] > kMostCost) total[0] = total[1] = 0;
   const int share = prefix_workers(gridDim.x, total[0], total[1], cost[0], cost[1]);
   const int W0 = sched::active(total[0], share);
   const int W1 = sched::active(total[1], static_cast<int>(gridDim.x) - share);
