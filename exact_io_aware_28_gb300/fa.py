@@ -1017,7 +1017,7 @@ def rope_table(rot: int, base: float = 10000.0, sections=None, frequencies=None,
         t = f / (2.0 * math.pi)
         if not math.isfinite(t):
             raise ValueError("frequencies must be finite")
-        u = round((t - math.floor(t)) * 2.0 ** 64) % 2 ** 64       # modulo a full turn
+        u = round(math.fmod(t, 1.0) * 2.0 ** 64) % 2 ** 64   # modulo a full turn, all bits of t kept
         turns.append(u - 2 ** 64 if u >= 2 ** 63 else u)
     axis = [a for a, n in enumerate(sections) for _ in range(n)]
     return (torch.tensor(turns, dtype=torch.int64, device=device),

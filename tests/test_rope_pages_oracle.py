@@ -1,5 +1,6 @@
 """The oracles of rotary positions and of a cache's pages, and the rotation's plan, on the CPU."""
 from decimal import Decimal, getcontext
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -32,6 +33,17 @@ def test_plan_of_sections_and_of_given_frequencies():
     turns, _ = _plan(16, frequencies=[0.0, 2 * np.pi, np.pi, -np.pi / 2, 7 * np.pi, 1e-9, 3.0, 1.0])
     assert turns[0] == 0 and turns[1] == 0 and turns[2] == 2 ** 63 and turns[3] == 3 * 2 ** 62
     assert turns[4] == 2 ** 63
+
+
+def test_plan_keeps_every_bit_of_its_frequencies_of_either_sign():
+    # the turns of the fp64 quotient by 2 pi, off by half a unit at most; the other way round the same
+    f = [0.3, 1.0, 1e-6, 1e-9, 7.1, 6.2, 2.0 ** -58, 1000.25]
+    turns, _ = _plan(16, frequencies=f)
+    back, _ = _plan(16, frequencies=[-x for x in f])
+    for x, t, b in zip(f, turns, back):
+        exact = Fraction(x / (2 * np.pi)) * 2 ** 64
+        assert abs((t - exact + 2 ** 63) % 2 ** 64 - 2 ** 63) <= Fraction(1, 2), x
+        assert (t + b) % 2 ** 64 == 0, x
 
 
 @pytest.mark.parametrize("kw", [dict(sections=[3, 4]), dict(frequencies=[1.0]), dict(sections=[-1, 9]),
