@@ -200,6 +200,47 @@ def test_free_and_compact_of_the_largest_batch():
     _run_compact(lens, table, 16, 3 * B)
 
 
+def test_free_and_compact_captured_and_replayed():
+    # what the tables, the lengths and the ended rows hold is read at every replay
+    B, M, page, P = 40, 30, 16, 1300
+    l, t = torch.zeros(B, dtype=I32, device="cuda"), torch.zeros(B, M, dtype=I32, device="cuda")
+    done, pool = torch.zeros(12, dtype=I32, device="cuda"), torch.zeros(P, 1, page, 64, device="cuda")
+    pool = pool.bfloat16()
+
+    def step():
+        ended = fa.paged_free(l, t, done, page, P)
+        moves = fa.paged_compact(l, t, page, P)
+        fa.paged_copy(pool, None, *moves[1:3])
+        return ended + moves
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        refs, free, n, moved, frm, to, used = step()
+    for seed in range(3):
+        rng, lens, table, _ = _cache(seed, B, M, page, P)
+        rows = rng.integers(-1, B + 1, done.numel())
+        before = torch.randn(pool.shape, generator=_gen(seed)).bfloat16()
+        for x, y in ((l, lens), (t, table), (done, rows)):
+            x.copy_(_i32(y))
+        pool.copy_(before)
+        gr.replay()
+        _ok()
+        rl, rt, rrefs, rfree = pages.free(lens, table, rows, page, P)
+        rt, rmoved, copies, U = pages.compact(rl, rt, page, P)
+        assert np.array_equal(l.cpu().numpy(), rl) and np.array_equal(t.cpu().numpy(), rt)
+        assert np.array_equal(refs.cpu().numpy(), rrefs) and n.item() == len(rfree)
+        assert free.tolist() == rfree + [-1] * (P - len(rfree))
+        assert np.array_equal(moved.cpu().numpy(), rmoved) and used.item() == U
+        m = len(copies)
+        assert list(zip(frm.tolist(), to.tolist()))[:m] == copies and (frm[m:] == -1).all()
+        assert np.array_equal(_np(pool), pages.copy(_np(before), frm.tolist(), to.tolist()))
+
+
 # ------------------------------------------------------------------ copies
 
 @pytest.mark.parametrize("page", [16, 64, 256])
