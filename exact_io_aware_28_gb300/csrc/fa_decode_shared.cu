@@ -9,7 +9,10 @@
 // in fa_decode_paged.cu.  P is rounded once to bf16 as an operand of P V in both.
 //
 // What bounds it: the bytes of the prefixes, once, and of the continuations; with many sequences a
-// group also the products over the prefix, 4 S d operations a row, on the tensor cores.  Measured
+// group also the products over the prefix, 4 S d operations a row, on the tensor cores.  (A group of
+// more than 256 rows a head reads its prefix from DRAM more often where the cut sets the pieces apart
+// in time: 256 sequences behind 16384 tokens with 128 of their own 350 MB for 201; set side by side by
+// other costs of the tiles they read 218, and the call took 94 us for 91.)  Measured
 // (32 / 8 heads, d = 128): 64 sequences, 8192 shared tokens and 512 of their own, pages of 64, 43 us
 // for 25 us of bytes (fa_decode_paged, with the prefix from L2 for all but the first, 173); 256
 // sequences, 32768 shared, pages of 128, 118 us for 72 us of operations.  A prefix tile with all 256

@@ -28,9 +28,9 @@
  * 16-byte aligned.  Calls are asynchronous on `stream` (a cudaStream_t passed as void*;
  * NULL is the legacy default stream): outputs are valid once the stream has synchronised.
  * The kernels of fa_fwd, fa_fwd_dropout, the three backward stages and of the paged-cache and
- * latent entry points (fp32 latent attention excepted) are launched with programmatic stream
- * serialization: one may be scheduled while the previous kernel in the
- * stream is still running, but it reads and writes global memory only after that kernel
+ * latent entry points (fp32 latent attention and the first kernel of fa_decode_shared excepted) are
+ * launched with programmatic stream serialization: one may be scheduled while the previous kernel in
+ * the stream is still running, but it reads and writes global memory only after that kernel
  * has completed, so stream order holds as for ordinary launches (also inside a captured
  * CUDA graph, which keeps the attribute).
  *
@@ -416,8 +416,9 @@ fa_status fa_decode_paged(const void* q, const void* k, const void* v, long long
  * max_pages * page_size below 2^36 (FA_ERR_UNSUPPORTED otherwise); starts that are not ascending give
  * no defined result, and touch no other memory.  The result is that of fa_decode_paged but for the
  * order of sums; a batch whose table has room for few tiles of 128 tokens (up to 4 + 40 groups / B an
- * SM) is computed by that call's kernels, which are faster then.  Two kernels run on `stream`; no
- * atomics: the same call gives the same bits.
+ * SM) is computed by that call's kernels, which are faster then.  The rule goes by the table's width,
+ * not by the lengths: give a small batch a table no wider than it needs.  Two kernels run on `stream`;
+ * no atomics: the same call gives the same bits, under a table of the same width.
  */
 size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int d);
 fa_status fa_decode_shared(const void* q, const void* k, const void* v, long long page_stride,
@@ -497,7 +498,8 @@ fa_status fa_paged_copy(void* k_cache, void* v_cache, long long page_stride,
  *   pos         in : int32, position of token (b, n) on axis a at a * pos_axis + b * pos_batch + n;
  *                 any value, negative ones too.
  *   turns       in : int64 [rot / 2], w_i / (2 pi), turns a position, in units of 2^-64 (modulo one
- *                 turn).  The angle is exact in them, however far the position is.
+ *                 turn).  n w_i is formed without error, modulo a turn, however far the position is;
+ *                 sine and cosine are taken of it rounded to fp32.
  *   axis        in : int32 [rot / 2], clamped to [0, axes).
  *   interleaved : 0: pair i is channels i and i + rot / 2;  nonzero: channels 2 i and 2 i + 1.
  *   inverse     : nonzero: the angles' signs change (the gradient).
